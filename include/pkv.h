@@ -464,6 +464,116 @@ pkv_status paged_decode_step_advance(const pkv_dims *dims, const void *q, const 
                                      size_t ws_bytes, void *out, const int32_t *free_pages,
                                      int num_free, int32_t *free_head, pkv_stream_t stream);
 
+/* ---- new tokens: normalised, rotated, written (bf16 or 8-bit cache) -------- */
+
+/* The new tokens of a step or of ragged chunks, and what is done to them on
+ * the way into the cache.  T rows: one a batch row for the append calls
+ * (T = B), total_q for the extend calls.
+ *   q [T, Hq, D], k and v [T, Hkv, D] bf16; row t starts t * stride elements
+ *   after the pointer (0: packed, H * D), so q, k and v may be slices of one
+ *   projection's output.  Strides are multiples of 8 and at least H * D; the
+ *   heads of a row are packed.
+ *   q == NULL: no query work (q_out, q_norm and q_stride are then ignored).
+ *   q_out [T, Hq, D] packed receives the processed queries; it may be q
+ *   itself where q is packed, and must not overlap it otherwise.
+ *   q_norm, k_norm: nullable [D] bf16 weights of a per-head RMS norm, applied
+ *   before the rotation: x * rsqrt(mean(x^2) + norm_eps) * weight.
+ *   rope_cos_sin, rope_max_pos: the table of pkv_rope_table, or NULL for no
+ *   rotation.
+ * Every step is done in fp32 and the result rounded once. */
+typedef struct {
+    const void *q;
+    const void *k;
+    const void *v;
+    long long q_stride, k_stride, v_stride;
+    void *q_out;
+    const void *q_norm;
+    const void *k_norm;
+    float norm_eps;          /* >= 0 and finite; used with a weight          */
+    const float *rope_cos_sin;
+    int rope_max_pos;
+} pkv_tokens;
+
+/* paged_kv_append with per-head norms of q and k in the same pass: row b's
+ * token (b of the tokens' rows) goes to position p = seq_lens[b] - 1.  K is
+ * normalised, rotated by p and stored as bf16 at the token's slot, V is
+ * copied, every query head is normalised and rotated and stored in q_out.
+ * Rows with seq_lens[b] = 0 are skipped.  A row with a negative length or one
+ * above max_seq_len (PKV_FLAG_BAD_LEN), a bad page (PKV_FLAG_BAD_PAGE) or a
+ * position past the table (PKV_FLAG_BAD_POS) writes nothing, its q_out rows
+ * included.  status as for paged_kv_append.  One launch; graph-capturable. */
+pkv_status paged_kv_append_norm(const pkv_dims *dims, const pkv_tokens *tokens, void *k_pool,
+                                void *v_pool, const int32_t *kv_indices,
+                                const int32_t *kv_indptr, const int32_t *seq_lens,
+                                uint32_t *status, pkv_stream_t stream);
+
+/* The same for ragged chunks (qo_indptr, total_q and positions as in
+ * paged_kv_extend).  A token before qo_indptr[0] or behind qo_indptr[B], and
+ * every token of a row whose chunk is longer than its length or whose length
+ * is above max_seq_len, sets PKV_FLAG_BAD_LEN and writes nothing. */
+pkv_status paged_kv_extend_norm(const pkv_dims *dims, const pkv_tokens *tokens,
+                                const int32_t *qo_indptr, int total_q, void *k_pool,
+                                void *v_pool, const int32_t *kv_indices,
+                                const int32_t *kv_indptr, const int32_t *seq_lens,
+                                uint32_t *status, pkv_stream_t stream);
+
+/* ---- the 8-bit cache -------------------------------------------------------- */
+
+/* A cache of e4m3 codes with one power-of-two scale for each token and kv
+ * head, in half the bytes of the bf16 pools:
+ *   k_codes, v_codes [num_pages, page_size, Hkv, D] e4m3, 16-byte aligned
+ *   k_scale, v_scale [num_pages, page_size, Hkv]    e8m0, 16-byte aligned
+ * A head vector is code * 2^(scale - 127).  The writes below choose, for a
+ * head vector whose largest magnitude is amax,
+ *   scale = 127 + clamp(ceil(log2(amax / 448)), -40, 40),
+ *   code  = x * 2^(127 - scale) rounded to the nearest e4m3 (ties to even,
+ *           saturating at 448),
+ * from the fp32 value (V: the bf16 value), in one rounding.  An infinite or
+ * NaN element becomes a NaN code; magnitudes above 448 * 2^40 saturate.  The
+ * same pages, tables and lengths as the bf16 calls. */
+
+/* paged_kv_append_norm into an 8-bit cache (norms optional). */
+pkv_status paged_kv_append_q8(const pkv_dims *dims, const pkv_tokens *tokens, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream);
+
+/* paged_kv_extend_norm into an 8-bit cache (norms optional). */
+pkv_status paged_kv_extend_q8(const pkv_dims *dims, const pkv_tokens *tokens,
+                              const int32_t *qo_indptr, int total_q, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream);
+
+/* The rows of an 8-bit cache read back as bf16, in logical order: k_out and
+ * v_out are [num_indices, page_size, Hkv, D], and token t of row b goes to
+ * page kv_indptr[b] + t / page_size, slot t % page_size of them -- the page
+ * that entry of kv_indices names, moved to the entry's own place.  With
+ * kv_indices = 0, 1, 2, ... they are pools for paged_prefill_attn and the
+ * other bf16 calls.  Codes times their scale are exact in bf16.  Slots of no
+ * row, and those past a row's length, keep what they held.  A row with a
+ * negative length or one above max_seq_len (PKV_FLAG_BAD_LEN) is not read; a
+ * malformed or short table and a page id outside the pool
+ * (PKV_FLAG_BAD_PAGE) leave the tokens without a page as they were.  One
+ * launch; graph-capturable. */
+pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const void *v_codes,
+                            const void *k_scale, const void *v_scale,
+                            const int32_t *kv_indices, const int32_t *kv_indptr,
+                            const int32_t *seq_lens, void *k_out, void *v_out,
+                            uint32_t *status, pkv_stream_t stream);
+
+/* paged_decode_attn over an 8-bit cache: q and out bf16 [B, Hq, D], fp32
+ * softmax, num_splits, workspace and flags as for that call.  Scales as the
+ * calls above write them; the output of a row holding others is undefined.
+ * More rows x kv-head groups than the persistent kernel serves run as
+ * several launches; more than 4096 groups of kv heads are refused
+ * (PKV_ERR_UNSUPPORTED). */
+pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
+                                const void *v_codes, const void *k_scale, const void *v_scale,
+                                const int32_t *kv_indices, const int32_t *kv_indptr,
+                                const int32_t *seq_lens, int num_splits, void *workspace,
+                                size_t ws_bytes, void *out, pkv_stream_t stream);
+
 /* ---- for callers that cannot allocate ------------------------------------ */
 
 /* Size of the library-held scratch used by paged_decode_attn_noalloc. */

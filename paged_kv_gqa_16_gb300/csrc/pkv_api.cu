@@ -420,7 +420,7 @@ extern "C" {
 
 int pkv_version(void)
 {
-    return (1 << 16) | 3;
+    return (1 << 16) | 4;
 }
 
 const char *pkv_status_str(pkv_status s)
@@ -939,6 +939,199 @@ pkv_status decode_combine(const pkv_dims *dims, const float *o_part, const float
     p.D = dims->D;
     p.num_splits = num_splits;
     return launch_status(pkv::launch_combine(p, (cudaStream_t)stream));
+}
+
+namespace {
+
+pkv_status check_row_stride(long long stride, int H, int D)
+{
+    return stride == 0 || (stride % 8 == 0 && stride >= (long long)H * D) ? PKV_OK
+                                                                         : PKV_ERR_INVALID_ARG;
+}
+
+// The append and extend of pkv_tokens; k_scale == nullptr: bf16 pools.
+pkv_status token_write(const pkv_dims *dims, const pkv_tokens *t, bool extend,
+                       const int32_t *qo_indptr, int total_q, void *k_pool, void *v_pool,
+                       bool q8, void *k_scale, void *v_scale, const int32_t *kv_indices,
+                       const int32_t *kv_indptr, const int32_t *seq_lens, uint32_t *status,
+                       pkv_stream_t stream)
+{
+    pkv_status st = check_dims(dims);
+    if (st != PKV_OK)
+        return st;
+    if (t == nullptr || (extend && total_q < 0))
+        return PKV_ERR_INVALID_ARG;
+    if (dims->B == 0 || (extend && total_q == 0))
+        return PKV_OK;
+    if (t->k == nullptr || t->v == nullptr || k_pool == nullptr || v_pool == nullptr ||
+        kv_indptr == nullptr || seq_lens == nullptr || (extend && qo_indptr == nullptr) ||
+        (q8 && (k_scale == nullptr || v_scale == nullptr)) ||
+        (dims->num_indices > 0 && kv_indices == nullptr) ||
+        (t->q != nullptr && t->q_out == nullptr))
+        return PKV_ERR_INVALID_ARG;
+    const bool has_q = t->q != nullptr;
+    if (!aligned(t->k, 16) || !aligned(t->v, 16) || !aligned(k_pool, 16) ||
+        !aligned(v_pool, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+        !aligned(t->k_norm, 16) ||
+        (has_q && (!aligned(t->q, 16) || !aligned(t->q_out, 16) || !aligned(t->q_norm, 16))) ||
+        !aligned(kv_indptr, 4) || !aligned(seq_lens, 4) || !aligned(kv_indices, 4) ||
+        !aligned(qo_indptr, 4) || !aligned(status, 4))
+        return PKV_ERR_INVALID_ARG;
+    if (check_row_stride(t->k_stride, dims->Hkv, dims->D) != PKV_OK ||
+        check_row_stride(t->v_stride, dims->Hkv, dims->D) != PKV_OK ||
+        (has_q && check_row_stride(t->q_stride, dims->Hq, dims->D) != PKV_OK))
+        return PKV_ERR_INVALID_ARG;
+    // in place only where q has q_out's layout
+    if (has_q && t->q == t->q_out && t->q_stride != 0 &&
+        t->q_stride != (long long)dims->Hq * dims->D)
+        return PKV_ERR_INVALID_ARG;
+    if (((has_q && t->q_norm != nullptr) || t->k_norm != nullptr) &&
+        !(t->norm_eps >= 0.f && std::isfinite(t->norm_eps)))
+        return PKV_ERR_INVALID_ARG;
+    if (t->rope_cos_sin != nullptr && (t->rope_max_pos <= 0 || !aligned(t->rope_cos_sin, 16)))
+        return PKV_ERR_INVALID_ARG;
+    // the kernel counts a block's head vectors in 32 bits
+    if ((long long)dims->Hq + 2ll * dims->Hkv > (1 << 24))
+        return PKV_ERR_UNSUPPORTED;
+    pkv::TokenWriteParams p{};
+    p.q = has_q ? static_cast<const __nv_bfloat16 *>(t->q) : nullptr;
+    p.k = static_cast<const __nv_bfloat16 *>(t->k);
+    p.v = static_cast<const __nv_bfloat16 *>(t->v);
+    p.Hq = has_q ? dims->Hq : 0;
+    p.q_stride = t->q_stride != 0 ? t->q_stride : (long long)dims->Hq * dims->D;
+    p.k_stride = t->k_stride != 0 ? t->k_stride : (long long)dims->Hkv * dims->D;
+    p.v_stride = t->v_stride != 0 ? t->v_stride : (long long)dims->Hkv * dims->D;
+    p.q_out = has_q ? static_cast<__nv_bfloat16 *>(t->q_out) : nullptr;
+    p.q_norm = has_q ? static_cast<const __nv_bfloat16 *>(t->q_norm) : nullptr;
+    p.k_norm = static_cast<const __nv_bfloat16 *>(t->k_norm);
+    p.norm_eps = t->norm_eps;
+    p.rope = t->rope_cos_sin;
+    p.rope_max_pos = t->rope_max_pos;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_scale = q8 ? static_cast<uint8_t *>(k_scale) : nullptr;
+    p.v_scale = q8 ? static_cast<uint8_t *>(v_scale) : nullptr;
+    p.kv_indices = kv_indices;
+    p.kv_indptr = kv_indptr;
+    p.seq_lens = seq_lens;
+    p.qo_indptr = extend ? qo_indptr : nullptr;
+    p.status = status;
+    p.T = extend ? total_q : dims->B;
+    p.B = dims->B;
+    p.Hkv = dims->Hkv;
+    p.page_size = dims->page_size;
+    p.num_pages = dims->num_pages;
+    p.num_indices = dims->num_indices;
+    p.max_seq_len = dims->max_seq_len;
+    return launch_status(pkv::launch_token_write(p, dims->D, (cudaStream_t)stream));
+}
+
+} // namespace
+
+pkv_status paged_kv_append_norm(const pkv_dims *dims, const pkv_tokens *tokens, void *k_pool,
+                                void *v_pool, const int32_t *kv_indices,
+                                const int32_t *kv_indptr, const int32_t *seq_lens,
+                                uint32_t *status, pkv_stream_t stream)
+{
+    return token_write(dims, tokens, false, nullptr, 0, k_pool, v_pool, false, nullptr, nullptr,
+                       kv_indices, kv_indptr, seq_lens, status, stream);
+}
+
+pkv_status paged_kv_extend_norm(const pkv_dims *dims, const pkv_tokens *tokens,
+                                const int32_t *qo_indptr, int total_q, void *k_pool,
+                                void *v_pool, const int32_t *kv_indices,
+                                const int32_t *kv_indptr, const int32_t *seq_lens,
+                                uint32_t *status, pkv_stream_t stream)
+{
+    return token_write(dims, tokens, true, qo_indptr, total_q, k_pool, v_pool, false, nullptr,
+                       nullptr, kv_indices, kv_indptr, seq_lens, status, stream);
+}
+
+pkv_status paged_kv_append_q8(const pkv_dims *dims, const pkv_tokens *tokens, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream)
+{
+    return token_write(dims, tokens, false, nullptr, 0, k_codes, v_codes, true, k_scale, v_scale,
+                       kv_indices, kv_indptr, seq_lens, status, stream);
+}
+
+pkv_status paged_kv_extend_q8(const pkv_dims *dims, const pkv_tokens *tokens,
+                              const int32_t *qo_indptr, int total_q, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream)
+{
+    return token_write(dims, tokens, true, qo_indptr, total_q, k_codes, v_codes, true, k_scale,
+                       v_scale, kv_indices, kv_indptr, seq_lens, status, stream);
+}
+
+pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const void *v_codes,
+                            const void *k_scale, const void *v_scale,
+                            const int32_t *kv_indices, const int32_t *kv_indptr,
+                            const int32_t *seq_lens, void *k_out, void *v_out,
+                            uint32_t *status, pkv_stream_t stream)
+{
+    pkv_status st = check_dims(dims);
+    if (st != PKV_OK)
+        return st;
+    if (dims->B == 0)
+        return PKV_OK;
+    if (k_codes == nullptr || v_codes == nullptr || k_scale == nullptr || v_scale == nullptr ||
+        kv_indptr == nullptr || seq_lens == nullptr || k_out == nullptr || v_out == nullptr ||
+        (dims->num_indices > 0 && kv_indices == nullptr))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 16) ||
+        !aligned(v_scale, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+        !aligned(kv_indptr, 4) || !aligned(seq_lens, 4) || !aligned(kv_indices, 4) ||
+        !aligned(status, 4))
+        return PKV_ERR_INVALID_ARG;
+    pkv::ReadQ8Params p{};
+    p.k_codes = static_cast<const uint8_t *>(k_codes);
+    p.v_codes = static_cast<const uint8_t *>(v_codes);
+    p.k_scale = static_cast<const uint8_t *>(k_scale);
+    p.v_scale = static_cast<const uint8_t *>(v_scale);
+    p.kv_indices = kv_indices;
+    p.kv_indptr = kv_indptr;
+    p.seq_lens = seq_lens;
+    p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    p.v_out = static_cast<__nv_bfloat16 *>(v_out);
+    p.status = status;
+    p.B = dims->B;
+    p.Hkv = dims->Hkv;
+    p.D = dims->D;
+    p.page_size = dims->page_size;
+    p.num_pages = dims->num_pages;
+    p.num_indices = dims->num_indices;
+    p.max_seq_len = dims->max_seq_len;
+    return launch_status(pkv::launch_read_q8(p, (cudaStream_t)stream));
+}
+
+pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
+                                const void *v_codes, const void *k_scale, const void *v_scale,
+                                const int32_t *kv_indices, const int32_t *kv_indptr,
+                                const int32_t *seq_lens, int num_splits, void *workspace,
+                                size_t ws_bytes, void *out, pkv_stream_t stream)
+{
+    pkv_status st = check_decode_args(dims, q, k_codes, v_codes, kv_indices, kv_indptr,
+                                      seq_lens, num_splits, workspace, ws_bytes, out, true);
+    if (st != PKV_OK || dims->B == 0)
+        return st;
+    if (k_scale == nullptr || v_scale == nullptr || !aligned(k_scale, 16) ||
+        !aligned(v_scale, 16))
+        return PKV_ERR_INVALID_ARG;
+    const Layout L = layout_for(dims, num_splits);
+    char *ws = static_cast<char *>(workspace);
+    pkv::FusedParams p = persistent_params(dims, L, ws, kv_indices, kv_indptr, seq_lens);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k_codes = static_cast<const uint8_t *>(k_codes);
+    p.v_codes = static_cast<const uint8_t *>(v_codes);
+    p.k_scale = static_cast<const uint8_t *>(k_scale);
+    p.v_scale = static_cast<const uint8_t *>(v_scale);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.scale_log2 = (float)((double)dims->scale * 1.4426950408889634);
+    return launch_status(
+        pkv::launch_decode_q8(p, dims->D, num_splits, (cudaStream_t)stream));
 }
 
 } // extern "C"

@@ -1099,23 +1099,6 @@ __global__ void __launch_bounds__(WPH > 8 ? 32 * WPH : 256)
     }
 }
 
-template <typename Kernel, typename... Params>
-cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                       const Params &...p)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, p...);
-}
-
 template <int D, int HPC>
 cudaError_t launch_fused_cfg(const FusedParams &p, int grid, cudaStream_t stream)
 {

@@ -53,6 +53,25 @@ private:
     std::atomic<bool> done_[kMaxDevices]{};
 };
 
+// Launch with programmatic stream serialisation: the kernel may start while
+// the one before it drains, and waits for it (griddepcontrol.wait) itself.
+template <typename Kernel, typename... Params>
+inline cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                       const Params &...p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, p...);
+}
+
 struct AppendParams {
     __nv_bfloat16 *q;
     const __nv_bfloat16 *k_new;
@@ -68,6 +87,46 @@ struct AppendParams {
     int rope_max_pos, rope_q;
     const int32_t *qo_indptr;  // extend: [B+1] chunk offsets (append: unused)
     int total_q;               // extend: tokens in all chunks
+};
+
+// New tokens written to the cache (pkv_tokens.cu); k_scale == nullptr: bf16
+// pools, else e4m3 codes and e8m0 scales.
+struct TokenWriteParams {
+    const __nv_bfloat16 *q;        // nullable: no query work
+    const __nv_bfloat16 *k;
+    const __nv_bfloat16 *v;
+    long long q_stride, k_stride, v_stride;
+    __nv_bfloat16 *q_out;
+    const __nv_bfloat16 *q_norm;   // [D] or nullptr
+    const __nv_bfloat16 *k_norm;
+    const float *rope;             // [rope_max_pos, D/2, 2] or nullptr
+    void *k_pool;                  // bf16 pools or e4m3 codes
+    void *v_pool;
+    uint8_t *k_scale;
+    uint8_t *v_scale;
+    const int32_t *kv_indices;
+    const int32_t *kv_indptr;
+    const int32_t *seq_lens;
+    const int32_t *qo_indptr;      // extend: [B+1]; append: nullptr
+    uint32_t *status;              // nullable
+    float norm_eps;
+    int T, B, Hq, Hkv, page_size, num_pages, num_indices, max_seq_len, rope_max_pos;
+    int per_block;                 // tokens a block takes (set by the launcher)
+};
+
+// An 8-bit cache read back as bf16 (pkv_q8_read.cu).
+struct ReadQ8Params {
+    const uint8_t *k_codes;
+    const uint8_t *v_codes;
+    const uint8_t *k_scale;
+    const uint8_t *v_scale;
+    const int32_t *kv_indices;
+    const int32_t *kv_indptr;
+    const int32_t *seq_lens;
+    __nv_bfloat16 *k_out;
+    __nv_bfloat16 *v_out;
+    uint32_t *status;              // nullable
+    int B, Hkv, D, page_size, num_pages, num_indices, max_seq_len;
 };
 
 struct DecodeParams {
@@ -194,6 +253,11 @@ struct FusedParams {
     // producer and the consumers (normally the full ~2 s; shortened only by
     // the testing call).  Waits for copies already issued keep the full limit.
     unsigned long long handoff_wait_ns;
+    // the 8-bit cache (pkv_q8_decode.cu), in place of k_pool and v_pool
+    const uint8_t *k_codes;
+    const uint8_t *v_codes;
+    const uint8_t *k_scale;
+    const uint8_t *v_scale;
     // the step's plan (paged_decode_plan) or nullptr: the partition computed
     // at the kernel's start instead
     const int32_t *plan;
@@ -234,6 +298,10 @@ struct CombineParams {
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_extend(const AppendParams &p, cudaStream_t stream);
+cudaError_t launch_token_write(const TokenWriteParams &p, int D, cudaStream_t stream);
+cudaError_t launch_read_q8(const ReadQ8Params &p, cudaStream_t stream);
+// the decode over an 8-bit cache; p.k_codes ... p.v_scale in place of the pools
+cudaError_t launch_decode_q8(const FusedParams &p, int D, int grid, cudaStream_t stream);
 cudaError_t launch_advance(const AdvanceParams &p, cudaStream_t stream);
 // one persistent block per SM over the units (pairs of query tiles x B x Hkv)
 // The prefill's list for a launch (host only): units of tile pairs, their

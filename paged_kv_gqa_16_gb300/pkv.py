@@ -40,7 +40,9 @@ EXPORTS = (
     "paged_prefill_attn", "paged_kv_extend", "paged_decode_step_advance",
     "pkv_testing_set_handoff_wait_ns", "paged_decode_plan", "paged_decode_attn_planned",
     "paged_decode_step_planned", "decode_attn_contig_planned", "paged_prefill_attn_ws",
-    "pkv_prefill_workspace_bytes", "pkv_prefill_plan",
+    "pkv_prefill_workspace_bytes", "pkv_prefill_plan", "paged_kv_append_norm",
+    "paged_kv_extend_norm", "paged_kv_append_q8", "paged_kv_extend_q8", "paged_kv_read_q8",
+    "paged_decode_attn_q8",
 )
 
 
@@ -62,6 +64,17 @@ class Dims(ctypes.Structure):
         return "Dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class Tokens(ctypes.Structure):
+    """pkv_tokens; made by :func:`tokens`, which keeps the tensors alive."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+        ("v_stride", ctypes.c_longlong), ("q_out", ctypes.c_void_p),
+        ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
+        ("rope_cos_sin", ctypes.c_void_p), ("rope_max_pos", ctypes.c_int),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -79,6 +92,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         DP = ctypes.POINTER(Dims)
+        TP = ctypes.POINTER(Tokens)
         sig = {
             "pkv_split_chunk": (I, [DP, I]),
             "pkv_workspace_bytes": (Z, [DP, I]),
@@ -105,6 +119,12 @@ def lib():
             "pkv_prefill_workspace_bytes": (Z, [I, I]),
             "pkv_prefill_plan": (I, [DP, I, I, Z, P]),
             "paged_kv_extend": (I, [DP, P, P, P, P, I, P, P, P, P, P, P, I, I, P, P]),
+            "paged_kv_append_norm": (I, [DP, TP, P, P, P, P, P, P, P]),
+            "paged_kv_extend_norm": (I, [DP, TP, P, I, P, P, P, P, P, P, P]),
+            "paged_kv_append_q8": (I, [DP, TP, P, P, P, P, P, P, P, P, P]),
+            "paged_kv_extend_q8": (I, [DP, TP, P, I, P, P, P, P, P, P, P, P, P]),
+            "paged_kv_read_q8": (I, [DP, P, P, P, P, P, P, P, P, P, P, P]),
+            "paged_decode_attn_q8": (I, [DP, P, P, P, P, P, P, P, P, I, P, Z, P, P]),
             "pkv_testing_set_handoff_wait_ns": (I, [ctypes.c_ulonglong]),
             "pkv_status_str": (ctypes.c_char_p, [I]),
             "pkv_version": (I, []),
@@ -341,6 +361,107 @@ def paged_kv_extend(d: Dims, q, k_new, v_new, qo_indptr, k_pool, v_pool, kv_indi
         ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(qo_indptr), total_q,
         _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
         _ptr(rope_cos_sin), rope_max_pos, int(bool(rope_q)), _ptr(status), _stream(stream)))
+
+
+# ---- new tokens: normalised, rotated, written --------------------------------
+def _rows(x, name: str):
+    """(pointer, row stride) of new-token rows [T, H, D] whose heads are packed."""
+    T, H, D = x.shape
+    if x.stride(2) != 1 or (H > 1 and x.stride(1) != D):
+        raise ValueError(f"{name} must be [tokens, heads, D] with packed heads")
+    return x.data_ptr(), x.stride(0) if T > 1 else 0
+
+
+def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6,
+           rope_cos_sin=None, rope_max_pos: int = 0) -> Tokens:
+    """The new tokens of a paged_kv_append_norm / _extend_norm / _append_q8 /
+    _extend_q8 call: q [T, Hq, D] (or None), k and v [T, Hkv, D] bf16 with any
+    row stride (slices of one projection's output), q_out [T, Hq, D] for the
+    processed queries (None: in place, which needs a packed q), optional [D]
+    norm weights, and the RoPE table."""
+    t = Tokens(norm_eps=norm_eps, rope_max_pos=rope_max_pos)
+    if q is not None:
+        t.q, t.q_stride = _rows(q, "q")
+        t.q_out = t.q if q_out is None else _ptr(q_out)
+        t.q_norm = _ptr(q_norm)
+        if q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+            raise ValueError("q and k must have the same tokens and head size")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    t.k, t.k_stride = _rows(k, "k")
+    t.v, t.v_stride = _rows(v, "v")
+    t.k_norm = _ptr(k_norm)
+    t.rope_cos_sin = _ptr(rope_cos_sin)
+    t.shape = (int(k.shape[0]), None if q is None else int(q.shape[1]), int(k.shape[1]),
+               int(k.shape[2]))
+    t.tensors = (q, k, v, q_out, q_norm, k_norm, rope_cos_sin)
+    return t
+
+
+def _token_count(d: Dims, t: Tokens, per_row: bool = False) -> int:
+    T, Hq, Hkv, D = t.shape
+    if (Hq is not None and Hq != d.Hq) or Hkv != d.Hkv or D != d.D or (per_row and T != d.B):
+        raise ValueError(f"tokens of shape {t.shape} do not fit {d!r}")
+    return T
+
+
+def paged_kv_append_norm(d: Dims, t: Tokens, k_pool, v_pool, kv_indices, kv_indptr, seq_lens,
+                         status=None, stream=None) -> None:
+    """One new token a row: q and K normalised and rotated, K/V to their slots."""
+    _token_count(d, t, per_row=True)
+    _check("paged_kv_append_norm", lib().paged_kv_append_norm(
+        ctypes.byref(d), ctypes.byref(t), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices),
+        _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
+
+
+def paged_kv_extend_norm(d: Dims, t: Tokens, qo_indptr, k_pool, v_pool, kv_indices, kv_indptr,
+                         seq_lens, status=None, stream=None) -> None:
+    """paged_kv_append_norm for ragged chunks of new tokens."""
+    _check("paged_kv_extend_norm", lib().paged_kv_extend_norm(
+        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t), _ptr(k_pool), _ptr(v_pool),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
+
+
+# ---- the 8-bit cache ----------------------------------------------------------
+def paged_kv_append_q8(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, kv_indices,
+                       kv_indptr, seq_lens, status=None, stream=None) -> None:
+    """paged_kv_append_norm into an 8-bit cache: codes [num_pages, page_size,
+    Hkv, D] (torch.float8_e4m3fn) and scales [num_pages, page_size, Hkv]
+    (torch.float8_e8m0fnu or uint8)."""
+    _token_count(d, t, per_row=True)
+    _check("paged_kv_append_q8", lib().paged_kv_append_q8(
+        ctypes.byref(d), ctypes.byref(t), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
+        _ptr(v_scale), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status),
+        _stream(stream)))
+
+
+def paged_kv_extend_q8(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale, v_scale,
+                       kv_indices, kv_indptr, seq_lens, status=None, stream=None) -> None:
+    """paged_kv_append_q8 for ragged chunks of new tokens."""
+    _check("paged_kv_extend_q8", lib().paged_kv_extend_q8(
+        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t), _ptr(k_codes),
+        _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), _ptr(kv_indices), _ptr(kv_indptr),
+        _ptr(seq_lens), _ptr(status), _stream(stream)))
+
+
+def paged_kv_read_q8(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
+                     seq_lens, k_out, v_out, status=None, stream=None) -> None:
+    """Every row's tokens as bf16 into pages [num_indices, page_size, Hkv, D]
+    in the table's order (pools for paged_prefill_attn with kv_indices 0, 1, ...)."""
+    _check("paged_kv_read_q8", lib().paged_kv_read_q8(
+        ctypes.byref(d), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(k_out), _ptr(v_out),
+        _ptr(status), _stream(stream)))
+
+
+def paged_decode_attn_q8(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
+                         seq_lens, num_splits: int, workspace, out, stream=None) -> None:
+    """paged_decode_attn over an 8-bit cache."""
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check("paged_decode_attn_q8", lib().paged_decode_attn_q8(
+        ctypes.byref(d), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
+        ws_bytes, _ptr(out), _stream(stream)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
