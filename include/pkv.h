@@ -563,16 +563,28 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
                             uint32_t *status, pkv_stream_t stream);
 
 /* paged_decode_attn over an 8-bit cache: q and out bf16 [B, Hq, D], fp32
- * softmax, num_splits, workspace and flags as for that call.  Scales as the
- * calls above write them; the output of a row holding others is undefined.
- * More rows x kv-head groups than the persistent kernel serves run as
- * several launches; more than 4096 groups of kv heads are refused
- * (PKV_ERR_UNSUPPORTED). */
+ * softmax, num_splits, workspace, flags and the plan left behind as for that
+ * call (paged_decode_plan serves both caches).  Scales as the writes above
+ * choose them, or any in [127 - 40, 127 + 40]; the output of a row holding
+ * others is undefined.  One persistent kernel plus, when num_splits > 1, the
+ * piece combine; a batch of more than 4096 rows x kv-head groups (a group: 8,
+ * 4, 2 or 1 kv heads, the most that divide Hkv) takes several such pairs, one
+ * after the other.  PKV_ERR_UNSUPPORTED: Hkv of more than 4096 groups, or
+ * max_seq_len x groups past 2^31. */
 pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
                                 const void *v_codes, const void *k_scale, const void *v_scale,
                                 const int32_t *kv_indices, const int32_t *kv_indptr,
                                 const int32_t *seq_lens, int num_splits, void *workspace,
                                 size_t ws_bytes, void *out, pkv_stream_t stream);
+
+/* paged_decode_attn_q8 on the workspace's plan, under the conditions of
+ * paged_decode_attn_planned; the same results, bit for bit. */
+pkv_status paged_decode_attn_q8_planned(const pkv_dims *dims, const void *q, const void *k_codes,
+                                        const void *v_codes, const void *k_scale,
+                                        const void *v_scale, const int32_t *kv_indices,
+                                        const int32_t *kv_indptr, const int32_t *seq_lens,
+                                        int num_splits, void *workspace, size_t ws_bytes,
+                                        void *out, pkv_stream_t stream);
 
 /* ---- for callers that cannot allocate ------------------------------------ */
 

@@ -1107,11 +1107,11 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
     return launch_status(pkv::launch_read_q8(p, (cudaStream_t)stream));
 }
 
-pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
-                                const void *v_codes, const void *k_scale, const void *v_scale,
-                                const int32_t *kv_indices, const int32_t *kv_indptr,
-                                const int32_t *seq_lens, int num_splits, void *workspace,
-                                size_t ws_bytes, void *out, pkv_stream_t stream)
+static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void *k_codes,
+                                 const void *v_codes, const void *k_scale, const void *v_scale,
+                                 const int32_t *kv_indices, const int32_t *kv_indptr,
+                                 const int32_t *seq_lens, int num_splits, void *workspace,
+                                 size_t ws_bytes, void *out, pkv_stream_t stream, bool planned)
 {
     pkv_status st = check_decode_args(dims, q, k_codes, v_codes, kv_indices, kv_indptr,
                                       seq_lens, num_splits, workspace, ws_bytes, out, true);
@@ -1121,17 +1121,80 @@ pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void 
         !aligned(v_scale, 16))
         return PKV_ERR_INVALID_ARG;
     const Layout L = layout_for(dims, num_splits);
+    const int groups = dims->Hkv / L.hpc;
+    // rows of one launch: its rows x kv-head groups have their prefix sums in
+    // shared memory, and their weights in 31 bits
+    const long long by_weight =
+        ((1ll << 31) - 1) / ((long long)dims->max_seq_len + pkv::kFusedRowCost) / groups;
+    const long long by_rows = pkv::kFusedMaxRows / groups;
+    const int most = (int)(by_weight < by_rows ? by_weight : by_rows);
+    if (most < 1)
+        return PKV_ERR_UNSUPPORTED;
     char *ws = static_cast<char *>(workspace);
-    pkv::FusedParams p = persistent_params(dims, L, ws, kv_indices, kv_indptr, seq_lens);
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k_codes = static_cast<const uint8_t *>(k_codes);
-    p.v_codes = static_cast<const uint8_t *>(v_codes);
-    p.k_scale = static_cast<const uint8_t *>(k_scale);
-    p.v_scale = static_cast<const uint8_t *>(v_scale);
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.scale_log2 = (float)((double)dims->scale * 1.4426950408889634);
-    return launch_status(
-        pkv::launch_decode_q8(p, dims->D, num_splits, (cudaStream_t)stream));
+    int32_t *plan = reinterpret_cast<int32_t *>(ws + L.plan_off);
+    const bool one = dims->B <= most;
+    for (int b0 = 0; b0 < dims->B; b0 += most) {
+        pkv_dims d = *dims;
+        d.B = dims->B - b0 < most ? dims->B - b0 : most;
+        pkv::FusedParams p =
+            persistent_params(&d, L, ws, kv_indices, kv_indptr + b0, seq_lens + b0);
+        p.Bv = d.B * groups;
+        p.q = static_cast<const __nv_bfloat16 *>(q) + (size_t)b0 * d.Hq * d.D;
+        p.out = static_cast<__nv_bfloat16 *>(out) + (size_t)b0 * d.Hq * d.D;
+        p.k_codes = static_cast<const uint8_t *>(k_codes);
+        p.v_codes = static_cast<const uint8_t *>(v_codes);
+        p.k_scale = static_cast<const uint8_t *>(k_scale);
+        p.v_scale = static_cast<const uint8_t *>(v_scale);
+        const size_t pieces = ((size_t)num_splits + p.Bv) * L.HQV;
+        p.ml_part = reinterpret_cast<float *>(ws + L.piece_ml_off);
+        p.o_part = reinterpret_cast<float *>(ws + L.piece_ml_off +
+                                             round_up(pieces * 2 * sizeof(float), 256));
+        // the plan is of all rows: a call of several launches has none
+        p.plan = one && planned ? plan : nullptr;
+        p.plan_out = one && !planned ? plan : nullptr;
+        p.scale_log2 = (float)((double)dims->scale * 1.4426950408889634);
+        st = launch_status(pkv::launch_decode_q8(p, d.D, num_splits, (cudaStream_t)stream));
+        if (st != PKV_OK)
+            return st;
+        if (num_splits == 1)
+            continue;
+        pkv::PieceCombineParams c{};
+        c.o_part = p.o_part;
+        c.ml_part = p.ml_part;
+        c.row_info = p.row_info;
+        c.out = p.out;
+        c.B = d.B;
+        c.Bv = p.Bv;
+        c.Hq = d.Hq;
+        c.HQV = L.HQV;
+        c.planned = p.plan != nullptr ? 1 : 0;
+        st = launch_status(
+            pkv::launch_piece_combine(c, d.D, num_splits, (cudaStream_t)stream));
+        if (st != PKV_OK)
+            return st;
+    }
+    return PKV_OK;
+}
+
+pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
+                                const void *v_codes, const void *k_scale, const void *v_scale,
+                                const int32_t *kv_indices, const int32_t *kv_indptr,
+                                const int32_t *seq_lens, int num_splits, void *workspace,
+                                size_t ws_bytes, void *out, pkv_stream_t stream)
+{
+    return decode_q8_impl(dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
+                          seq_lens, num_splits, workspace, ws_bytes, out, stream, false);
+}
+
+pkv_status paged_decode_attn_q8_planned(const pkv_dims *dims, const void *q, const void *k_codes,
+                                        const void *v_codes, const void *k_scale,
+                                        const void *v_scale, const int32_t *kv_indices,
+                                        const int32_t *kv_indptr, const int32_t *seq_lens,
+                                        int num_splits, void *workspace, size_t ws_bytes,
+                                        void *out, pkv_stream_t stream)
+{
+    return decode_q8_impl(dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
+                          seq_lens, num_splits, workspace, ws_bytes, out, stream, true);
 }
 
 } // extern "C"

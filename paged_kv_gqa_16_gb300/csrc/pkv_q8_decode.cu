@@ -1,165 +1,668 @@
-// pkv_q8_decode.cu -- split-free decode attention over the 8-bit cache.
+// pkv_q8_decode.cu -- decode attention over the 8-bit cache.
 //
 // out[b, h] = sum_t w_t V_t / sum_t w_t, w_t = exp(scale q.K_t - max), with
-// K_t = 2^ek code, V_t = 2^ev code.  One block per (row, kv head): chunks of
-// 128 tokens, a thread a token for the scores, a thread a column for the sum.
+// K_t = 2^ek_t code, V_t = 2^ev_t code of the token's kv head.  A step reads
+// every cached token once and does 4 Hq/Hkv D operations for 2 D + 2 bytes,
+// so it is bound by memory; the work is split over the cache's length as in
+// the bf16 decode (pkv_fused.cu): one persistent block per SM takes an equal
+// range of all rows' tokens laid end to end, a producer warp streams whole
+// token rows (HPC kv heads) into a ring of shared-memory stages, and the
+// piece combine joins the rows that several blocks share.
+//
+// What the 8-bit cache changes:
+//  - Half the bytes a token means twice the tokens a second, so the tensor
+//    products must waste less: here the tokens are the M rows of the
+//    products (S^T = K Q^T, O^T = V^T P^T, m16n8k16) and the query heads the
+//    eight columns, which a group of 8 heads fills and a group of 4 fills
+//    half -- half the products and half the accumulators of heads as rows.
+//    NT = 2 column tiles serve groups of 9 to 16 heads.
+//  - Codes become f16 exactly (one cvt for two codes).  q is scaled by a
+//    power of two to at most 2 in size, which keeps its eight significant
+//    bits in f16; that power and the softmax scale go into the score's
+//    factor in fp32.
+//  - Both scales act on the scores: x_t = 2^ek_t (s_t c) and y_t = x_t + ev_t
+//    in the log2 domain.  The weights used for O are 2^(y_t - M), M following
+//    the largest y_t, so they are in f16's range however the values' scales
+//    differ; the sum of softmax weights takes each of them times 2^-ev_t (a
+//    power of two, exact).  Both sums carry the same 2^-M.
+//  - M is raised only when some y_t exceeds it by more than 8: a weight is
+//    then at most 2^8 and the usual tile needs no maximum over its lanes and
+//    no rescaling.
+//  - Eight consumer warps whatever the number of kv heads: HPC heads times
+//    WPH = 8 / HPC groups of tokens, each group with sums of its own, joined
+//    through shared memory at the end of a piece.
 #include <cmath>
 
-#include "pkv_device.cuh"
-#include "pkv_internal.h"
+#include "pkv_partition.cuh"
 #include "pkv_q8.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kChunk = 128;
+constexpr int kWarps = 8;                 // consumer warps
+constexpr float kRaise = 8.f;             // how far a score may exceed its base
+
+template <int D, int HPC, int NT>
+struct Q8Cfg {
+    static constexpr int kWph = kWarps / HPC;         // warps of a kv head
+    static constexpr int kTok = 16 * kWph;            // tokens of a stage
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kRowBytes = HPC * D;         // one token, HPC kv heads
+    // an odd number of 16-byte units: eight tokens' vectors of one head lie in
+    // different banks
+    static constexpr int kPitch = kRowBytes + 16;
+    static constexpr int kCodeBytes = 2 * kTok * kPitch;
+    static constexpr int kScaleBytes = 2 * kTok * 8;  // 8 bytes a token row, K then V
+    static constexpr int kStageBytes = kCodeBytes + kScaleBytes;
+    // join of a head's warps: their sums [warp][NT * 8][D + 4], base and sum
+    static constexpr int kSumPitch = D + 4;
+    static constexpr int kJoinBytes =
+        kWph == 1 ? 0 : kWarps * NT * 8 * (kSumPitch + 2) * 4;
+    static constexpr int kFixedBytes = kJoinBytes + (kFusedMaxRows + 1) * 4 + 16 + 2 * 8 * 8 + 128;
+    static constexpr int kStagesFit = (kSmemLimit - kFixedBytes) / kStageBytes;
+    static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
+    static_assert(kStages >= 2, "ring needs two stages");
+    static constexpr int kJoinOffset = kStages * kStageBytes;
+    static constexpr int kBarOffset = kJoinOffset + kJoinBytes;
+    static constexpr int kAbortOffset = kBarOffset + 2 * kStages * 8;
+    static constexpr int kPrefixOffset = kAbortOffset + 16;
+    static constexpr int kSmemBytes = kPrefixOffset + (kFusedMaxRows + 1) * 4;
+    static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
+    static_assert(kStageBytes % 16 == 0 && kJoinBytes % 16 == 0, "alignment");
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two floats to f16x2, the first in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
+{
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// This thread's earlier cp.async copies arrive on `bar` when they have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// Four or eight bytes global -> shared, of which the first `bytes` are read
+// (the others are zero).
+template <int SIZE>
+__device__ __forceinline__ void cp_async(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src),
+                 "n"(SIZE), "r"(bytes)
+                 : "memory");
+}
+
+template <int D, int HPC, int NT>
+__global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
+    decode_q8_kernel(const FusedParams p)
+{
+    using C = Q8Cfg<D, HPC, NT>;
+    constexpr int NST = C::kStages;
+    extern __shared__ __align__(128) unsigned char smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOffset);
+    uint64_t *empty = full + NST;
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kAbortOffset);
+    int *prefix = reinterpret_cast<int *>(smem + C::kPrefixOffset);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    const int Bv = p.Bv;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 64);     // every producer lane, and its scale copies
+            mbar_init(&empty[i], kWarps);
+        }
+        fence_mbar_init();
+        *abort = 0;
+    }
+    grid_dependency_wait();
+
+    // the partition, from the step's plan or computed here (as in pkv_fused.cu)
+    bool planned = false;
+    if (p.plan != nullptr) {
+        planned = p.plan[2] == (int)gridDim.x && p.plan[3] == Bv && p.plan[4] == p.B &&
+                  p.plan[5] == p.page_size;
+        for (int i = threadIdx.x; i <= Bv; i += C::kThreads)
+            prefix[i] = p.plan[kPlanHeaderInts + i];
+        __syncthreads();
+    }
+    if (!planned)
+        row_prefix(p, prefix, cta == 0);
+
+    const unsigned T = (unsigned)prefix[Bv];
+    const unsigned Gu = active_blocks(T, gridDim.x);
+    const int G = (int)Gu;
+
+    // rows with no tokens: zero output, no pieces (owner: block r mod grid)
+    for (int r = cta; r < Bv; r += gridDim.x) {
+        if (prefix[r + 1] == prefix[r]) {
+            const int b = r % p.B, hg = r / p.B;
+            uint4 *o = reinterpret_cast<uint4 *>(
+                p.out + ((size_t)b * p.Hq + (size_t)hg * HPC * p.n_rep) * D);
+            for (int i = threadIdx.x; i < HPC * p.n_rep * D / 8; i += blockDim.x)
+                o[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (threadIdx.x == 0 && !planned) {
+                p.row_info[2 * r] = 0;
+                p.row_info[2 * r + 1] = 0;
+            }
+        }
+    }
+    // an unplanned call leaves its partition behind as the step's plan
+    int32_t *plan_e = p.plan_out != nullptr
+                          ? const_cast<int32_t *>(plan_entry(p.plan_out, Bv, cta)) : nullptr;
+    if (p.plan_out != nullptr && cta == 0) {
+        for (int i = threadIdx.x; i <= Bv; i += blockDim.x)
+            p.plan_out[kPlanHeaderInts + i] = prefix[i];
+        if (threadIdx.x == 0) {
+            p.plan_out[0] = (int)T;
+            p.plan_out[1] = G;
+            p.plan_out[2] = (int)gridDim.x;
+            p.plan_out[3] = Bv;
+            p.plan_out[4] = p.B;
+            p.plan_out[5] = p.page_size;
+        }
+    }
+    const unsigned t_q = T / Gu, t_r = T % Gu;
+    const long long start = (long long)t_q * cta + t_r * (unsigned)cta / Gu;
+    const long long end = (long long)t_q * (cta + 1) + t_r * (unsigned)(cta + 1) / Gu;
+    if (cta >= G || start >= end) {
+        if (plan_e != nullptr && threadIdx.x == 0)
+            plan_e[0] = -1;
+        return;
+    }
+    const int r0 = first_row(prefix, Bv, start);
+
+    if (warp == kWarps) {
+        // ======================= producer warp ============================
+        const uint64_t policy = policy_evict_first();
+        const int my_t = lane & 15;
+        const bool my_v = lane >= 16;
+        const uint8_t *codes = my_v ? p.v_codes : p.k_codes;
+        const uint8_t *scales = my_v ? p.v_scale : p.k_scale;
+        const size_t scale_bytes = (size_t)p.num_pages * p.page_size * p.Hkv;
+        int it = 0;
+        bool aborted = false;
+        auto page_of_tok = [&](int t) {
+            return p.ps_shift >= 0 ? (t >> p.ps_shift) : (t / p.page_size);
+        };
+        for (int r = r0; r < Bv && !aborted; ++r) {
+            // [lo, hi): the positions of the row's tokens
+            const long long lo = (long long)prefix[r] + p.row_cost, hi = prefix[r + 1];
+            if (lo >= end)
+                break;
+            if (hi == prefix[r])
+                continue;
+            const int t0 = (int)((start > lo ? start : lo) - lo);
+            const int t1 = (int)((end < hi ? end : hi) - lo);
+            const int b = r % p.B, hg = r / p.B;
+            const int pg0 = p.kv_indptr[b];
+            int npg = p.kv_indptr[b + 1] - pg0;
+            if (pg0 < 0 || npg < 0 || pg0 > p.num_indices - npg)
+                npg = 0;                               // a table changed since the plan
+            // page-table window: lane l holds entries wb + l and wb + 32 + l
+            int wb = (page_of_tok(t0) >> 5) << 5;
+            int idx0 = wb + lane < npg ? __ldg(p.kv_indices + pg0 + wb + lane) : 0;
+            int idx1 = wb + 32 + lane < npg ? __ldg(p.kv_indices + pg0 + wb + 32 + lane) : 0;
+            if (plan_e != nullptr && r == r0) {
+                plan_e[8 + lane] = idx0;
+                plan_e[40 + lane] = idx1;
+                if (lane < 8) {
+                    const long long v = lane == 0 ? r0 : lane == 1 ? wb : lane == 2 ? pg0
+                                      : lane == 3 ? npg : lane == 4 ? lo : lane == 5 ? hi
+                                      : lane == 6 ? start : end;
+                    plan_e[lane] = (int)v;
+                }
+            }
+            for (int tok = t0; tok < t1; tok += C::kTok, ++it) {
+                const int st = it % NST;
+                if (it >= NST) {
+                    const bool ok = mbar_wait_or_abort(
+                        &empty[st], (uint32_t)(((it / NST) - 1) & 1), p.handoff_wait_ns, abort);
+                    if (!__all_sync(kFull, ok)) {
+                        aborted = true;
+                        if (lane == 0) {
+                            *abort = 1;
+                            atomicOr(p.status, kFlagTimeout);
+                        }
+                        break;
+                    }
+                }
+                fence_proxy_async_smem();
+                unsigned char *stage = smem + st * C::kStageBytes;
+                const int nvalid = min(C::kTok, t1 - tok);
+                if (lane == 0)
+                    mbar_expect_tx(&full[st], (uint32_t)(nvalid * 2 * C::kRowBytes));
+                for (int sub = 0; sub < nvalid; sub += 16) {
+                    const int tb = tok + sub, n16 = min(16, t1 - tb);
+                    if (page_of_tok(tb) >= wb + 32) {       // slide the window by 32
+                        wb += 32;
+                        idx0 = idx1;
+                        idx1 = wb + 32 + lane < npg
+                                   ? __ldg(p.kv_indices + pg0 + wb + 32 + lane) : 0;
+                    }
+                    // every lane joins the shuffles; only lanes with a token use them
+                    const int t = tb + (my_t < n16 ? my_t : 0);
+                    const int pi = page_of_tok(t);
+                    const int sl = t - pi * p.page_size;
+                    const int wofs = pi - wb;                // in [0, 64)
+                    const int e0 = __shfl_sync(kFull, idx0, wofs & 31);
+                    const int e1 = __shfl_sync(kFull, idx1, wofs & 31);
+                    int page = wofs < 32 ? e0 : e1;
+                    const int srow = (my_v ? C::kTok : 0) + sub + my_t;
+                    unsigned char *row = stage + srow * C::kPitch;
+                    if (my_t < n16) {
+                        if (page < 0 || page >= p.num_pages) {
+                            atomicOr(p.status, kFlagBadPage);
+                            page = 0;
+                        }
+                        const size_t head =
+                            ((size_t)page * p.page_size + sl) * (size_t)p.Hkv + (size_t)hg * HPC;
+                        bulk_copy_g2s_hint(row, codes + head * D, C::kRowBytes, &full[st], policy);
+                        unsigned char *sc = stage + C::kCodeBytes + srow * 8;
+                        if constexpr (HPC == 8) {
+                            cp_async<8>(sc, scales + head, 8);
+                        } else if constexpr (HPC == 4) {
+                            cp_async<4>(sc, scales + head, 4);
+                        } else {
+                            // the aligned word around the HPC bytes, and where they are in it
+                            const size_t word = head & ~(size_t)3;
+                            const size_t left = scale_bytes - word;
+                            cp_async<4>(sc, scales + word, left < 4 ? (int)left : 4);
+                            sc[4] = (unsigned char)(head & 3);
+                        }
+                    } else if (my_v) {
+                        // V rows past the piece's end must be finite (their weight is 0)
+                        uint4 *z = reinterpret_cast<uint4 *>(row);
+                        for (int k = 0; k < C::kRowBytes / 16; ++k)
+                            z[k] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                cp_async_arrive(&full[st]);
+                mbar_arrive(&full[st]);
+            }
+        }
+        // Let the copies already issued land before this warp exits, with the
+        // full time limit: a consumer that gave up skips its stages, and the
+        // block must not exit while a copy into its shared memory is in flight.
+        for (int k = (it > NST ? it - NST : 0); k < it; ++k)
+            (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
+        grid_launch_dependents();
+        return;
+    }
+
+    // ========================= consumer warps ===============================
+    const int hw = warp % HPC, tg = warp / HPC;   // kv head, token group
+    const int g = lane >> 2, c = lane & 3;
+    const uint32_t smem_s = smem_addr(smem);
+    // K: matrices of 8 tokens x 16 bytes: (tokens 0-7, 8-15) x two 16-byte columns
+    const uint32_t k_off = (uint32_t)((tg * 16 + (lane & 15)) * C::kPitch + hw * D + (lane >> 4) * 16);
+    const uint32_t v_off = k_off + C::kTok * C::kPitch;
+    int it = 0;
+    bool aborted = false;
+
+    for (int r = r0; r < Bv; ++r) {
+        const long long lo = (long long)prefix[r] + p.row_cost, hi = prefix[r + 1];
+        if (lo >= end)
+            break;
+        if (hi == prefix[r])
+            continue;
+        const int t0 = (int)((start > lo ? start : lo) - lo);
+        const int t1 = (int)((end < hi ? end : hi) - lo);
+        const int b = r % p.B, hg = r / p.B;
+        const size_t qrow0 = (size_t)b * p.Hq + (size_t)(hg * HPC + hw) * p.n_rep;
+        const int first = block_of(lo, T, G);
+        const int last = block_of(hi - 1, T, G);
+        if (t0 == 0 && warp == 0 && lane == 0 && !planned) {
+            p.row_info[2 * r] = first;
+            p.row_info[2 * r + 1] = last - first + 1;
+        }
+
+        // q as the products' B operand: lane (g, c) holds elements 4c .. 4c + 3
+        // of each 16 of head g, the order in which a K word's four codes come
+        uint32_t qf[NT][D / 16][2];
+        float cq[NT][2];                   // factors of heads 2c, 2c + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * 8 + g;
+            uint2 raw[D / 16];
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                raw[j] = h < p.n_rep
+                             ? __ldg(reinterpret_cast<const uint2 *>(p.q + (qrow0 + h) * D) + j * 4 + c)
+                             : make_uint2(0u, 0u);
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(raw[j].x)), fabsf(bf16_hi(raw[j].x))),
+                                         fmaxf(fabsf(bf16_lo(raw[j].y)), fabsf(bf16_hi(raw[j].y)))));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+            // 2^-n, n the exponent of amax, both powers kept in the normal range
+            const int n = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
+            const float down = __uint_as_float((unsigned)(127 - n) << 23);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                qf[nt][j][0] = pack_f16x2(bf16_lo(raw[j].x) * down, bf16_hi(raw[j].x) * down);
+                qf[nt][j][1] = pack_f16x2(bf16_lo(raw[j].y) * down, bf16_hi(raw[j].y) * down);
+            }
+            const float up = __uint_as_float((unsigned)(127 + n) << 23) * p.scale_log2;
+            cq[nt][0] = __shfl_sync(kFull, up, (2 * c) * 4);
+            cq[nt][1] = __shfl_sync(kFull, up, (2 * c + 1) * 4);
+        }
+
+        float m_run[NT][2], l_run[NT][2];
+        float oacc[NT][D / 16][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m_run[nt][0] = m_run[nt][1] = -INFINITY;
+            l_run[nt][0] = l_run[nt][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                oacc[nt][j][0] = oacc[nt][j][1] = oacc[nt][j][2] = oacc[nt][j][3] = 0.f;
+        }
+
+        for (int tok = t0; tok < t1; tok += C::kTok, ++it) {
+            const int st = it % NST;
+            if (!aborted) {
+                const bool ok = mbar_wait_or_abort(&full[st], (uint32_t)((it / NST) & 1),
+                                                   p.handoff_wait_ns, abort);
+                if (!__all_sync(kFull, ok)) {
+                    aborted = true;
+                    if (lane == 0) {
+                        *abort = 1;
+                        atomicOr(p.status, kFlagTimeout);
+                    }
+                }
+            }
+            const int nvalid = t1 - tok - tg * 16;           // of this warp's 16 tokens
+            if (!aborted && nvalid > 0) {
+                const uint32_t stage_s = smem_s + st * C::kStageBytes;
+                const unsigned char *sc = smem + st * C::kStageBytes + C::kCodeBytes;
+
+                float sacc[NT][2][4] = {};
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t r0_, r1_, r2_, r3_;
+                    ldmatrix_x4(r0_, r1_, r2_, r3_, stage_s + k_off + i * 32);
+                    const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2(r1_),
+                                            f16x2_of_e4m3x2_hi(r0_), f16x2_of_e4m3x2_hi(r1_)};
+                    const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2(r3_),
+                                            f16x2_of_e4m3x2_hi(r2_), f16x2_of_e4m3x2_hi(r3_)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(sacc[nt][0], a0, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+                        mma_f16(sacc[nt][1], a1, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+                    }
+                }
+                // this lane's tokens g and g + 8: their scales
+                float fk[2], ev[2], inv_v[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int row = tg * 16 + g + u * 8;
+                    const unsigned char *sk = sc + row * 8, *sv = sk + C::kTok * 8;
+                    const unsigned bk = HPC >= 4 ? sk[hw] : sk[(sk[4] & 3) + hw];
+                    const unsigned bv = HPC >= 4 ? sv[hw] : sv[(sv[4] & 3) + hw];
+                    const bool in = g + u * 8 < nvalid;
+                    fk[u] = q8_scale(bk);
+                    ev[u] = in ? (float)((int)bv - 127) : -INFINITY;
+                    inv_v[u] = in ? __uint_as_float((254u - bv) << 23) : 0.f;
+                }
+                float y[NT][4];
+                bool raise = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = (sacc[nt][0][e] + sacc[nt][1][e]) * (fk[e >> 1] * cq[nt][e & 1]);
+                        // (a token past the end: whatever its row held)
+                        y[nt][e] = ev[e >> 1] == -INFINITY ? -INFINITY : x + ev[e >> 1];
+                        raise |= y[nt][e] > m_run[nt][e & 1] + kRaise;
+                    }
+                if (__any_sync(kFull, raise)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float mx = fmaxf(y[nt][e], y[nt][e + 2]);
+                            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                            const float mn = fmaxf(m_run[nt][e], mx);
+                            const float a = mn == -INFINITY ? 1.f : exp2f(m_run[nt][e] - mn);
+                            m_run[nt][e] = mn;
+                            l_run[nt][e] *= a;
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                oacc[nt][j][e] *= a;
+                                oacc[nt][j][e + 2] *= a;
+                            }
+                        }
+                }
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float base = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+                        w[e] = exp2f(y[nt][e] - base);
+                        l_run[nt][e & 1] = fmaf(w[e], inv_v[e >> 1], l_run[nt][e & 1]);
+                    }
+                    // S^T's layout has a token's heads in a lane, P^T's B operand a
+                    // head's tokens: transpose the two 8 x 8 halves
+                    pb[nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                    pb[nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+                }
+                // V^T: a transposed 8-token x 16-byte matrix gives lane (g, c) the codes
+                // (t, d), (t, d+1), (t+1, d), (t+1, d+1) of t = 2c, d = 2g: swapping the
+                // middle two leaves the token pairs of column d and of column d + 1
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t r0_, r1_, r2_, r3_;
+                    ldmatrix_x4_trans(r0_, r1_, r2_, r3_, stage_s + v_off + i * 32);
+                    r0_ = __byte_perm(r0_, 0, 0x3120);
+                    r1_ = __byte_perm(r1_, 0, 0x3120);
+                    r2_ = __byte_perm(r2_, 0, 0x3120);
+                    r3_ = __byte_perm(r3_, 0, 0x3120);
+                    const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2_hi(r0_),
+                                            f16x2_of_e4m3x2(r1_), f16x2_of_e4m3x2_hi(r1_)};
+                    const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2_hi(r2_),
+                                            f16x2_of_e4m3x2(r3_), f16x2_of_e4m3x2_hi(r3_)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(oacc[nt][2 * i], a0, pb[nt][0], pb[nt][1]);
+                        mma_f16(oacc[nt][2 * i + 1], a1, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&empty[st]);
+        }
+
+        // ---- end of the piece ----------------------------------------------
+        // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + 2g + (e >> 1)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float &l = l_run[nt][e];
+                l += __shfl_xor_sync(kFull, l, 4);
+                l += __shfl_xor_sync(kFull, l, 8);
+                l += __shfl_xor_sync(kFull, l, 16);
+            }
+        const bool whole = first == last;
+        const size_t slot0 = (size_t)(cta + r) * (HPC * p.n_rep) + (size_t)hw * p.n_rep;
+        if constexpr (C::kWph == 1) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = nt * 8 + 2 * c + e;
+                    if (h >= p.n_rep)
+                        continue;
+                    float l = l_run[nt][e], m = m_run[nt][e];
+                    if (l != l)                  // NaN: kept through the combine
+                        l = 1.f, m = 0.f;
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    if (whole) {
+                        __nv_bfloat16 *o = p.out + (qrow0 + h) * D + 2 * g;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            *reinterpret_cast<uint32_t *>(o + 16 * j) =
+                                pack_bf16x2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
+                    } else {
+                        float *o = p.o_part + (slot0 + h) * D + 2 * g;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            *reinterpret_cast<float2 *>(o + 16 * j) =
+                                make_float2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
+                        if (g == 0)
+                            reinterpret_cast<float2 *>(p.ml_part)[slot0 + h] =
+                                l > 0.f ? make_float2(m * kLn2f, l) : make_float2(-INFINITY, 0.f);
+                    }
+                }
+        } else {
+            // join the head's warps: each leaves its sums, base and weight sum
+            constexpr int NH = NT * 8;
+            float *sums = reinterpret_cast<float *>(smem + C::kJoinOffset);
+            float2 *ml = reinterpret_cast<float2 *>(sums + kWarps * NH * C::kSumPitch);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = nt * 8 + 2 * c + e;
+                    float *o = sums + (warp * NH + h) * C::kSumPitch + 2 * g;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        *reinterpret_cast<float2 *>(o + 16 * j) =
+                            make_float2(oacc[nt][j][e], oacc[nt][j][e + 2]);
+                    if (g == 0)
+                        ml[warp * NH + h] = make_float2(m_run[nt][e], l_run[nt][e]);
+                }
+            named_bar_sync(1, kWarps * 32);
+            // one warp a query head in turn; a lane D / 32 columns
+            constexpr int V = D / 32;
+            for (int i = warp; i < HPC * p.n_rep; i += kWarps) {
+                const int kh = i / p.n_rep, h = i - kh * p.n_rep;
+                float M = -INFINITY, l = 0.f, acc[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    acc[v] = 0.f;
+#pragma unroll
+                for (int w = 0; w < C::kWph; ++w)
+                    M = fmaxf(M, ml[(w * HPC + kh) * NH + h].x);
+                const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int w = 0; w < C::kWph; ++w) {
+                    const int at = (w * HPC + kh) * NH + h;
+                    const float2 x = ml[at];
+                    // (a warp without tokens has base -inf: weight 0)
+                    const float f = exp2f(x.x - base);
+                    l = fmaf(x.y, f, l);
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        acc[v] = fmaf(sums[at * C::kSumPitch + lane + 32 * v], f, acc[v]);
+                }
+                if (l != l)
+                    l = 1.f, M = 0.f;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const size_t qrow = (size_t)b * p.Hq + (size_t)hg * HPC * p.n_rep + i;
+                const size_t slot = (size_t)(cta + r) * (HPC * p.n_rep) + i;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (whole)
+                        p.out[qrow * D + lane + 32 * v] = __float2bfloat16_rn(acc[v] * inv);
+                    else
+                        p.o_part[slot * D + lane + 32 * v] = acc[v] * inv;
+                }
+                if (!whole && lane == 0)
+                    reinterpret_cast<float2 *>(p.ml_part)[slot] =
+                        l > 0.f ? make_float2(M * kLn2f, l) : make_float2(-INFINITY, 0.f);
+            }
+            named_bar_sync(1, kWarps * 32);
+        }
+    }
+    grid_launch_dependents();
+}
+
+template <int D, int HPC, int NT>
+cudaError_t launch(const FusedParams &p, int grid, cudaStream_t stream)
+{
+    using C = Q8Cfg<D, HPC, NT>;
+    static DeviceOnce attrs;
+    cudaError_t e = attrs.run([] {
+        cudaError_t r = cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::kSmemBytes);
+        if (r != cudaSuccess)
+            return r;
+        return cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT>,
+                                    cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared);
+    });
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(decode_q8_kernel<D, HPC, NT>, dim3(grid), dim3(C::kThreads), C::kSmemBytes,
+                      stream, p);
+}
+
+template <int D, int HPC>
+cudaError_t launch_nt(const FusedParams &p, int grid, cudaStream_t stream)
+{
+    return p.n_rep <= 8 ? launch<D, HPC, 1>(p, grid, stream) : launch<D, HPC, 2>(p, grid, stream);
+}
 
 template <int D>
-__global__ void __launch_bounds__(kChunk) decode_q8_kernel(const FusedParams p)
+cudaError_t launch_d(const FusedParams &p, int grid, cudaStream_t stream)
 {
-    __shared__ float s_q[16][D];
-    __shared__ float s_p[16][kChunk];
-    __shared__ float s_m[16], s_l[16], s_a[16];
-    __shared__ long long s_slot[kChunk];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x % p.Hkv, tid = threadIdx.x;
-    const int rep = p.n_rep;
-    int L = p.seq_lens[b];
-    const int pg0 = p.kv_indptr[b], pg1 = p.kv_indptr[b + 1];
-    unsigned bad = 0;
-    if (L < 0 || L > p.max_seq_len) {
-        bad |= kFlagBadLen;
-        L = L < 0 ? 0 : p.max_seq_len;
-    }
-    if (pg0 < 0 || pg1 < pg0 || pg1 > p.num_indices) {
-        bad |= kFlagBadPage;
-        L = 0;
-    } else if ((long long)(pg1 - pg0) * p.page_size < L) {
-        bad |= kFlagBadPage;
-        L = (pg1 - pg0) * p.page_size;
-    }
-    if (bad && kvh == 0 && tid == 0)
-        atomicOr(p.status, bad);
-    const size_t q0 = ((size_t)b * p.Hq + (size_t)kvh * rep) * D;
-    for (int i = tid; i < rep * D; i += kChunk)
-        s_q[i / D][i % D] = __bfloat162float(p.q[q0 + i]) * p.scale_log2;
-    if (tid < 16) {
-        s_m[tid] = -INFINITY;
-        s_l[tid] = 0.f;
-    }
-    const int g = tid / D, col = tid % D;        // PV: column col, tokens g, g + groups
-    constexpr int kGroups = kChunk / D;
-    float acc[16];
-    for (int h = 0; h < 16; ++h)
-        acc[h] = 0.f;
-    __syncthreads();
-    for (int c0 = 0; c0 < L; c0 += kChunk) {
-        const int t = c0 + tid;
-        long long slot = -1;
-        if (t < L) {
-            int page = p.kv_indices[pg0 + t / p.page_size];
-            if (page < 0 || page >= p.num_pages) {
-                atomicOr(p.status, kFlagBadPage);
-                page = 0;
-            }
-            slot = (long long)page * p.page_size + t % p.page_size;
-            const size_t row = (size_t)slot * p.Hkv + kvh;
-            const float f = q8_scale(p.k_scale[row]);
-            const uint32_t *k = reinterpret_cast<const uint32_t *>(p.k_codes + row * D);
-            float s[16];
-            for (int h = 0; h < 16; ++h)
-                s[h] = 0.f;
-            for (int d = 0; d < D / 4; ++d) {
-                const uint32_t w = k[d];
-                const uint32_t a = f16x2_of_e4m3x2(w), c = f16x2_of_e4m3x2_hi(w);
-                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
-                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&c));
-#pragma unroll
-                for (int h = 0; h < 16; ++h)
-                    if (h < rep)
-                        s[h] += x.x * s_q[h][4 * d] + x.y * s_q[h][4 * d + 1] +
-                                y.x * s_q[h][4 * d + 2] + y.y * s_q[h][4 * d + 3];
-            }
-#pragma unroll
-            for (int h = 0; h < 16; ++h)
-                if (h < rep)
-                    s_p[h][tid] = s[h] * f;
-        } else {
-            for (int h = 0; h < rep; ++h)
-                s_p[h][tid] = -INFINITY;
-        }
-        s_slot[tid] = slot;
-        __syncthreads();
-        for (int h = tid / 32; h < rep; h += kChunk / 32) {
-            const int lane = tid % 32;
-            float m = s_m[h];
-            for (int i = lane; i < kChunk; i += 32)
-                m = fmaxf(m, s_p[h][i]);
-            for (int o = 1; o < 32; o <<= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float base = m == -INFINITY ? 0.f : m;
-            float l = 0.f;
-            for (int i = lane; i < kChunk; i += 32) {
-                const float e = exp2f(s_p[h][i] - base);
-                s_p[h][i] = e;
-                l += e;
-            }
-            for (int o = 1; o < 32; o <<= 1)
-                l += __shfl_xor_sync(0xffffffffu, l, o);
-            __syncwarp();
-            if (lane == 0) {
-                const float a = exp2f(s_m[h] - base);
-                s_a[h] = a;
-                s_l[h] = s_l[h] * a + l;
-                s_m[h] = m;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 16; ++h)
-            if (h < rep)
-                acc[h] *= s_a[h];
-        for (int i = g; i < kChunk && c0 + i < L; i += kGroups) {
-            const size_t row = (size_t)s_slot[i] * p.Hkv + kvh;
-            const uint32_t a = f16x2_of_e4m3x2(p.v_codes[row * D + col]);
-            const float v = __low2float(*reinterpret_cast<const __half2 *>(&a)) *
-                            q8_scale(p.v_scale[row]);
-#pragma unroll
-            for (int h = 0; h < 16; ++h)
-                if (h < rep)
-                    acc[h] = fmaf(s_p[h][i], v, acc[h]);
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int h = 0; h < 16; ++h) {
-        if (h >= rep)
-            break;
-        float o = acc[h];
-        if (kGroups > 1) {                // the column's other groups
-            s_p[h][tid] = o;
-            __syncthreads();
-            if (g == 0)
-                for (int k = 1; k < kGroups; ++k)
-                    o += s_p[h][k * D + col];
-        }
-        if (g == 0)
-            p.out[q0 + (size_t)h * D + col] =
-                __float2bfloat16_rn(s_l[h] > 0.f ? o / s_l[h] : 0.f);
+    switch (p.hpc) {
+    case 8:
+        return launch_nt<D, 8>(p, grid, stream);
+    case 4:
+        return launch_nt<D, 4>(p, grid, stream);
+    case 2:
+        return launch_nt<D, 2>(p, grid, stream);
+    default:
+        return launch_nt<D, 1>(p, grid, stream);
     }
 }
 
 } // namespace
 
-cudaError_t launch_decode_q8(const FusedParams &p, int D, int grid, cudaStream_t stream)
+cudaError_t launch_decode_q8(const FusedParams &params, int D, int grid, cudaStream_t stream)
 {
-    (void)grid;
-    const dim3 blocks((unsigned)(p.B * p.Hkv));
-    if (D == 64)
-        return launch_pdl(decode_q8_kernel<64>, blocks, dim3(kChunk), 0, stream, p);
-    return launch_pdl(decode_q8_kernel<128>, blocks, dim3(kChunk), 0, stream, p);
+    FusedParams p = params;
+    p.handoff_wait_ns = handoff_wait_ns();
+    return D == 64 ? launch_d<64>(p, grid, stream) : launch_d<128>(p, grid, stream);
 }
 
 } // namespace pkv

@@ -42,7 +42,7 @@ EXPORTS = (
     "paged_decode_step_planned", "decode_attn_contig_planned", "paged_prefill_attn_ws",
     "pkv_prefill_workspace_bytes", "pkv_prefill_plan", "paged_kv_append_norm",
     "paged_kv_extend_norm", "paged_kv_append_q8", "paged_kv_extend_q8", "paged_kv_read_q8",
-    "paged_decode_attn_q8",
+    "paged_decode_attn_q8", "paged_decode_attn_q8_planned",
 )
 
 
@@ -125,6 +125,7 @@ def lib():
             "paged_kv_extend_q8": (I, [DP, TP, P, I, P, P, P, P, P, P, P, P, P]),
             "paged_kv_read_q8": (I, [DP, P, P, P, P, P, P, P, P, P, P, P]),
             "paged_decode_attn_q8": (I, [DP, P, P, P, P, P, P, P, P, I, P, Z, P, P]),
+            "paged_decode_attn_q8_planned": (I, [DP, P, P, P, P, P, P, P, P, I, P, Z, P, P]),
             "pkv_testing_set_handoff_wait_ns": (I, [ctypes.c_ulonglong]),
             "pkv_status_str": (ctypes.c_char_p, [I]),
             "pkv_version": (I, []),
@@ -459,6 +460,17 @@ def paged_decode_attn_q8(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indi
     """paged_decode_attn over an 8-bit cache."""
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_attn_q8", lib().paged_decode_attn_q8(
+        ctypes.byref(d), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
+        ws_bytes, _ptr(out), _stream(stream)))
+
+
+def paged_decode_attn_q8_planned(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices,
+                                 kv_indptr, seq_lens, num_splits: int, workspace, out,
+                                 stream=None) -> None:
+    """paged_decode_attn_q8 on the workspace's plan (a step's later layers)."""
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check("paged_decode_attn_q8_planned", lib().paged_decode_attn_q8_planned(
         ctypes.byref(d), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
         ws_bytes, _ptr(out), _stream(stream)))
