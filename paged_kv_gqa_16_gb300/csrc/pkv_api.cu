@@ -1126,7 +1126,7 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
     // shared memory, and their weights in 31 bits
     const long long by_weight =
         ((1ll << 31) - 1) / ((long long)dims->max_seq_len + pkv::kFusedRowCost) / groups;
-    const long long by_rows = pkv::kFusedMaxRows / groups;
+    const long long by_rows = pkv::kQ8MaxRows / groups;
     const int most = (int)(by_weight < by_rows ? by_weight : by_rows);
     if (most < 1)
         return PKV_ERR_UNSUPPORTED;

@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <mutex>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -71,6 +72,9 @@ inline cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, size_t smem, cuda
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, p...);
 }
+
+// cuTensorMapEncodeTiled, or nullptr when the driver has none (pkv_prefill.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 struct AppendParams {
     __nv_bfloat16 *q;
@@ -265,6 +269,10 @@ struct FusedParams {
     // (nullptr: nowhere)
     int32_t *plan_out;
 };
+
+// Rows x kv-head groups of one launch over the 8-bit cache (pkv_q8_decode.cu),
+// whose ring of stages needs the room of the other half's prefix sums.
+constexpr int kQ8MaxRows = 2048;
 
 // Threads of a plan block.
 constexpr int kPlanThreads = 256;

@@ -42,7 +42,6 @@
 // Every mbarrier wait is time-bounded; tensor memory is allocated at the
 // start and released on every path.
 #include <cmath>
-#include <cudaTypedefs.h>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -1399,8 +1398,6 @@ cudaError_t launch_prefill_d(const PrefillParams &p, int sms, cudaStream_t strea
 
 } // namespace
 
-namespace {
-
 // cuTensorMapEncodeTiled through the runtime's driver entry point (the
 // library links the runtime only); nullptr when the driver has none.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
@@ -1416,6 +1413,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     }();
     return fn;
 }
+
+namespace {
 
 // A bf16 tensor [rows, mid, D] as the 3-D tiled tensor {D, mid, rows} with
 // a box of {64, box_mid, box_rows}, 128-byte swizzled.

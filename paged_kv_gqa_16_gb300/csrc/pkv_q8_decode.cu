@@ -5,9 +5,9 @@
 // every cached token once and does 4 Hq/Hkv D operations for 2 D + 2 bytes,
 // so it is bound by memory; the work is split over the cache's length as in
 // the bf16 decode (pkv_fused.cu): one persistent block per SM takes an equal
-// range of all rows' tokens laid end to end, a producer warp streams whole
-// token rows (HPC kv heads) into a ring of shared-memory stages, and the
-// piece combine joins the rows that several blocks share.
+// range of all rows' tokens laid end to end, producer warps stream the tokens
+// of HPC kv heads into a ring of shared-memory stages, and the piece combine
+// joins the rows that several blocks share.
 //
 // What the 8-bit cache changes:
 //  - Half the bytes a token means twice the tokens a second, so the tensor
@@ -28,9 +28,19 @@
 //  - M is raised only when some y_t exceeds it by more than 8: a weight is
 //    then at most 2^8 and the usual tile needs no maximum over its lanes and
 //    no rescaling.
-//  - Eight consumer warps whatever the number of kv heads: HPC heads times
-//    WPH = 8 / HPC groups of tokens, each group with sums of its own, joined
-//    through shared memory at the end of a piece.
+//  - A kv head has several warps with sums of their own (parts): WPH = 8 / HPC
+//    take 16 tokens each of every stage, and SETS = 2 sets of eight warps take
+//    the stages in turn, so a warp's chain (products, exponentials, products)
+//    has two stages' time.  The parts are joined in pairs through shared memory
+//    at the end of a piece.
+//  - Copies.  Pages of a multiple of 8 tokens come as TMA boxes of {D bytes,
+//    8 or 16 tokens, HPC heads}, which lie head by head in the stage, swizzled
+//    so that eight tokens' vectors of a head are in different banks: one copy
+//    a page and pool.  (One copy a token, as the bf16 decode makes them, sets
+//    the pace here: 86 us of copies alone for 322 MB, serving batch of 128,
+//    against 47.5 us at the measured copy bandwidth.)  A box may reach over
+//    the piece's ends; those tokens weigh nothing.  Other page sizes take one
+//    copy a token into padded rows.
 #include <cmath>
 
 #include "pkv_partition.cuh"
@@ -40,35 +50,52 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;                 // consumer warps
+constexpr int kSetWarps = 8;              // consumer warps of a set
+constexpr int kProducers = 2;             // producer warps, a stage each in turn
 constexpr float kRaise = 8.f;             // how far a score may exceed its base
 
-template <int D, int HPC, int NT>
+struct Q8Params {
+    FusedParams f;
+    // the pools as {D, tokens, Hkv} bytes with boxes {D, box tokens, HPC}
+    CUtensorMap map_k, map_v;
+    int box_shift;                        // log2 of a box's tokens (TILED)
+};
+
+template <int D, int HPC, int NT, bool TILED>
 struct Q8Cfg {
-    static constexpr int kWph = kWarps / HPC;         // warps of a kv head
+    static constexpr int kSets = NT == 1 ? 2 : 1;
+    static constexpr int kWarps = kSets * kSetWarps;  // consumer warps
+    static constexpr int kWph = kSetWarps / HPC;      // warps of a kv head in a set
+    static constexpr int kParts = kSets * kWph;       // warps of a kv head
     static constexpr int kTok = 16 * kWph;            // tokens of a stage
-    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kRowBytes = HPC * D;         // one token, HPC kv heads
-    // an odd number of 16-byte units: eight tokens' vectors of one head lie in
-    // different banks
-    static constexpr int kPitch = kRowBytes + 16;
-    static constexpr int kCodeBytes = 2 * kTok * kPitch;
-    static constexpr int kScaleBytes = 2 * kTok * 8;  // 8 bytes a token row, K then V
-    static constexpr int kStageBytes = kCodeBytes + kScaleBytes;
-    // join of a head's warps: their sums [warp][NT * 8][D + 4], base and sum
-    static constexpr int kSumPitch = D + 4;
-    static constexpr int kJoinBytes =
-        kWph == 1 ? 0 : kWarps * NT * 8 * (kSumPitch + 2) * 4;
-    static constexpr int kFixedBytes = kJoinBytes + (kFusedMaxRows + 1) * 4 + 16 + 2 * 8 * 8 + 128;
-    static constexpr int kStagesFit = (kSmemLimit - kFixedBytes) / kStageBytes;
-    static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
-    static_assert(kStages >= 2, "ring needs two stages");
-    static constexpr int kJoinOffset = kStages * kStageBytes;
+    // rows: an odd number of 16-byte units, so that eight tokens' vectors of
+    // one head lie in different banks
+    static constexpr int kPitch = TILED ? kRowBytes : kRowBytes + 16;
+    static constexpr int kStageBytes = 2 * kTok * kPitch;
+    static constexpr int kScaleBytes = 2 * kTok * 8;  // 8 bytes a token, K then V
+    // joining parts: half of them leave half of their registers, a slot a warp
+    static constexpr int kJoinFloats = NT * (D / 16 * 2 + 2);
+    static constexpr int kJoinBytes = kParts == 1 ? 0 : kWarps / 2 * kJoinFloats * 32 * 4;
+    static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 16;
+    static constexpr int kStagesFit =
+        (kSmemLimit - kFixedBytes) / (kStageBytes + kScaleBytes + 16);
+    // An even number of stages: a slot then always belongs to the same producer
+    // warp and the same set of consumers.  With an odd one a producer could
+    // reach a slot before the other had filled it for its previous use, and
+    // take the parity of the use before that for its own.
+    static constexpr int kStages = kStagesFit > 10 ? 10 : kStagesFit / 2 * 2;
+    static_assert(kStages >= 4 && kStages % kProducers == 0 && kStages % kSets == 0,
+                  "two slots a set, none shared");
+    static constexpr int kScaleOffset = kStages * kStageBytes;
+    static constexpr int kJoinOffset = kScaleOffset + kStages * kScaleBytes;
     static constexpr int kBarOffset = kJoinOffset + kJoinBytes;
     static constexpr int kAbortOffset = kBarOffset + 2 * kStages * 8;
     static constexpr int kPrefixOffset = kAbortOffset + 16;
-    static constexpr int kSmemBytes = kPrefixOffset + (kFusedMaxRows + 1) * 4;
+    static constexpr int kSmemBytes = kPrefixOffset + (kQ8MaxRows + 1) * 4;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
+    static_assert(!TILED || kStageBytes % 1024 == 0, "swizzled boxes");
     static_assert(kStageBytes % 16 == 0 && kJoinBytes % 16 == 0, "alignment");
 };
 
@@ -119,13 +146,26 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src, int bytes)
                  : "memory");
 }
 
-template <int D, int HPC, int NT>
-__global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
-    decode_q8_kernel(const FusedParams p)
+// Box {D bytes, tokens, heads} at (0, token, head) of a tensor map.
+__device__ __forceinline__ void box_copy_g2s(void *dst, const CUtensorMap *map, int token,
+                                             int head, uint64_t *bar, uint64_t policy)
 {
-    using C = Q8Cfg<D, HPC, NT>;
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(head), "r"(smem_addr(bar)),
+        "l"(policy)
+        : "memory");
+}
+
+template <int D, int HPC, int NT, bool TILED>
+__global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
+    decode_q8_kernel(const __grid_constant__ Q8Params params)
+{
+    using C = Q8Cfg<D, HPC, NT, TILED>;
     constexpr int NST = C::kStages;
-    extern __shared__ __align__(128) unsigned char smem[];
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const FusedParams &p = params.f;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOffset);
     uint64_t *empty = full + NST;
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kAbortOffset);
@@ -135,11 +175,12 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
     const int Bv = p.Bv;
+    const int box = 1 << params.box_shift;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 64);     // every producer lane, and its scale copies
-            mbar_init(&empty[i], kWarps);
+            mbar_init(&empty[i], kSetWarps);
         }
         fence_mbar_init();
         *abort = 0;
@@ -201,14 +242,17 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     }
     const int r0 = first_row(prefix, Bv, start);
 
-    if (warp == kWarps) {
-        // ======================= producer warp ============================
+    if (warp >= C::kWarps) {
+        // ======================= producer warps ===========================
+        // Stage i belongs to warp i % kProducers.  Lanes 0-15 copy K, 16-31 V:
+        // TILED, a box each of the stage's kTok / box; else a token each of 16.
+        const int pw = warp - C::kWarps;
         const uint64_t policy = policy_evict_first();
         const int my_t = lane & 15;
         const bool my_v = lane >= 16;
-        const uint8_t *codes = my_v ? p.v_codes : p.k_codes;
         const uint8_t *scales = my_v ? p.v_scale : p.k_scale;
         const size_t scale_bytes = (size_t)p.num_pages * p.page_size * p.Hkv;
+        constexpr int IDS = TILED ? 1 : C::kWph;      // page ids a lane holds for a stage
         int it = 0;
         bool aborted = false;
         auto page_of_tok = [&](int t) {
@@ -228,13 +272,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
             int npg = p.kv_indptr[b + 1] - pg0;
             if (pg0 < 0 || npg < 0 || pg0 > p.num_indices - npg)
                 npg = 0;                               // a table changed since the plan
-            // page-table window: lane l holds entries wb + l and wb + 32 + l
-            int wb = (page_of_tok(t0) >> 5) << 5;
-            int idx0 = wb + lane < npg ? __ldg(p.kv_indices + pg0 + wb + lane) : 0;
-            int idx1 = wb + 32 + lane < npg ? __ldg(p.kv_indices + pg0 + wb + 32 + lane) : 0;
-            if (plan_e != nullptr && r == r0) {
-                plan_e[8 + lane] = idx0;
-                plan_e[40 + lane] = idx1;
+            if (plan_e != nullptr && r == r0 && pw == 0) {
+                // the bf16 decode's entry holds a 64-entry window of the table
+                const int wb = (page_of_tok(t0) >> 5) << 5;
+                for (int k = lane; k < 64; k += 32)
+                    plan_e[8 + k] = wb + k < npg ? __ldg(p.kv_indices + pg0 + wb + k) : 0;
                 if (lane < 8) {
                     const long long v = lane == 0 ? r0 : lane == 1 ? wb : lane == 2 ? pg0
                                       : lane == 3 ? npg : lane == 4 ? lo : lane == 5 ? hi
@@ -242,11 +284,34 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                     plan_e[lane] = (int)v;
                 }
             }
-            for (int tok = t0; tok < t1; tok += C::kTok, ++it) {
+            const int ta = TILED ? t0 & -box : t0;     // a piece's first stage starts here
+            // the table's entry for this lane's box (token) of the stage at tok
+            auto load_id = [&](int tok, int sub) {
+                const int t = TILED ? tok + (my_t << params.box_shift) : tok + sub * 16 + my_t;
+                const bool there = t < t1 && (!TILED || (my_t << params.box_shift) < C::kTok);
+                const int pi = page_of_tok(there ? t : 0);
+                return there && pi < npg ? __ldg(p.kv_indices + pg0 + pi) : 0;
+            };
+            int ids[IDS];
+            int skip = (pw - it % kProducers + kProducers) % kProducers;   // to its first stage
+#pragma unroll
+            for (int k = 0; k < IDS; ++k)
+                ids[k] = load_id(ta + skip * C::kTok, k);
+            for (int tok = ta; tok < t1; tok += C::kTok, ++it) {
+                if (it % kProducers != pw)
+                    continue;
                 const int st = it % NST;
+                int next[IDS];
+#pragma unroll
+                for (int k = 0; k < IDS; ++k)
+                    next[k] = load_id(tok + kProducers * C::kTok, k);
                 if (it >= NST) {
-                    const bool ok = mbar_wait_or_abort(
-                        &empty[st], (uint32_t)(((it / NST) - 1) & 1), p.handoff_wait_ns, abort);
+                    // (a consumer that gave up releases its stages without having
+                    // waited for them, after it has set the abort word)
+                    const bool ok =
+                        mbar_wait_or_abort(&empty[st], (uint32_t)(((it / NST) - 1) & 1),
+                                           p.handoff_wait_ns, abort) &&
+                        !*abort;
                     if (!__all_sync(kFull, ok)) {
                         aborted = true;
                         if (lane == 0) {
@@ -256,38 +321,56 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                         break;
                     }
                 }
-                fence_proxy_async_smem();
                 unsigned char *stage = smem + st * C::kStageBytes;
+                unsigned char *sc0 = smem + C::kScaleOffset + st * C::kScaleBytes;
                 const int nvalid = min(C::kTok, t1 - tok);
-                if (lane == 0)
-                    mbar_expect_tx(&full[st], (uint32_t)(nvalid * 2 * C::kRowBytes));
-                for (int sub = 0; sub < nvalid; sub += 16) {
-                    const int tb = tok + sub, n16 = min(16, t1 - tb);
-                    if (page_of_tok(tb) >= wb + 32) {       // slide the window by 32
-                        wb += 32;
-                        idx0 = idx1;
-                        idx1 = wb + 32 + lane < npg
-                                   ? __ldg(p.kv_indices + pg0 + wb + 32 + lane) : 0;
-                    }
-                    // every lane joins the shuffles; only lanes with a token use them
-                    const int t = tb + (my_t < n16 ? my_t : 0);
-                    const int pi = page_of_tok(t);
-                    const int sl = t - pi * p.page_size;
-                    const int wofs = pi - wb;                // in [0, 64)
-                    const int e0 = __shfl_sync(kFull, idx0, wofs & 31);
-                    const int e1 = __shfl_sync(kFull, idx1, wofs & 31);
-                    int page = wofs < 32 ? e0 : e1;
-                    const int srow = (my_v ? C::kTok : 0) + sub + my_t;
-                    unsigned char *row = stage + srow * C::kPitch;
-                    if (my_t < n16) {
+                if constexpr (TILED) {
+                    const int boxes = (nvalid + box - 1) >> params.box_shift;
+                    if (lane == 0)
+                        mbar_expect_tx(&full[st],
+                                       (uint32_t)(boxes * box) * (2u * C::kRowBytes));
+                    int page = ids[0];
+                    const int tb = tok + (my_t << params.box_shift);
+                    if (my_t < boxes) {
                         if (page < 0 || page >= p.num_pages) {
                             atomicOr(p.status, kFlagBadPage);
                             page = 0;
                         }
+                        box_copy_g2s(stage + ((my_v ? C::kTok : 0) + (my_t << params.box_shift)) *
+                                                 C::kRowBytes,
+                                     my_v ? &params.map_v : &params.map_k,
+                                     page * p.page_size + (tb - page_of_tok(tb) * p.page_size),
+                                     hg * HPC, &full[st], policy);
+                    }
+                    ids[0] = page;
+                } else {
+                    if (lane == 0)
+                        mbar_expect_tx(&full[st], (uint32_t)(nvalid * 2 * C::kRowBytes));
+                }
+#pragma unroll
+                for (int sub = 0; sub < C::kWph; ++sub) {
+                    if (sub * 16 >= nvalid)
+                        break;
+                    const int row = sub * 16 + my_t, t = tok + row;
+                    const bool there = t < t1;
+                    int page = TILED ? __shfl_sync(kFull, ids[0],
+                                                   (row >> params.box_shift) + (lane & 16))
+                                     : ids[TILED ? 0 : sub];
+                    const int srow = (my_v ? C::kTok : 0) + row;
+                    if (there) {
+                        if (!TILED && (page < 0 || page >= p.num_pages)) {
+                            atomicOr(p.status, kFlagBadPage);
+                            page = 0;
+                        }
                         const size_t head =
-                            ((size_t)page * p.page_size + sl) * (size_t)p.Hkv + (size_t)hg * HPC;
-                        bulk_copy_g2s_hint(row, codes + head * D, C::kRowBytes, &full[st], policy);
-                        unsigned char *sc = stage + C::kCodeBytes + srow * 8;
+                            ((size_t)page * p.page_size + (t - page_of_tok(t) * p.page_size)) *
+                                (size_t)p.Hkv +
+                            (size_t)hg * HPC;
+                        if constexpr (!TILED)
+                            bulk_copy_g2s_hint(stage + srow * C::kPitch,
+                                               (my_v ? p.v_codes : p.k_codes) + head * D,
+                                               C::kRowBytes, &full[st], policy);
+                        unsigned char *sc = sc0 + srow * 8;
                         if constexpr (HPC == 8) {
                             cp_async<8>(sc, scales + head, 8);
                         } else if constexpr (HPC == 4) {
@@ -299,33 +382,45 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                             cp_async<4>(sc, scales + word, left < 4 ? (int)left : 4);
                             sc[4] = (unsigned char)(head & 3);
                         }
-                    } else if (my_v) {
-                        // V rows past the piece's end must be finite (their weight is 0)
-                        uint4 *z = reinterpret_cast<uint4 *>(row);
-                        for (int k = 0; k < C::kRowBytes / 16; ++k)
-                            z[k] = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
                 cp_async_arrive(&full[st]);
                 mbar_arrive(&full[st]);
+#pragma unroll
+                for (int k = 0; k < IDS; ++k)
+                    ids[k] = next[k];
             }
         }
-        // Let the copies already issued land before this warp exits, with the
-        // full time limit: a consumer that gave up skips its stages, and the
-        // block must not exit while a copy into its shared memory is in flight.
+        // Let this warp's copies land before it exits, with the full time
+        // limit: a consumer that gave up skips its stages, and the block must
+        // not exit while a copy into its shared memory is in flight.
         for (int k = (it > NST ? it - NST : 0); k < it; ++k)
-            (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
+            if (k % kProducers == pw)
+                (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
         grid_launch_dependents();
         return;
     }
 
     // ========================= consumer warps ===============================
-    const int hw = warp % HPC, tg = warp / HPC;   // kv head, token group
+    const int set = warp / kSetWarps, hw = warp % HPC, tg = warp % kSetWarps / HPC;
+    const int part = set * C::kWph + tg;
     const int g = lane >> 2, c = lane & 3;
     const uint32_t smem_s = smem_addr(smem);
-    // K: matrices of 8 tokens x 16 bytes: (tokens 0-7, 8-15) x two 16-byte columns
-    const uint32_t k_off = (uint32_t)((tg * 16 + (lane & 15)) * C::kPitch + hw * D + (lane >> 4) * 16);
-    const uint32_t v_off = k_off + C::kTok * C::kPitch;
+    // this lane's row of the matrices of 8 tokens x 16 bytes: token lane % 16
+    // of the warp's 16, 16-byte column lane / 16 of each two
+    uint32_t row_off, swz = 0;
+    {
+        const int t = tg * 16 + (lane & 15);
+        if constexpr (TILED) {
+            const int row = ((((t >> params.box_shift) * HPC + hw) << params.box_shift) |
+                             (t & (box - 1)));
+            row_off = (uint32_t)(row * D);
+            swz = (uint32_t)(D == 128 ? row & 7 : (row >> 1) & 3) << 4;
+        } else {
+            row_off = (uint32_t)(t * C::kPitch + hw * D);
+        }
+    }
+    const uint32_t half_col = (uint32_t)(lane >> 4) * 16;
     int it = 0;
     bool aborted = false;
 
@@ -389,7 +484,9 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                 oacc[nt][j][0] = oacc[nt][j][1] = oacc[nt][j][2] = oacc[nt][j][3] = 0.f;
         }
 
-        for (int tok = t0; tok < t1; tok += C::kTok, ++it) {
+        for (int tok = TILED ? t0 & -box : t0; tok < t1; tok += C::kTok, ++it) {
+            if (it % C::kSets != set)
+                continue;
             const int st = it % NST;
             if (!aborted) {
                 const bool ok = mbar_wait_or_abort(&full[st], (uint32_t)((it / NST) & 1),
@@ -402,16 +499,17 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                     }
                 }
             }
-            const int nvalid = t1 - tok - tg * 16;           // of this warp's 16 tokens
-            if (!aborted && nvalid > 0) {
-                const uint32_t stage_s = smem_s + st * C::kStageBytes;
-                const unsigned char *sc = smem + st * C::kStageBytes + C::kCodeBytes;
+            // tokens [v0, v1) of this warp's 16 belong to the piece
+            const int v0 = t0 - tok - tg * 16, v1 = t1 - tok - tg * 16;
+            if (!aborted && v1 > 0 && v0 < 16) {
+                const uint32_t stage_s = smem_s + st * C::kStageBytes + row_off;
+                const unsigned char *sc = smem + C::kScaleOffset + st * C::kScaleBytes;
 
                 float sacc[NT][2][4] = {};
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t r0_, r1_, r2_, r3_;
-                    ldmatrix_x4(r0_, r1_, r2_, r3_, stage_s + k_off + i * 32);
+                    ldmatrix_x4(r0_, r1_, r2_, r3_, stage_s + ((i * 32 + half_col) ^ swz));
                     const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2(r1_),
                                             f16x2_of_e4m3x2_hi(r0_), f16x2_of_e4m3x2_hi(r1_)};
                     const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2(r3_),
@@ -426,11 +524,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                 float fk[2], ev[2], inv_v[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int row = tg * 16 + g + u * 8;
-                    const unsigned char *sk = sc + row * 8, *sv = sk + C::kTok * 8;
+                    const int t = g + u * 8;
+                    const unsigned char *sk = sc + (tg * 16 + t) * 8, *sv = sk + C::kTok * 8;
                     const unsigned bk = HPC >= 4 ? sk[hw] : sk[(sk[4] & 3) + hw];
                     const unsigned bv = HPC >= 4 ? sv[hw] : sv[(sv[4] & 3) + hw];
-                    const bool in = g + u * 8 < nvalid;
+                    const bool in = t >= v0 && t < v1;
                     fk[u] = q8_scale(bk);
                     ev[u] = in ? (float)((int)bv - 127) : -INFINITY;
                     inv_v[u] = in ? __uint_as_float((254u - bv) << 23) : 0.f;
@@ -442,7 +540,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float x = (sacc[nt][0][e] + sacc[nt][1][e]) * (fk[e >> 1] * cq[nt][e & 1]);
-                        // (a token past the end: whatever its row held)
+                        // (a token of no piece: whatever its row held)
                         y[nt][e] = ev[e >> 1] == -INFINITY ? -INFINITY : x + ev[e >> 1];
                         raise |= y[nt][e] > m_run[nt][e & 1] + kRaise;
                     }
@@ -483,15 +581,26 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                 }
                 // V^T: a transposed 8-token x 16-byte matrix gives lane (g, c) the codes
                 // (t, d), (t, d+1), (t+1, d), (t+1, d+1) of t = 2c, d = 2g: swapping the
-                // middle two leaves the token pairs of column d and of column d + 1
+                // middle two leaves the token pairs of column d and of column d + 1.
+                // Tokens outside the piece are replaced by zeros (selector 4).
+                unsigned sel0 = 0x3120, sel1 = 0x3120;
+                if (v0 > 0 || v1 < 16) {
+                    auto selector = [&](int t) {
+                        return (t >= v0 && t < v1 ? 0x0100u : 0x0404u) |
+                               (t + 1 >= v0 && t + 1 < v1 ? 0x3020u : 0x4040u);
+                    };
+                    sel0 = selector(2 * c);
+                    sel1 = selector(2 * c + 8);
+                }
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t r0_, r1_, r2_, r3_;
-                    ldmatrix_x4_trans(r0_, r1_, r2_, r3_, stage_s + v_off + i * 32);
-                    r0_ = __byte_perm(r0_, 0, 0x3120);
-                    r1_ = __byte_perm(r1_, 0, 0x3120);
-                    r2_ = __byte_perm(r2_, 0, 0x3120);
-                    r3_ = __byte_perm(r3_, 0, 0x3120);
+                    ldmatrix_x4_trans(r0_, r1_, r2_, r3_,
+                                      stage_s + C::kTok * C::kPitch + ((i * 32 + half_col) ^ swz));
+                    r0_ = __byte_perm(r0_, 0, sel0);
+                    r1_ = __byte_perm(r1_, 0, sel1);
+                    r2_ = __byte_perm(r2_, 0, sel0);
+                    r3_ = __byte_perm(r3_, 0, sel1);
                     const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2_hi(r0_),
                                             f16x2_of_e4m3x2(r1_), f16x2_of_e4m3x2_hi(r1_)};
                     const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2_hi(r2_),
@@ -508,151 +617,161 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                 mbar_arrive(&empty[st]);
         }
 
-        // ---- end of the piece ----------------------------------------------
+        // ---- end of the piece: join the head's parts in pairs -----------------
+        if constexpr (C::kParts > 1) {
+            float *slots = reinterpret_cast<float *>(smem + C::kJoinOffset) + lane;
+#pragma unroll
+            for (int s = C::kParts / 2; s >= 1; s >>= 1)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {              // heads 2c, then 2c + 1
+                    if (part >= s && part < 2 * s) {
+                        float *to = slots + ((part - s) * HPC + hw) * (C::kJoinFloats * 32);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            *to = m_run[nt][e], to += 32;
+                            *to = l_run[nt][e], to += 32;
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                *to = oacc[nt][j][e], to += 32;
+                                *to = oacc[nt][j][e + 2], to += 32;
+                            }
+                        }
+                    }
+                    named_bar_sync(1, C::kWarps * 32);
+                    if (part < s) {
+                        const float *from = slots + (part * HPC + hw) * (C::kJoinFloats * 32);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float m = *from;
+                            const float mn = fmaxf(m_run[nt][e], m);
+                            const float base = mn == -INFINITY ? 0.f : mn;
+                            const float fa = exp2f(m_run[nt][e] - base), fb = exp2f(m - base);
+                            m_run[nt][e] = mn;
+                            l_run[nt][e] = l_run[nt][e] * fa + from[32] * fb;
+                            from += 64;
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                oacc[nt][j][e] = oacc[nt][j][e] * fa + *from * fb;
+                                oacc[nt][j][e + 2] = oacc[nt][j][e + 2] * fa + from[32] * fb;
+                                from += 64;
+                            }
+                        }
+                    }
+                    named_bar_sync(1, C::kWarps * 32);
+                }
+        }
+        if (part != 0)
+            continue;
         // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + 2g + (e >> 1)
+        const bool whole = first == last;
+        const size_t slot0 = (size_t)(cta + r) * (HPC * p.n_rep) + (size_t)hw * p.n_rep;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float &l = l_run[nt][e];
+                float l = l_run[nt][e], m = m_run[nt][e];
                 l += __shfl_xor_sync(kFull, l, 4);
                 l += __shfl_xor_sync(kFull, l, 8);
                 l += __shfl_xor_sync(kFull, l, 16);
-            }
-        const bool whole = first == last;
-        const size_t slot0 = (size_t)(cta + r) * (HPC * p.n_rep) + (size_t)hw * p.n_rep;
-        if constexpr (C::kWph == 1) {
+                const int h = nt * 8 + 2 * c + e;
+                if (h >= p.n_rep)
+                    continue;
+                if (l != l)                  // NaN: kept through the combine
+                    l = 1.f, m = 0.f;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                if (whole) {
+                    __nv_bfloat16 *o = p.out + (qrow0 + h) * D + 2 * g;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int h = nt * 8 + 2 * c + e;
-                    if (h >= p.n_rep)
-                        continue;
-                    float l = l_run[nt][e], m = m_run[nt][e];
-                    if (l != l)                  // NaN: kept through the combine
-                        l = 1.f, m = 0.f;
-                    const float inv = l > 0.f ? 1.f / l : 0.f;
-                    if (whole) {
-                        __nv_bfloat16 *o = p.out + (qrow0 + h) * D + 2 * g;
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            *reinterpret_cast<uint32_t *>(o + 16 * j) =
-                                pack_bf16x2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
-                    } else {
-                        float *o = p.o_part + (slot0 + h) * D + 2 * g;
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            *reinterpret_cast<float2 *>(o + 16 * j) =
-                                make_float2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
-                        if (g == 0)
-                            reinterpret_cast<float2 *>(p.ml_part)[slot0 + h] =
-                                l > 0.f ? make_float2(m * kLn2f, l) : make_float2(-INFINITY, 0.f);
-                    }
-                }
-        } else {
-            // join the head's warps: each leaves its sums, base and weight sum
-            constexpr int NH = NT * 8;
-            float *sums = reinterpret_cast<float *>(smem + C::kJoinOffset);
-            float2 *ml = reinterpret_cast<float2 *>(sums + kWarps * NH * C::kSumPitch);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int h = nt * 8 + 2 * c + e;
-                    float *o = sums + (warp * NH + h) * C::kSumPitch + 2 * g;
+                    for (int j = 0; j < D / 16; ++j)
+                        *reinterpret_cast<uint32_t *>(o + 16 * j) =
+                            pack_bf16x2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
+                } else {
+                    float *o = p.o_part + (slot0 + h) * D + 2 * g;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j)
                         *reinterpret_cast<float2 *>(o + 16 * j) =
-                            make_float2(oacc[nt][j][e], oacc[nt][j][e + 2]);
+                            make_float2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
                     if (g == 0)
-                        ml[warp * NH + h] = make_float2(m_run[nt][e], l_run[nt][e]);
+                        reinterpret_cast<float2 *>(p.ml_part)[slot0 + h] =
+                            l > 0.f ? make_float2(m * kLn2f, l) : make_float2(-INFINITY, 0.f);
                 }
-            named_bar_sync(1, kWarps * 32);
-            // one warp a query head in turn; a lane D / 32 columns
-            constexpr int V = D / 32;
-            for (int i = warp; i < HPC * p.n_rep; i += kWarps) {
-                const int kh = i / p.n_rep, h = i - kh * p.n_rep;
-                float M = -INFINITY, l = 0.f, acc[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    acc[v] = 0.f;
-#pragma unroll
-                for (int w = 0; w < C::kWph; ++w)
-                    M = fmaxf(M, ml[(w * HPC + kh) * NH + h].x);
-                const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                for (int w = 0; w < C::kWph; ++w) {
-                    const int at = (w * HPC + kh) * NH + h;
-                    const float2 x = ml[at];
-                    // (a warp without tokens has base -inf: weight 0)
-                    const float f = exp2f(x.x - base);
-                    l = fmaf(x.y, f, l);
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        acc[v] = fmaf(sums[at * C::kSumPitch + lane + 32 * v], f, acc[v]);
-                }
-                if (l != l)
-                    l = 1.f, M = 0.f;
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                const size_t qrow = (size_t)b * p.Hq + (size_t)hg * HPC * p.n_rep + i;
-                const size_t slot = (size_t)(cta + r) * (HPC * p.n_rep) + i;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (whole)
-                        p.out[qrow * D + lane + 32 * v] = __float2bfloat16_rn(acc[v] * inv);
-                    else
-                        p.o_part[slot * D + lane + 32 * v] = acc[v] * inv;
-                }
-                if (!whole && lane == 0)
-                    reinterpret_cast<float2 *>(p.ml_part)[slot] =
-                        l > 0.f ? make_float2(M * kLn2f, l) : make_float2(-INFINITY, 0.f);
             }
-            named_bar_sync(1, kWarps * 32);
-        }
     }
     grid_launch_dependents();
 }
 
-template <int D, int HPC, int NT>
-cudaError_t launch(const FusedParams &p, int grid, cudaStream_t stream)
+template <int D, int HPC, int NT, bool TILED>
+cudaError_t launch(const Q8Params &p, int grid, cudaStream_t stream)
 {
-    using C = Q8Cfg<D, HPC, NT>;
+    using C = Q8Cfg<D, HPC, NT, TILED>;
     static DeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        cudaError_t r = cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT>,
+        cudaError_t r = cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, TILED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemBytes);
         if (r != cudaSuccess)
             return r;
-        return cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT>,
+        return cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, TILED>,
                                     cudaFuncAttributePreferredSharedMemoryCarveout,
                                     cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(decode_q8_kernel<D, HPC, NT>, dim3(grid), dim3(C::kThreads), C::kSmemBytes,
-                      stream, p);
+    return launch_pdl(decode_q8_kernel<D, HPC, NT, TILED>, dim3(grid), dim3(C::kThreads),
+                      C::kSmemBytes, stream, p);
+}
+
+// Boxes of 16 tokens (8 where a page is not a multiple of 16) if the pages
+// hold whole boxes and a token's index fits the copy's 32-bit coordinate.
+template <int D>
+bool box_maps(Q8Params &q)
+{
+    const FusedParams &p = q.f;
+    const long long tokens = (long long)p.num_pages * p.page_size;
+    if (p.page_size % 8 != 0 || tokens >= (1ll << 31))
+        return false;
+    q.box_shift = p.page_size % 16 == 0 ? 4 : 3;
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr)
+        return false;
+    const cuuint64_t dims[3] = {D, (cuuint64_t)tokens, (cuuint64_t)p.Hkv};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.Hkv * D, D};
+    const cuuint32_t box[3] = {D, 1u << q.box_shift, (cuuint32_t)p.hpc};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    for (int v = 0; v < 2; ++v)
+        if (encode(v ? &q.map_v : &q.map_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                   const_cast<uint8_t *>(v ? p.v_codes : p.k_codes), dims, strides, box, steps,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
 }
 
 template <int D, int HPC>
-cudaError_t launch_nt(const FusedParams &p, int grid, cudaStream_t stream)
+cudaError_t launch_nt(Q8Params &q, int grid, cudaStream_t stream)
 {
-    return p.n_rep <= 8 ? launch<D, HPC, 1>(p, grid, stream) : launch<D, HPC, 2>(p, grid, stream);
+    const bool tiled = box_maps<D>(q);
+    if (q.f.n_rep <= 8)
+        return tiled ? launch<D, HPC, 1, true>(q, grid, stream)
+                     : launch<D, HPC, 1, false>(q, grid, stream);
+    return tiled ? launch<D, HPC, 2, true>(q, grid, stream)
+                 : launch<D, HPC, 2, false>(q, grid, stream);
 }
 
 template <int D>
-cudaError_t launch_d(const FusedParams &p, int grid, cudaStream_t stream)
+cudaError_t launch_d(Q8Params &q, int grid, cudaStream_t stream)
 {
-    switch (p.hpc) {
+    switch (q.f.hpc) {
     case 8:
-        return launch_nt<D, 8>(p, grid, stream);
+        return launch_nt<D, 8>(q, grid, stream);
     case 4:
-        return launch_nt<D, 4>(p, grid, stream);
+        return launch_nt<D, 4>(q, grid, stream);
     case 2:
-        return launch_nt<D, 2>(p, grid, stream);
+        return launch_nt<D, 2>(q, grid, stream);
     default:
-        return launch_nt<D, 1>(p, grid, stream);
+        return launch_nt<D, 1>(q, grid, stream);
     }
 }
 
@@ -660,9 +779,10 @@ cudaError_t launch_d(const FusedParams &p, int grid, cudaStream_t stream)
 
 cudaError_t launch_decode_q8(const FusedParams &params, int D, int grid, cudaStream_t stream)
 {
-    FusedParams p = params;
-    p.handoff_wait_ns = handoff_wait_ns();
-    return D == 64 ? launch_d<64>(p, grid, stream) : launch_d<128>(p, grid, stream);
+    Q8Params q{};
+    q.f = params;
+    q.f.handoff_wait_ns = handoff_wait_ns();
+    return D == 64 ? launch_d<64>(q, grid, stream) : launch_d<128>(q, grid, stream);
 }
 
 } // namespace pkv
