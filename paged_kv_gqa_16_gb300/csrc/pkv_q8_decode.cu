@@ -16,23 +16,30 @@
 //    eight columns, which a group of 8 heads fills and a group of 4 fills
 //    half -- half the products and half the accumulators of heads as rows.
 //    NT = 2 column tiles serve groups of 9 to 16 heads.
-//  - Codes become f16 exactly (one cvt for two codes).  q is scaled by a
-//    power of two to at most 2 in size, which keeps its eight significant
-//    bits in f16; that power and the softmax scale go into the score's
-//    factor in fp32.
+//  - The products take the codes as they are (e4m3 x e4m3, m16n8k32, fp32
+//    sums): no conversion, and a quarter of the tensor time of f16 products
+//    (measured: 4.2 against 8 cycles an instruction, of twice the depth).
+//    The other operands are split in two codes each.  q, scaled by a power of
+//    two to a largest value in [128, 256), is hi + lo / 32: hi keeps four of
+//    bf16's eight significant bits, lo the other four (down to 2^-14 of the
+//    largest value, 2^-22 of it below), and their products have sums of their
+//    own.  A weight w is hi + lo, eight significant bits as a bf16 weight
+//    would have (in steps of 2^-9 at least, the largest weight being 2^7 or
+//    more): hi takes the first 16 of the 32 places of depth, lo the others,
+//    against the same 16 tokens of V twice.
 //  - Both scales act on the scores: x_t = 2^ek_t (s_t c) and y_t = x_t + ev_t
-//    in the log2 domain.  The weights used for O are 2^(y_t - M), M following
-//    the largest y_t, so they are in f16's range however the values' scales
-//    differ; the sum of softmax weights takes each of them times 2^-ev_t (a
-//    power of two, exact).  Both sums carry the same 2^-M.
-//  - M is raised only when some y_t exceeds it by more than 8: a weight is
-//    then at most 2^8 and the usual tile needs no maximum over its lanes and
+//    in the log2 domain.  The weights used for O are 2^(y_t - base), base
+//    following the largest y_t, so they are in e4m3's range however the
+//    values' scales differ; the sum of softmax weights takes each of them, in
+//    fp32, times 2^-ev_t (a power of two, exact).  Both sums carry 2^-base.
+//  - base is 7 under the largest y_t of the time it was set and is raised when
+//    some y_t exceeds it by more than 8.5 (a weight is then at most 2^8.5, the
+//    format ends at 448): the usual tile needs no maximum over its lanes and
 //    no rescaling.
-//  - A kv head has several warps with sums of their own (parts): WPH = 8 / HPC
-//    take 16 tokens each of every stage, and SETS = 2 sets of eight warps take
-//    the stages in turn, so a warp's chain (products, exponentials, products)
-//    has two stages' time.  The parts are joined in pairs through shared memory
-//    at the end of a piece.
+//  - A kv head has WPH = 8 / HPC warps, which take 16 tokens each of every
+//    stage and have sums of their own, joined in pairs through shared memory at
+//    the end of a piece.  A warp takes two stages at a time: the products and
+//    exponentials of one overlap those of the other.
 //  - Copies.  Pages of a multiple of 8 tokens come as TMA boxes of {D bytes,
 //    8 or 16 tokens, HPC heads}, which lie head by head in the stage, swizzled
 //    so that eight tokens' vectors of a head are in different banks: one copy
@@ -50,9 +57,10 @@ namespace pkv {
 
 namespace {
 
-constexpr int kSetWarps = 8;              // consumer warps of a set
+constexpr int kWarps = 8;                 // consumer warps
 constexpr int kProducers = 2;             // producer warps, a stage each in turn
-constexpr float kRaise = 8.f;             // how far a score may exceed its base
+constexpr float kRoom = 7.f;              // a base is this far under the largest score
+constexpr float kRaise = 8.5f;            // and is raised when one exceeds it by more
 
 struct Q8Params {
     FusedParams f;
@@ -63,11 +71,11 @@ struct Q8Params {
 
 template <int D, int HPC, int NT, bool TILED>
 struct Q8Cfg {
-    static constexpr int kSets = NT == 1 ? 2 : 1;
-    static constexpr int kWarps = kSets * kSetWarps;  // consumer warps
-    static constexpr int kWph = kSetWarps / HPC;      // warps of a kv head in a set
-    static constexpr int kParts = kSets * kWph;       // warps of a kv head
+    static constexpr int kWph = kWarps / HPC;         // warps of a kv head
     static constexpr int kTok = 16 * kWph;            // tokens of a stage
+    // stages a warp takes at a time: two chains of products and exponentials
+    // to overlap, where the registers allow it
+    static constexpr int kTake = NT == 1 ? 2 : 1;
     static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kRowBytes = HPC * D;         // one token, HPC kv heads
     // rows: an odd number of 16-byte units, so that eight tokens' vectors of
@@ -77,17 +85,16 @@ struct Q8Cfg {
     static constexpr int kScaleBytes = 2 * kTok * 8;  // 8 bytes a token, K then V
     // joining parts: half of them leave half of their registers, a slot a warp
     static constexpr int kJoinFloats = NT * (D / 16 * 2 + 2);
-    static constexpr int kJoinBytes = kParts == 1 ? 0 : kWarps / 2 * kJoinFloats * 32 * 4;
+    static constexpr int kJoinBytes = kWph == 1 ? 0 : kWarps / 2 * kJoinFloats * 32 * 4;
     static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 16;
     static constexpr int kStagesFit =
         (kSmemLimit - kFixedBytes) / (kStageBytes + kScaleBytes + 16);
     // An even number of stages: a slot then always belongs to the same producer
-    // warp and the same set of consumers.  With an odd one a producer could
-    // reach a slot before the other had filled it for its previous use, and
-    // take the parity of the use before that for its own.
+    // warp.  With an odd one a producer could reach a slot before the other had
+    // filled it for its previous use, and take the parity of the use before
+    // that for its own.
     static constexpr int kStages = kStagesFit > 10 ? 10 : kStagesFit / 2 * 2;
-    static_assert(kStages >= 4 && kStages % kProducers == 0 && kStages % kSets == 0,
-                  "two slots a set, none shared");
+    static_assert(kStages >= 4 && kStages % kProducers == 0, "a slot has one producer");
     static constexpr int kScaleOffset = kStages * kStageBytes;
     static constexpr int kJoinOffset = kScaleOffset + kStages * kScaleBytes;
     static constexpr int kBarOffset = kJoinOffset + kJoinBytes;
@@ -99,20 +106,48 @@ struct Q8Cfg {
     static_assert(kStageBytes % 16 == 0 && kJoinBytes % 16 == 0, "alignment");
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1)
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
                  "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two floats to f16x2, the first in the low half.
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+// Two transposed matrices of 16 rows x 16 bytes: row r of a matrix is at the
+// address of lane r (the second's: of lane 16 + r), and lane (g, c) gets its
+// columns g (r0; r2) and g + 8 (r1; r3), rows 4c .. 4c + 3.
+__device__ __forceinline__ void ldmatrix_trans_b8(uint32_t &r0, uint32_t &r1, uint32_t &r2,
+                                                  uint32_t &r3, uint32_t addr)
 {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ float exp2_ftz(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two values as codes hi (their nearest) and lo (of what hi leaves):
+// bytes (hi of a, lo of a, hi of b, lo of b).
+__device__ __forceinline__ uint32_t split_pair(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
+    uint16_t hi, lo;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(w));
+    const uint32_t back = f16x2_of_e4m3x2(hi);
+    const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2 *>(&back));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+        : "=h"(lo)
+        : "r"(*reinterpret_cast<const uint32_t *>(&rest)));
+    return __byte_perm(hi, lo, 0x5140);
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
@@ -180,7 +215,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 64);     // every producer lane, and its scale copies
-            mbar_init(&empty[i], kSetWarps);
+            mbar_init(&empty[i], kWarps);
         }
         fence_mbar_init();
         *abort = 0;
@@ -233,8 +268,9 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
         }
     }
     const unsigned t_q = T / Gu, t_r = T % Gu;
-    const long long start = (long long)t_q * cta + t_r * (unsigned)cta / Gu;
-    const long long end = (long long)t_q * (cta + 1) + t_r * (unsigned)(cta + 1) / Gu;
+    // (T < 2^31)
+    const int start = (int)(t_q * cta + t_r * (unsigned)cta / Gu);
+    const int end = (int)(t_q * (cta + 1) + t_r * (unsigned)(cta + 1) / Gu);
     if (cta >= G || start >= end) {
         if (plan_e != nullptr && threadIdx.x == 0)
             plan_e[0] = -1;
@@ -242,11 +278,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
     }
     const int r0 = first_row(prefix, Bv, start);
 
-    if (warp >= C::kWarps) {
+    if (warp >= kWarps) {
         // ======================= producer warps ===========================
         // Stage i belongs to warp i % kProducers.  Lanes 0-15 copy K, 16-31 V:
         // TILED, a box each of the stage's kTok / box; else a token each of 16.
-        const int pw = warp - C::kWarps;
+        const int pw = warp - kWarps;
         const uint64_t policy = policy_evict_first();
         const int my_t = lane & 15;
         const bool my_v = lane >= 16;
@@ -260,13 +296,12 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
         };
         for (int r = r0; r < Bv && !aborted; ++r) {
             // [lo, hi): the positions of the row's tokens
-            const long long lo = (long long)prefix[r] + p.row_cost, hi = prefix[r + 1];
+            const int lo = prefix[r] + p.row_cost, hi = prefix[r + 1];
             if (lo >= end)
                 break;
             if (hi == prefix[r])
                 continue;
-            const int t0 = (int)((start > lo ? start : lo) - lo);
-            const int t1 = (int)((end < hi ? end : hi) - lo);
+            const int t0 = max(start, lo) - lo, t1 = min(end, hi) - lo;
             const int b = r % p.B, hg = r / p.B;
             const int pg0 = p.kv_indptr[b];
             int npg = p.kv_indptr[b + 1] - pg0;
@@ -278,10 +313,9 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                 for (int k = lane; k < 64; k += 32)
                     plan_e[8 + k] = wb + k < npg ? __ldg(p.kv_indices + pg0 + wb + k) : 0;
                 if (lane < 8) {
-                    const long long v = lane == 0 ? r0 : lane == 1 ? wb : lane == 2 ? pg0
-                                      : lane == 3 ? npg : lane == 4 ? lo : lane == 5 ? hi
-                                      : lane == 6 ? start : end;
-                    plan_e[lane] = (int)v;
+                    plan_e[lane] = lane == 0 ? r0 : lane == 1 ? wb : lane == 2 ? pg0
+                                 : lane == 3 ? npg : lane == 4 ? lo : lane == 5 ? hi
+                                 : lane == 6 ? start : end;
                 }
             }
             const int ta = TILED ? t0 & -box : t0;     // a piece's first stage starts here
@@ -402,48 +436,51 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
     }
 
     // ========================= consumer warps ===============================
-    const int set = warp / kSetWarps, hw = warp % HPC, tg = warp % kSetWarps / HPC;
-    const int part = set * C::kWph + tg;
+    const int hw = warp % HPC, tg = warp / HPC;   // kv head, its part
     const int g = lane >> 2, c = lane & 3;
     const uint32_t smem_s = smem_addr(smem);
-    // this lane's row of the matrices of 8 tokens x 16 bytes: token lane % 16
-    // of the warp's 16, 16-byte column lane / 16 of each two
-    uint32_t row_off, swz = 0;
-    {
-        const int t = tg * 16 + (lane & 15);
+    // Matrix loads: lane l addresses token l % 16 of the warp's 16 and the
+    // 16-byte column l / 16 of each two.  For V the tokens are in the order in
+    // which the weights' operand has them: 2c, 2c + 1, 2c + 8, 2c + 9 of c = 0..3.
+    auto token_addr = [&](int t) {
+        const uint32_t col = (uint32_t)(lane >> 4) * 16;
         if constexpr (TILED) {
             const int row = ((((t >> params.box_shift) * HPC + hw) << params.box_shift) |
                              (t & (box - 1)));
-            row_off = (uint32_t)(row * D);
-            swz = (uint32_t)(D == 128 ? row & 7 : (row >> 1) & 3) << 4;
+            return (uint32_t)(row * D) + (col ^ (uint32_t)(D == 128 ? row & 7 : (row >> 1) & 3) << 4);
         } else {
-            row_off = (uint32_t)(t * C::kPitch + hw * D);
+            return (uint32_t)(t * C::kPitch + hw * D) + col;
         }
-    }
-    const uint32_t half_col = (uint32_t)(lane >> 4) * 16;
+    };
+    // the 32-byte column i of a row whose first is at `addr` (TILED: the
+    // swizzle is in the same bits)
+    auto column = [](uint32_t addr, int i) { return TILED ? addr ^ (i * 32u) : addr + i * 32u; };
+    // The products' rows 8-15 are tokens 12-15, 8-11: with that both K's loads
+    // (rows) and V's (places of depth, 4c + i: rows 2c, 2c + 1, 2c + 8, 2c + 9)
+    // take eight tokens at a time that differ modulo 8, in different banks.
+    auto token_of_row = [](int m) { return m < 8 ? m : m ^ 4; };
+    const int l16 = lane & 15;
+    const uint32_t k_off = smem_s + token_addr(tg * 16 + token_of_row(l16));
+    const uint32_t v_off =
+        smem_s + C::kTok * C::kPitch +
+        token_addr(tg * 16 +
+                   token_of_row(2 * (l16 >> 2) + (l16 & 1) + ((l16 & 2) ? 8 : 0)));
     int it = 0;
     bool aborted = false;
 
     for (int r = r0; r < Bv; ++r) {
-        const long long lo = (long long)prefix[r] + p.row_cost, hi = prefix[r + 1];
+        const int lo = prefix[r] + p.row_cost, hi = prefix[r + 1];
         if (lo >= end)
             break;
         if (hi == prefix[r])
             continue;
-        const int t0 = (int)((start > lo ? start : lo) - lo);
-        const int t1 = (int)((end < hi ? end : hi) - lo);
+        const int t0 = max(start, lo) - lo, t1 = min(end, hi) - lo;
         const int b = r % p.B, hg = r / p.B;
         const size_t qrow0 = (size_t)b * p.Hq + (size_t)(hg * HPC + hw) * p.n_rep;
-        const int first = block_of(lo, T, G);
-        const int last = block_of(hi - 1, T, G);
-        if (t0 == 0 && warp == 0 && lane == 0 && !planned) {
-            p.row_info[2 * r] = first;
-            p.row_info[2 * r + 1] = last - first + 1;
-        }
 
         // q as the products' B operand: lane (g, c) holds elements 4c .. 4c + 3
-        // of each 16 of head g, the order in which a K word's four codes come
-        uint32_t qf[NT][D / 16][2];
+        // of each 16 of head g, as codes hi and lo
+        uint32_t qh[NT][D / 16], ql[NT][D / 16];
         float cq[NT][2];                   // factors of heads 2c, 2c + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -460,15 +497,26 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
             }
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-            // 2^-n, n the exponent of amax, both powers kept in the normal range
-            const int n = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
-            const float down = __uint_as_float((unsigned)(127 - n) << 23);
+            // 2^(7 - n), n the exponent of amax, both powers kept in the normal range
+            const int n = max((int)(__float_as_uint(amax) >> 23) - 127, -119);
+            const float down = __uint_as_float((unsigned)(134 - n) << 23);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                qf[nt][j][0] = pack_f16x2(bf16_lo(raw[j].x) * down, bf16_hi(raw[j].x) * down);
-                qf[nt][j][1] = pack_f16x2(bf16_lo(raw[j].y) * down, bf16_hi(raw[j].y) * down);
+                const float x[4] = {bf16_lo(raw[j].x), bf16_hi(raw[j].x), bf16_lo(raw[j].y),
+                                    bf16_hi(raw[j].y)};
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)        // (an infinite element becomes NaN)
+                    y[i] = fabsf(x[i]) == INFINITY ? __uint_as_float(0x7fffffffu) : x[i] * down;
+                qh[nt][j] = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
+                const uint32_t h01 = f16x2_of_e4m3x2(qh[nt][j]);
+                const uint32_t h23 = f16x2_of_e4m3x2_hi(qh[nt][j]);
+                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h01));
+                const float2 b2 = __half22float2(*reinterpret_cast<const __half2 *>(&h23));
+                ql[nt][j] = e4m3x2((y[0] - a.x) * 32.f, (y[1] - a.y) * 32.f) |
+                            (e4m3x2((y[2] - b2.x) * 32.f, (y[3] - b2.y) * 32.f) << 16);
             }
-            const float up = __uint_as_float((unsigned)(127 + n) << 23) * p.scale_log2;
+            const float up = __uint_as_float((unsigned)(120 + n) << 23) * p.scale_log2;
             cq[nt][0] = __shfl_sync(kFull, up, (2 * c) * 4);
             cq[nt][1] = __shfl_sync(kFull, up, (2 * c + 1) * 4);
         }
@@ -484,77 +532,120 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                 oacc[nt][j][0] = oacc[nt][j][1] = oacc[nt][j][2] = oacc[nt][j][3] = 0.f;
         }
 
-        for (int tok = TILED ? t0 & -box : t0; tok < t1; tok += C::kTok, ++it) {
-            if (it % C::kSets != set)
-                continue;
-            const int st = it % NST;
-            if (!aborted) {
-                const bool ok = mbar_wait_or_abort(&full[st], (uint32_t)((it / NST) & 1),
-                                                   p.handoff_wait_ns, abort);
-                if (!__all_sync(kFull, ok)) {
-                    aborted = true;
-                    if (lane == 0) {
-                        *abort = 1;
-                        atomicOr(p.status, kFlagTimeout);
+        for (int tok = TILED ? t0 & -box : t0; tok < t1;) {
+            constexpr int U = C::kTake;
+            // this turn's stages: U, or one before the piece's end
+            const int take = U == 2 && tok + C::kTok < t1 ? 2 : 1;
+            uint32_t stage[U];
+            const unsigned char *sc[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int st = (it + u) % NST;
+                stage[u] = (uint32_t)st * C::kStageBytes;
+                sc[u] = smem + C::kScaleOffset + st * C::kScaleBytes + tg * 16 * 8;
+                if (!aborted && u < take) {
+                    const bool ok = mbar_wait_or_abort(&full[st], (uint32_t)(((it + u) / NST) & 1),
+                                                       p.handoff_wait_ns, abort);
+                    if (!__all_sync(kFull, ok)) {
+                        aborted = true;
+                        if (lane == 0) {
+                            *abort = 1;
+                            atomicOr(p.status, kFlagTimeout);
+                        }
                     }
                 }
             }
-            // tokens [v0, v1) of this warp's 16 belong to the piece
+            // tokens [v0, v1) of this warp's 16 of the first stage belong to the
+            // piece, [v0, v1) - kTok of the second (none of a stage not taken)
             const int v0 = t0 - tok - tg * 16, v1 = t1 - tok - tg * 16;
-            if (!aborted && v1 > 0 && v0 < 16) {
-                const uint32_t stage_s = smem_s + st * C::kStageBytes + row_off;
-                const unsigned char *sc = smem + C::kScaleOffset + st * C::kScaleBytes;
-
-                float sacc[NT][2][4] = {};
+            if (!aborted && v1 > 0 && v0 < 16 + (U - 1) * C::kTok) {
+                // S^T = K q: one sum for q's hi codes, one for its lo codes
+                float sacc[NT][U][2][4] = {};
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t r0_, r1_, r2_, r3_;
-                    ldmatrix_x4(r0_, r1_, r2_, r3_, stage_s + ((i * 32 + half_col) ^ swz));
-                    const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2(r1_),
-                                            f16x2_of_e4m3x2_hi(r0_), f16x2_of_e4m3x2_hi(r1_)};
-                    const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2(r3_),
-                                            f16x2_of_e4m3x2_hi(r2_), f16x2_of_e4m3x2_hi(r3_)};
+                for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(sacc[nt][0], a0, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-                        mma_f16(sacc[nt][1], a1, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+                    for (int u = 0; u < U; ++u) {
+                        uint32_t a0, a1, a2, a3;
+                        ldmatrix_x4(a0, a1, a2, a3, column(stage[u] + k_off, i));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_e4m3(sacc[nt][u][0], a0, a1, a2, a3, qh[nt][2 * i],
+                                     qh[nt][2 * i + 1]);
+                            mma_e4m3(sacc[nt][u][1], a0, a1, a2, a3, ql[nt][2 * i],
+                                     ql[nt][2 * i + 1]);
+                        }
+                    }
+                // the scales of this lane's tokens, rows g and g + 8
+                float y[NT][U][4], inv_v[U][2];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const unsigned char *sk = sc[u] + token_of_row(g + k * 8) * 8;
+                        const unsigned char *sv = sk + C::kTok * 8;
+                        const unsigned bk = HPC >= 4 ? sk[hw] : sk[(sk[4] & 3) + hw];
+                        const unsigned bv = HPC >= 4 ? sv[hw] : sv[(sv[4] & 3) + hw];
+                        const float fk = q8_scale(bk);
+                        const float ev = __uint_as_float(0x4b000000u | bv) - 8388735.f;  // bv - 127
+                        inv_v[u][k] = __uint_as_float((254u - bv) << 23);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int x = 2 * k + e;
+                                y[nt][u][x] = fmaf(fmaf(sacc[nt][u][1][x], 1.f / 32,
+                                                        sacc[nt][u][0][x]),
+                                                   fk * cq[nt][e], ev);
+                            }
+                    }
+                // some of the tokens are of no piece: no weight, and V's bytes (which
+                // may be NaN) masked
+                const bool cut = v0 > 0 || v1 < 16 + (U - 1) * C::kTok;
+                uint32_t keep[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    keep[u] = 0xffffffffu;
+                if (cut) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        auto in = [&](int row) {
+                            const int t = token_of_row(row) + u * C::kTok;
+                            return t >= v0 && t < v1;
+                        };
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (!in(g + k * 8)) {
+                                inv_v[u][k] = 0.f;
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    y[nt][u][2 * k] = y[nt][u][2 * k + 1] = -INFINITY;
+                            }
+                        keep[u] = (in(2 * c) ? 0xffu : 0u) | (in(2 * c + 1) ? 0xff00u : 0u) |
+                                  (in(2 * c + 8) ? 0xff0000u : 0u) |
+                                  (in(2 * c + 9) ? 0xff000000u : 0u);
                     }
                 }
-                // this lane's tokens g and g + 8: their scales
-                float fk[2], ev[2], inv_v[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = g + u * 8;
-                    const unsigned char *sk = sc + (tg * 16 + t) * 8, *sv = sk + C::kTok * 8;
-                    const unsigned bk = HPC >= 4 ? sk[hw] : sk[(sk[4] & 3) + hw];
-                    const unsigned bv = HPC >= 4 ? sv[hw] : sv[(sv[4] & 3) + hw];
-                    const bool in = t >= v0 && t < v1;
-                    fk[u] = q8_scale(bk);
-                    ev[u] = in ? (float)((int)bv - 127) : -INFINITY;
-                    inv_v[u] = in ? __uint_as_float((254u - bv) << 23) : 0.f;
-                }
-                float y[NT][4];
                 bool raise = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = (sacc[nt][0][e] + sacc[nt][1][e]) * (fk[e >> 1] * cq[nt][e & 1]);
-                        // (a token of no piece: whatever its row held)
-                        y[nt][e] = ev[e >> 1] == -INFINITY ? -INFINITY : x + ev[e >> 1];
-                        raise |= y[nt][e] > m_run[nt][e & 1] + kRaise;
-                    }
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            raise |= y[nt][u][x] > m_run[nt][x & 1] + kRaise;
                 if (__any_sync(kFull, raise)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float mx = fmaxf(y[nt][e], y[nt][e + 2]);
+                            float mx = fmaxf(y[nt][0][e], y[nt][0][e + 2]);
+                            if (U == 2)
+                                mx = fmaxf(mx, fmaxf(y[nt][U - 1][e], y[nt][U - 1][e + 2]));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                            const float mn = fmaxf(m_run[nt][e], mx);
-                            const float a = mn == -INFINITY ? 1.f : exp2f(m_run[nt][e] - mn);
+                            const float mn = fmaxf(m_run[nt][e], mx - kRoom);
+                            const float a = mn == -INFINITY ? 1.f : exp2_ftz(m_run[nt][e] - mn);
                             m_run[nt][e] = mn;
                             l_run[nt][e] *= a;
 #pragma unroll
@@ -564,68 +655,84 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                             }
                         }
                 }
-                uint32_t pb[NT][2];
+                uint32_t ph[NT][U], pl[NT][U];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
+                    const float base0 = m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0];
+                    const float base1 = m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float base = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
-                        w[e] = exp2f(y[nt][e] - base);
-                        l_run[nt][e & 1] = fmaf(w[e], inv_v[e >> 1], l_run[nt][e & 1]);
+                    for (int u = 0; u < U; ++u) {
+                        float w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            w[x] = exp2_ftz(y[nt][u][x] - (x & 1 ? base1 : base0));
+                            l_run[nt][x & 1] = fmaf(w[x], inv_v[u][x >> 1], l_run[nt][x & 1]);
+                        }
+                        // S^T's layout has a token's heads in a lane, P^T's operand a
+                        // head's tokens: transpose the two 8 x 8 halves, a weight's hi
+                        // and lo codes being one 16-bit element, then part the codes
+                        const uint32_t h0 = movmatrix_trans(split_pair(w[0], w[1]));
+                        const uint32_t h1 = movmatrix_trans(split_pair(w[2], w[3]));
+                        ph[nt][u] = __byte_perm(h0, h1, 0x6420);
+                        pl[nt][u] = __byte_perm(h0, h1, 0x7531);
                     }
-                    // S^T's layout has a token's heads in a lane, P^T's B operand a
-                    // head's tokens: transpose the two 8 x 8 halves
-                    pb[nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
-                    pb[nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
                 }
-                // V^T: a transposed 8-token x 16-byte matrix gives lane (g, c) the codes
-                // (t, d), (t, d+1), (t+1, d), (t+1, d+1) of t = 2c, d = 2g: swapping the
-                // middle two leaves the token pairs of column d and of column d + 1.
-                // Tokens outside the piece are replaced by zeros (selector 4).
-                unsigned sel0 = 0x3120, sel1 = 0x3120;
-                if (v0 > 0 || v1 < 16) {
-                    auto selector = [&](int t) {
-                        return (t >= v0 && t < v1 ? 0x0100u : 0x0404u) |
-                               (t + 1 >= v0 && t + 1 < v1 ? 0x3020u : 0x4040u);
-                    };
-                    sel0 = selector(2 * c);
-                    sel1 = selector(2 * c + 8);
-                }
+                // O^T += V^T P^T: 32 places of depth are two tiles' tokens (hi codes,
+                // then lo codes), or one tile's twice (hi and lo codes)
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    uint32_t r0_, r1_, r2_, r3_;
-                    ldmatrix_x4_trans(r0_, r1_, r2_, r3_,
-                                      stage_s + C::kTok * C::kPitch + ((i * 32 + half_col) ^ swz));
-                    r0_ = __byte_perm(r0_, 0, sel0);
-                    r1_ = __byte_perm(r1_, 0, sel1);
-                    r2_ = __byte_perm(r2_, 0, sel0);
-                    r3_ = __byte_perm(r3_, 0, sel1);
-                    const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2_hi(r0_),
-                                            f16x2_of_e4m3x2(r1_), f16x2_of_e4m3x2_hi(r1_)};
-                    const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2_hi(r2_),
-                                            f16x2_of_e4m3x2(r3_), f16x2_of_e4m3x2_hi(r3_)};
+                    uint32_t a[U][2], b2[U][2];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        ldmatrix_trans_b8(a[u][0], a[u][1], b2[u][0], b2[u][1],
+                                          column(stage[u] + v_off, i));
+                        if (cut) {
+                            a[u][0] &= keep[u];
+                            a[u][1] &= keep[u];
+                            b2[u][0] &= keep[u];
+                            b2[u][1] &= keep[u];
+                        }
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(oacc[nt][2 * i], a0, pb[nt][0], pb[nt][1]);
-                        mma_f16(oacc[nt][2 * i + 1], a1, pb[nt][0], pb[nt][1]);
+                        constexpr int V = U - 1;
+                        if (U == 2) {
+                            mma_e4m3(oacc[nt][2 * i], a[0][0], a[0][1], a[V][0], a[V][1],
+                                     ph[nt][0], ph[nt][V]);
+                            mma_e4m3(oacc[nt][2 * i + 1], b2[0][0], b2[0][1], b2[V][0], b2[V][1],
+                                     ph[nt][0], ph[nt][V]);
+                            mma_e4m3(oacc[nt][2 * i], a[0][0], a[0][1], a[V][0], a[V][1],
+                                     pl[nt][0], pl[nt][V]);
+                            mma_e4m3(oacc[nt][2 * i + 1], b2[0][0], b2[0][1], b2[V][0], b2[V][1],
+                                     pl[nt][0], pl[nt][V]);
+                        } else {
+                            mma_e4m3(oacc[nt][2 * i], a[0][0], a[0][1], a[0][0], a[0][1],
+                                     ph[nt][0], pl[nt][0]);
+                            mma_e4m3(oacc[nt][2 * i + 1], b2[0][0], b2[0][1], b2[0][0], b2[0][1],
+                                     ph[nt][0], pl[nt][0]);
+                        }
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&empty[st]);
+            if (lane == 0) {
+                mbar_arrive(&empty[it % NST]);
+                if (U == 2 && take == 2)
+                    mbar_arrive(&empty[(it + 1) % NST]);
+            }
+            tok += take * C::kTok;
+            it += take;
         }
 
         // ---- end of the piece: join the head's parts in pairs -----------------
-        if constexpr (C::kParts > 1) {
+        if constexpr (C::kWph > 1) {
             float *slots = reinterpret_cast<float *>(smem + C::kJoinOffset) + lane;
 #pragma unroll
-            for (int s = C::kParts / 2; s >= 1; s >>= 1)
+            for (int s = C::kWph / 2; s >= 1; s >>= 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {              // heads 2c, then 2c + 1
-                    if (part >= s && part < 2 * s) {
-                        float *to = slots + ((part - s) * HPC + hw) * (C::kJoinFloats * 32);
+                    if (tg >= s && tg < 2 * s) {
+                        float *to = slots + ((tg - s) * HPC + hw) * (C::kJoinFloats * 32);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             *to = m_run[nt][e], to += 32;
@@ -637,15 +744,15 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                             }
                         }
                     }
-                    named_bar_sync(1, C::kWarps * 32);
-                    if (part < s) {
-                        const float *from = slots + (part * HPC + hw) * (C::kJoinFloats * 32);
+                    named_bar_sync(1, kWarps * 32);
+                    if (tg < s) {
+                        const float *from = slots + (tg * HPC + hw) * (C::kJoinFloats * 32);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const float m = *from;
                             const float mn = fmaxf(m_run[nt][e], m);
                             const float base = mn == -INFINITY ? 0.f : mn;
-                            const float fa = exp2f(m_run[nt][e] - base), fb = exp2f(m - base);
+                            const float fa = exp2_ftz(m_run[nt][e] - base), fb = exp2_ftz(m - base);
                             m_run[nt][e] = mn;
                             l_run[nt][e] = l_run[nt][e] * fa + from[32] * fb;
                             from += 64;
@@ -657,12 +764,18 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                             }
                         }
                     }
-                    named_bar_sync(1, C::kWarps * 32);
+                    named_bar_sync(1, kWarps * 32);
                 }
         }
-        if (part != 0)
+        if (tg != 0)
             continue;
-        // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + 2g + (e >> 1)
+        // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + g + 8 (e >> 1)
+        const int first = block_of(lo, T, G);
+        const int last = block_of(hi - 1, T, G);
+        if (t0 == 0 && warp == 0 && lane == 0 && !planned) {
+            p.row_info[2 * r] = first;
+            p.row_info[2 * r + 1] = last - first + 1;
+        }
         const bool whole = first == last;
         const size_t slot0 = (size_t)(cta + r) * (HPC * p.n_rep) + (size_t)hw * p.n_rep;
 #pragma unroll
@@ -680,17 +793,19 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                     l = 1.f, m = 0.f;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 if (whole) {
-                    __nv_bfloat16 *o = p.out + (qrow0 + h) * D + 2 * g;
+                    __nv_bfloat16 *o = p.out + (qrow0 + h) * D + g;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        *reinterpret_cast<uint32_t *>(o + 16 * j) =
-                            pack_bf16x2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[16 * j] = __float2bfloat16_rn(oacc[nt][j][e] * inv);
+                        o[16 * j + 8] = __float2bfloat16_rn(oacc[nt][j][e + 2] * inv);
+                    }
                 } else {
-                    float *o = p.o_part + (slot0 + h) * D + 2 * g;
+                    float *o = p.o_part + (slot0 + h) * D + g;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        *reinterpret_cast<float2 *>(o + 16 * j) =
-                            make_float2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[16 * j] = oacc[nt][j][e] * inv;
+                        o[16 * j + 8] = oacc[nt][j][e + 2] * inv;
+                    }
                     if (g == 0)
                         reinterpret_cast<float2 *>(p.ml_part)[slot0 + h] =
                             l > 0.f ? make_float2(m * kLn2f, l) : make_float2(-INFINITY, 0.f);
