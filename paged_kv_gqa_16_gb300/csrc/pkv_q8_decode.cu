@@ -16,25 +16,20 @@
 //    eight columns, which a group of 8 heads fills and a group of 4 fills
 //    half -- half the products and half the accumulators of heads as rows.
 //    NT = 2 column tiles serve groups of 9 to 16 heads.
-//  - The products take the codes as they are (e4m3 x e4m3, m16n8k32, fp32
-//    sums): no conversion, and a quarter of the tensor time of f16 products
-//    (measured: 4.2 against 8 cycles an instruction, of twice the depth).
-//    The other operands are split in two codes each.  q, scaled by a power of
-//    two to a largest value in [128, 256), is hi + lo / 32: hi keeps four of
-//    bf16's eight significant bits, lo the other four (down to 2^-14 of the
-//    largest value, 2^-22 of it below), and their products have sums of their
-//    own.  A weight w is hi + lo, eight significant bits as a bf16 weight
-//    would have (in steps of 2^-9 at least, the largest weight being 2^7 or
-//    more): hi takes the first 16 of the 32 places of depth, lo the others,
-//    against the same 16 tokens of V twice.
+//  - Codes become f16 exactly (one cvt for two codes).  q is scaled by a
+//    power of two to at most 2 in size, which keeps its eight significant
+//    bits in f16; that power and the softmax scale go into the score's
+//    factor in fp32.  (e4m3 x e4m3 products, with q and the weights as two
+//    codes each, were slower: 62.8 us for the serving batch below, at twice
+//    the tensor pipe's time -- this GPU makes them out of f16 products.)
 //  - Both scales act on the scores: x_t = 2^ek_t (s_t c) and y_t = x_t + ev_t
 //    in the log2 domain.  The weights used for O are 2^(y_t - base), base
-//    following the largest y_t, so they are in e4m3's range however the
+//    following the largest y_t, so they are in f16's range however the
 //    values' scales differ; the sum of softmax weights takes each of them, in
 //    fp32, times 2^-ev_t (a power of two, exact).  Both sums carry 2^-base.
-//  - base is 7 under the largest y_t of the time it was set and is raised when
-//    some y_t exceeds it by more than 8.5 (a weight is then at most 2^8.5, the
-//    format ends at 448): the usual tile needs no maximum over its lanes and
+//    A weight is rounded to f16 (11 significant bits) for the product.
+//  - base is raised only when some y_t exceeds it by more than 8: a weight is
+//    then at most 2^8 and the usual tile needs no maximum over its lanes and
 //    no rescaling.
 //  - A kv head has WPH = 8 / HPC warps, which take 16 tokens each of every
 //    stage and have sums of their own, joined in pairs through shared memory at
@@ -59,8 +54,7 @@ namespace {
 
 constexpr int kWarps = 8;                 // consumer warps
 constexpr int kProducers = 2;             // producer warps, a stage each in turn
-constexpr float kRoom = 7.f;              // a base is this far under the largest score
-constexpr float kRaise = 8.5f;            // and is raised when one exceeds it by more
+constexpr float kRaise = 8.f;             // how far a score may exceed its base
 
 struct Q8Params {
     FusedParams f;
@@ -106,25 +100,20 @@ struct Q8Cfg {
     static_assert(kStageBytes % 16 == 0 && kJoinBytes % 16 == 0, "alignment");
 };
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
                  "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two transposed matrices of 16 rows x 16 bytes: row r of a matrix is at the
-// address of lane r (the second's: of lane 16 + r), and lane (g, c) gets its
-// columns g (r0; r2) and g + 8 (r1; r3), rows 4c .. 4c + 3.
-__device__ __forceinline__ void ldmatrix_trans_b8(uint32_t &r0, uint32_t &r1, uint32_t &r2,
-                                                  uint32_t &r3, uint32_t addr)
+// Two floats to f16x2, the first in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
-    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-                 : "r"(addr)
-                 : "memory");
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 __device__ __forceinline__ float exp2_ftz(float x)
@@ -132,22 +121,6 @@ __device__ __forceinline__ float exp2_ftz(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// Two values as codes hi (their nearest) and lo (of what hi leaves):
-// bytes (hi of a, lo of a, hi of b, lo of b).
-__device__ __forceinline__ uint32_t split_pair(float a, float b)
-{
-    const __half2 v = __floats2half2_rn(a, b);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
-    uint16_t hi, lo;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(w));
-    const uint32_t back = f16x2_of_e4m3x2(hi);
-    const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2 *>(&back));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
-        : "=h"(lo)
-        : "r"(*reinterpret_cast<const uint32_t *>(&rest)));
-    return __byte_perm(hi, lo, 0x5140);
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
@@ -455,16 +428,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
     // the 32-byte column i of a row whose first is at `addr` (TILED: the
     // swizzle is in the same bits)
     auto column = [](uint32_t addr, int i) { return TILED ? addr ^ (i * 32u) : addr + i * 32u; };
-    // The products' rows 8-15 are tokens 12-15, 8-11: with that both K's loads
-    // (rows) and V's (places of depth, 4c + i: rows 2c, 2c + 1, 2c + 8, 2c + 9)
-    // take eight tokens at a time that differ modulo 8, in different banks.
-    auto token_of_row = [](int m) { return m < 8 ? m : m ^ 4; };
-    const int l16 = lane & 15;
-    const uint32_t k_off = smem_s + token_addr(tg * 16 + token_of_row(l16));
-    const uint32_t v_off =
-        smem_s + C::kTok * C::kPitch +
-        token_addr(tg * 16 +
-                   token_of_row(2 * (l16 >> 2) + (l16 & 1) + ((l16 & 2) ? 8 : 0)));
+    const uint32_t k_off = smem_s + token_addr(tg * 16 + (lane & 15));
+    const uint32_t v_off = k_off + C::kTok * C::kPitch;
     int it = 0;
     bool aborted = false;
 
@@ -479,8 +444,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
         const size_t qrow0 = (size_t)b * p.Hq + (size_t)(hg * HPC + hw) * p.n_rep;
 
         // q as the products' B operand: lane (g, c) holds elements 4c .. 4c + 3
-        // of each 16 of head g, as codes hi and lo
-        uint32_t qh[NT][D / 16], ql[NT][D / 16];
+        // of each 16 of head g, the order in which a K word's four codes come
+        uint32_t qf[NT][D / 16][2];
         float cq[NT][2];                   // factors of heads 2c, 2c + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -497,26 +462,15 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
             }
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-            // 2^(7 - n), n the exponent of amax, both powers kept in the normal range
-            const int n = max((int)(__float_as_uint(amax) >> 23) - 127, -119);
-            const float down = __uint_as_float((unsigned)(134 - n) << 23);
+            // 2^-n, n the exponent of amax, both powers kept in the normal range
+            const int n = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
+            const float down = __uint_as_float((unsigned)(127 - n) << 23);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                const float x[4] = {bf16_lo(raw[j].x), bf16_hi(raw[j].x), bf16_lo(raw[j].y),
-                                    bf16_hi(raw[j].y)};
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)        // (an infinite element becomes NaN)
-                    y[i] = fabsf(x[i]) == INFINITY ? __uint_as_float(0x7fffffffu) : x[i] * down;
-                qh[nt][j] = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
-                const uint32_t h01 = f16x2_of_e4m3x2(qh[nt][j]);
-                const uint32_t h23 = f16x2_of_e4m3x2_hi(qh[nt][j]);
-                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h01));
-                const float2 b2 = __half22float2(*reinterpret_cast<const __half2 *>(&h23));
-                ql[nt][j] = e4m3x2((y[0] - a.x) * 32.f, (y[1] - a.y) * 32.f) |
-                            (e4m3x2((y[2] - b2.x) * 32.f, (y[3] - b2.y) * 32.f) << 16);
+                qf[nt][j][0] = pack_f16x2(bf16_lo(raw[j].x) * down, bf16_hi(raw[j].x) * down);
+                qf[nt][j][1] = pack_f16x2(bf16_lo(raw[j].y) * down, bf16_hi(raw[j].y) * down);
             }
-            const float up = __uint_as_float((unsigned)(120 + n) << 23) * p.scale_log2;
+            const float up = __uint_as_float((unsigned)(127 + n) << 23) * p.scale_log2;
             cq[nt][0] = __shfl_sync(kFull, up, (2 * c) * 4);
             cq[nt][1] = __shfl_sync(kFull, up, (2 * c + 1) * 4);
         }
@@ -559,20 +513,24 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
             // piece, [v0, v1) - kTok of the second (none of a stage not taken)
             const int v0 = t0 - tok - tg * 16, v1 = t1 - tok - tg * 16;
             if (!aborted && v1 > 0 && v0 < 16 + (U - 1) * C::kTok) {
-                // S^T = K q: one sum for q's hi codes, one for its lo codes
+                // S^T = K q, in two sums: a word of four codes gives two pairs of f16,
+                // places 2c, 2c + 1 and 2c + 8, 2c + 9 of a product's depth
                 float sacc[NT][U][2][4] = {};
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i)
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        uint32_t a0, a1, a2, a3;
-                        ldmatrix_x4(a0, a1, a2, a3, column(stage[u] + k_off, i));
+                        uint32_t r0_, r1_, r2_, r3_;
+                        ldmatrix_x4(r0_, r1_, r2_, r3_, column(stage[u] + k_off, i));
+                        const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2(r1_),
+                                                f16x2_of_e4m3x2_hi(r0_), f16x2_of_e4m3x2_hi(r1_)};
+                        const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2(r3_),
+                                                f16x2_of_e4m3x2_hi(r2_), f16x2_of_e4m3x2_hi(r3_)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_e4m3(sacc[nt][u][0], a0, a1, a2, a3, qh[nt][2 * i],
-                                     qh[nt][2 * i + 1]);
-                            mma_e4m3(sacc[nt][u][1], a0, a1, a2, a3, ql[nt][2 * i],
-                                     ql[nt][2 * i + 1]);
+                            mma_f16(sacc[nt][u][0], a0, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+                            mma_f16(sacc[nt][u][1], a1, qf[nt][2 * i + 1][0],
+                                    qf[nt][2 * i + 1][1]);
                         }
                     }
                 // the scales of this lane's tokens, rows g and g + 8
@@ -581,7 +539,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const unsigned char *sk = sc[u] + token_of_row(g + k * 8) * 8;
+                        const unsigned char *sk = sc[u] + (g + k * 8) * 8;
                         const unsigned char *sv = sk + C::kTok * 8;
                         const unsigned bk = HPC >= 4 ? sk[hw] : sk[(sk[4] & 3) + hw];
                         const unsigned bv = HPC >= 4 ? sv[hw] : sv[(sv[4] & 3) + hw];
@@ -593,36 +551,35 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int x = 2 * k + e;
-                                y[nt][u][x] = fmaf(fmaf(sacc[nt][u][1][x], 1.f / 32,
-                                                        sacc[nt][u][0][x]),
+                                y[nt][u][x] = fmaf(sacc[nt][u][0][x] + sacc[nt][u][1][x],
                                                    fk * cq[nt][e], ev);
                             }
                     }
                 // some of the tokens are of no piece: no weight, and V's bytes (which
                 // may be NaN) masked
                 const bool cut = v0 > 0 || v1 < 16 + (U - 1) * C::kTok;
-                uint32_t keep[U];
+                unsigned sel[U][2];                    // byte selectors of V's words, below
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    keep[u] = 0xffffffffu;
+                    sel[u][0] = sel[u][1] = 0x3120;
                 if (cut) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        auto in = [&](int row) {
-                            const int t = token_of_row(row) + u * C::kTok;
-                            return t >= v0 && t < v1;
+                        auto in = [&](int t) {
+                            return t + u * C::kTok >= v0 && t + u * C::kTok < v1;
                         };
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
+                        for (int k = 0; k < 2; ++k) {
                             if (!in(g + k * 8)) {
                                 inv_v[u][k] = 0.f;
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
                                     y[nt][u][2 * k] = y[nt][u][2 * k + 1] = -INFINITY;
                             }
-                        keep[u] = (in(2 * c) ? 0xffu : 0u) | (in(2 * c + 1) ? 0xff00u : 0u) |
-                                  (in(2 * c + 8) ? 0xff0000u : 0u) |
-                                  (in(2 * c + 9) ? 0xff000000u : 0u);
+                            // (selector 4: a zero byte)
+                            sel[u][k] = (in(2 * c + k * 8) ? 0x0100u : 0x0404u) |
+                                        (in(2 * c + 1 + k * 8) ? 0x3020u : 0x4040u);
+                        }
                     }
                 }
                 bool raise = false;
@@ -644,7 +601,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                            const float mn = fmaxf(m_run[nt][e], mx - kRoom);
+                            const float mn = fmaxf(m_run[nt][e], mx);
                             const float a = mn == -INFINITY ? 1.f : exp2_ftz(m_run[nt][e] - mn);
                             m_run[nt][e] = mn;
                             l_run[nt][e] *= a;
@@ -655,7 +612,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                             }
                         }
                 }
-                uint32_t ph[NT][U], pl[NT][U];
+                uint32_t pb[NT][U][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float base0 = m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0];
@@ -668,51 +625,36 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                             w[x] = exp2_ftz(y[nt][u][x] - (x & 1 ? base1 : base0));
                             l_run[nt][x & 1] = fmaf(w[x], inv_v[u][x >> 1], l_run[nt][x & 1]);
                         }
-                        // S^T's layout has a token's heads in a lane, P^T's operand a
-                        // head's tokens: transpose the two 8 x 8 halves, a weight's hi
-                        // and lo codes being one 16-bit element, then part the codes
-                        const uint32_t h0 = movmatrix_trans(split_pair(w[0], w[1]));
-                        const uint32_t h1 = movmatrix_trans(split_pair(w[2], w[3]));
-                        ph[nt][u] = __byte_perm(h0, h1, 0x6420);
-                        pl[nt][u] = __byte_perm(h0, h1, 0x7531);
+                        // S^T's layout has a token's heads in a lane, P^T's B operand a
+                        // head's tokens: transpose the two 8 x 8 halves
+                        pb[nt][u][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                        pb[nt][u][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
                     }
                 }
-                // O^T += V^T P^T: 32 places of depth are two tiles' tokens (hi codes,
-                // then lo codes), or one tile's twice (hi and lo codes)
+                // O^T += V^T P^T: a transposed 8-token x 16-byte matrix gives lane (g, c)
+                // the codes (t, d), (t, d+1), (t+1, d), (t+1, d+1) of t = 2c, d = 2g:
+                // swapping the middle two leaves the token pairs of column d and of
+                // column d + 1
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t a[U][2], b2[U][2];
+                for (int i = 0; i < D / 32; ++i)
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        ldmatrix_trans_b8(a[u][0], a[u][1], b2[u][0], b2[u][1],
-                                          column(stage[u] + v_off, i));
-                        if (cut) {
-                            a[u][0] &= keep[u];
-                            a[u][1] &= keep[u];
-                            b2[u][0] &= keep[u];
-                            b2[u][1] &= keep[u];
-                        }
-                    }
+                        uint32_t r0_, r1_, r2_, r3_;
+                        ldmatrix_x4_trans(r0_, r1_, r2_, r3_, column(stage[u] + v_off, i));
+                        r0_ = __byte_perm(r0_, 0, sel[u][0]);
+                        r1_ = __byte_perm(r1_, 0, sel[u][1]);
+                        r2_ = __byte_perm(r2_, 0, sel[u][0]);
+                        r3_ = __byte_perm(r3_, 0, sel[u][1]);
+                        const uint32_t a0[4] = {f16x2_of_e4m3x2(r0_), f16x2_of_e4m3x2_hi(r0_),
+                                                f16x2_of_e4m3x2(r1_), f16x2_of_e4m3x2_hi(r1_)};
+                        const uint32_t a1[4] = {f16x2_of_e4m3x2(r2_), f16x2_of_e4m3x2_hi(r2_),
+                                                f16x2_of_e4m3x2(r3_), f16x2_of_e4m3x2_hi(r3_)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        constexpr int V = U - 1;
-                        if (U == 2) {
-                            mma_e4m3(oacc[nt][2 * i], a[0][0], a[0][1], a[V][0], a[V][1],
-                                     ph[nt][0], ph[nt][V]);
-                            mma_e4m3(oacc[nt][2 * i + 1], b2[0][0], b2[0][1], b2[V][0], b2[V][1],
-                                     ph[nt][0], ph[nt][V]);
-                            mma_e4m3(oacc[nt][2 * i], a[0][0], a[0][1], a[V][0], a[V][1],
-                                     pl[nt][0], pl[nt][V]);
-                            mma_e4m3(oacc[nt][2 * i + 1], b2[0][0], b2[0][1], b2[V][0], b2[V][1],
-                                     pl[nt][0], pl[nt][V]);
-                        } else {
-                            mma_e4m3(oacc[nt][2 * i], a[0][0], a[0][1], a[0][0], a[0][1],
-                                     ph[nt][0], pl[nt][0]);
-                            mma_e4m3(oacc[nt][2 * i + 1], b2[0][0], b2[0][1], b2[0][0], b2[0][1],
-                                     ph[nt][0], pl[nt][0]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(oacc[nt][2 * i], a0, pb[nt][u][0], pb[nt][u][1]);
+                            mma_f16(oacc[nt][2 * i + 1], a1, pb[nt][u][0], pb[nt][u][1]);
                         }
                     }
-                }
             }
             __syncwarp();
             if (lane == 0) {
@@ -769,7 +711,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
         }
         if (tg != 0)
             continue;
-        // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + g + 8 (e >> 1)
+        // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + 2g + (e >> 1)
         const int first = block_of(lo, T, G);
         const int last = block_of(hi - 1, T, G);
         if (t0 == 0 && warp == 0 && lane == 0 && !planned) {
@@ -793,19 +735,17 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                     l = 1.f, m = 0.f;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 if (whole) {
-                    __nv_bfloat16 *o = p.out + (qrow0 + h) * D + g;
+                    __nv_bfloat16 *o = p.out + (qrow0 + h) * D + 2 * g;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        o[16 * j] = __float2bfloat16_rn(oacc[nt][j][e] * inv);
-                        o[16 * j + 8] = __float2bfloat16_rn(oacc[nt][j][e + 2] * inv);
-                    }
+                    for (int j = 0; j < D / 16; ++j)
+                        *reinterpret_cast<uint32_t *>(o + 16 * j) =
+                            pack_bf16x2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
                 } else {
-                    float *o = p.o_part + (slot0 + h) * D + g;
+                    float *o = p.o_part + (slot0 + h) * D + 2 * g;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        o[16 * j] = oacc[nt][j][e] * inv;
-                        o[16 * j + 8] = oacc[nt][j][e + 2] * inv;
-                    }
+                    for (int j = 0; j < D / 16; ++j)
+                        *reinterpret_cast<float2 *>(o + 16 * j) =
+                            make_float2(oacc[nt][j][e] * inv, oacc[nt][j][e + 2] * inv);
                     if (g == 0)
                         reinterpret_cast<float2 *>(p.ml_part)[slot0 + h] =
                             l > 0.f ? make_float2(m * kLn2f, l) : make_float2(-INFINITY, 0.f);

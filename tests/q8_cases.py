@@ -52,16 +52,10 @@ def decode_values(codes, scale):
 
 
 def attention(q, k, v, scale):
-    """q [Hq, D], k and v [L, Hkv, D]: the output [Hq, D] and its bound against
-    sum_t w_t |v_t|.
-
-    The output's rounding: 2^-8.  The scores: 128 products summed in 32 bits,
-    2^-23 each at most, so under 2^-16 of sum |q k|, and twice that in a weight
-    and in the weights' sum.  The weights are held as two e4m3 codes of a
-    multiple x of them whose largest value is 2^7 or more: the first code is off
-    by x 2^-4 at most, the second by 2^-4 of what is left or half a step of
-    2^-9, so a weight is off by w 2^-8 or, where that is less, by
-    2^-10 / 2^7 = 2^-17 of the largest weight (and never by more than itself)."""
+    """q [Hq, D], k and v [L, Hkv, D]: the output [Hq, D] and its bound: the
+    output's rounding (2^-8), the weights' rounding to 11 bits (2^-11 of each) and
+    the scores' error (128 products of 2^-23 each at most, so under 2^-16 of
+    sum |q k|, twice in the weights and their sum) against sum_t w_t |v_t|."""
     Hq, D = q.shape
     L, Hkv, _ = k.shape
     q = q.double().view(Hkv, Hq // Hkv, D)
@@ -69,10 +63,8 @@ def attention(q, k, v, scale):
     w = torch.softmax(x, -1)
     out = torch.einsum("grl,lgd->grd", w, v)
     size = torch.einsum("grl,lgd->grd", w, v.abs())
-    held = torch.maximum(w * 2.0 ** -8, torch.minimum(w, w.amax(-1, keepdim=True) * 2.0 ** -17))
     far = torch.einsum("grd,lgd->grl", q.abs(), k.abs()).amax(-1, keepdim=True) * scale * 2.0 ** -16
-    bound = (out.abs() * 2.0 ** -8 + torch.einsum("grl,lgd->grd", held, v.abs()) + size * (2.0 ** -20 + 2 * far)
-             + 1e-30)
+    bound = out.abs() * 2.0 ** -8 + size * (2.0 ** -10 + 2 * far) + 1e-30
     return out.reshape(Hq, D), bound.reshape(Hq, D)
 
 
