@@ -1099,12 +1099,12 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
     p.status = status;
     p.B = dims->B;
     p.Hkv = dims->Hkv;
-    p.D = dims->D;
+    p.ps_shift = log2_exact(dims->page_size);
     p.page_size = dims->page_size;
     p.num_pages = dims->num_pages;
     p.num_indices = dims->num_indices;
     p.max_seq_len = dims->max_seq_len;
-    return launch_status(pkv::launch_read_q8(p, (cudaStream_t)stream));
+    return launch_status(pkv::launch_read_q8(p, dims->D, (cudaStream_t)stream));
 }
 
 static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void *k_codes,

@@ -115,7 +115,7 @@ struct TokenWriteParams {
     uint32_t *status;              // nullable
     float norm_eps;
     int T, B, Hq, Hkv, page_size, num_pages, num_indices, max_seq_len, rope_max_pos;
-    int per_block;                 // tokens a block takes (set by the launcher)
+    int width_shift;               // log2 of the lane groups a token takes (set by the launcher)
 };
 
 // An 8-bit cache read back as bf16 (pkv_q8_read.cu).
@@ -130,7 +130,9 @@ struct ReadQ8Params {
     __nv_bfloat16 *k_out;
     __nv_bfloat16 *v_out;
     uint32_t *status;              // nullable
-    int B, Hkv, D, page_size, num_pages, num_indices, max_seq_len;
+    int B, Hkv, page_size, num_pages, num_indices, max_seq_len;
+    int ps_shift;                  // log2 of page_size, or -1
+    int per_block;                 // token slots a block takes (set by the launcher)
 };
 
 struct DecodeParams {
@@ -307,7 +309,7 @@ struct CombineParams {
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_extend(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_token_write(const TokenWriteParams &p, int D, cudaStream_t stream);
-cudaError_t launch_read_q8(const ReadQ8Params &p, cudaStream_t stream);
+cudaError_t launch_read_q8(const ReadQ8Params &p, int D, cudaStream_t stream);
 // the decode over an 8-bit cache; p.k_codes ... p.v_scale in place of the pools
 cudaError_t launch_decode_q8(const FusedParams &p, int D, int grid, cudaStream_t stream);
 cudaError_t launch_advance(const AdvanceParams &p, cudaStream_t stream);

@@ -1,5 +1,5 @@
-// pkv_q8.cuh -- the 8-bit cache's number format and the rotation in fp32,
-// shared by the kernels that write, read back and attend over it.
+// pkv_q8.cuh -- the 8-bit cache's number format, shared by the kernels that
+// write, read back and attend over it.
 #pragma once
 
 #include <cstdint>
@@ -13,13 +13,6 @@ namespace pkv {
 // are held, and the attention's sums over any two scales stay in fp32 range.
 constexpr int kQ8MinExp = -40;
 constexpr int kQ8MaxExp = 40;
-
-__device__ __forceinline__ void rotate(float &a, float &b, float c, float s)
-{
-    const float x = a, y = b;
-    a = fmaf(x, c, -y * s);
-    b = fmaf(x, s, y * c);
-}
 
 // The scale byte 127 + clamp(ceil(log2(amax / 448)), min, max).  448 = 1.75 *
 // 2^8: for amax = 1.f * 2^n the power is n - 8, one more if 1.f > 1.75.
@@ -38,14 +31,21 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return r;
 }
 
-// Eight values to codes at scale byte sb; an infinite value becomes NaN.
-__device__ __forceinline__ uint2 q8_encode8(const float (&x)[8], int sb)
+// Eight values times f (> 0) to codes at scale byte sb; with `inf`, infinite
+// values become NaN (they would saturate).
+__device__ __forceinline__ uint2 q8_encode8(const float (&x)[8], float f, int sb, bool inf)
 {
-    const float inv = __uint_as_float((unsigned)(254 - sb) << 23);      // 2^(127 - sb)
+    const float by = f * __uint_as_float((unsigned)(254 - sb) << 23);   // f 2^(127 - sb)
     float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        y[j] = fabsf(x[j]) == INFINITY ? __uint_as_float(0x7fffffffu) : x[j] * inv;
+        y[j] = x[j] * by;
+    if (inf) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (fabsf(y[j]) == INFINITY)
+                y[j] = __uint_as_float(0x7fffffffu);
+    }
     uint2 r;
     r.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
     r.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);

@@ -10,11 +10,17 @@
 //             are floating point, so a power of two keeps the precision of an
 //             arbitrary scale, costs one byte, and scales without rounding.
 //
-// A head vector belongs to a group of D / 8 lanes with eight values each, so
-// the norm's sum and the largest magnitude are log2(D / 8) shuffles, and every
-// load is 16 bytes.  A block takes a few consecutive tokens: their rows,
-// positions and slots are looked up once into shared memory, then its groups
-// run over the tokens' Hq + 2 Hkv vectors.
+// The pass reads and writes every value once and is bound by memory, if the
+// arithmetic is kept small: a head vector belongs to a group of D / 8 lanes with
+// eight values each (16-byte loads; the norm's sum and the largest magnitude
+// are log2(D / 8) shuffles), a group keeps one token, and the norm's weight
+// and the rotation become four coefficients a pair that its lanes form once for
+// all the token's query heads (and once for its K heads):
+//   y[2i]   = r (x[2i] (w c) - x[2i+1] (w' s)),
+//   y[2i+1] = r (x[2i] (w s) + x[2i+1] (w' c)),   r = rsqrt(mean + eps),
+// in two-wide fp32 operations.  `width` groups share a token; a block's tokens
+// are looked up once into shared memory while their first vectors are already
+// on their way.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_q8.cuh"
@@ -24,7 +30,10 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;        // tokens a block takes at most
+constexpr int kMaxTokens = 32;       // tokens a block takes at most
+constexpr int kQ = 4;                // query vectors a group has in flight,
+constexpr int kKv = 1;               // and K and V vectors
+constexpr int kManyBlocks = 1024;    // blocks that fill the GPU several times over
 
 struct TokenPlace {
     int pos;                         // -1: the token writes nothing
@@ -101,15 +110,164 @@ __device__ __forceinline__ float group_max(float x)
     return x;
 }
 
+// Two fp32 values in one 64-bit register.
+struct F2 {
+    unsigned long long v;
+};
+
+__device__ __forceinline__ F2 f2(float x, float y)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+
+__device__ __forceinline__ float2 parts(F2 a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// Eight values of a head vector: the pairs' first and second values.
+struct Eight {
+    F2 a[2], b[2];
+};
+
+__device__ __forceinline__ Eight unpack(uint4 r)
+{
+    return {{f2(bf16_lo(r.x), bf16_lo(r.y)), f2(bf16_lo(r.z), bf16_lo(r.w))},
+            {f2(bf16_hi(r.x), bf16_hi(r.y)), f2(bf16_hi(r.z), bf16_hi(r.w))}};
+}
+
+// The lane's coefficients: y = (a ca + b nsb, a sa + b cb).
+struct Turn {
+    F2 ca[2], nsb[2], sa[2], cb[2];
+};
+
+__device__ __forceinline__ Turn turn_of(float4 c01, float4 c23, const Eight &w)
+{
+    const F2 c[2] = {f2(c01.x, c01.z), f2(c23.x, c23.z)};
+    const F2 s[2] = {f2(c01.y, c01.w), f2(c23.y, c23.w)};
+    const F2 minus = f2(-1.f, -1.f);
+    Turn t;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        t.ca[i] = mul2(w.a[i], c[i]);
+        t.sa[i] = mul2(w.a[i], s[i]);
+        t.cb[i] = mul2(w.b[i], c[i]);
+        t.nsb[i] = mul2(minus, mul2(w.b[i], s[i]));
+    }
+    return t;
+}
+
+// Without a rotation the other value of a pair stays out of it (0 times an
+// infinity would be NaN).
+__device__ __forceinline__ void apply(Eight &x, const Turn &t, bool rotate)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const F2 a = x.a[i], b = x.b[i];
+        if (!rotate) {
+            x.a[i] = mul2(a, t.ca[i]);
+            x.b[i] = mul2(b, t.cb[i]);
+            continue;
+        }
+        x.a[i] = fma2(a, t.ca[i], mul2(b, t.nsb[i]));
+        x.b[i] = fma2(a, t.sa[i], mul2(b, t.cb[i]));
+    }
+}
+
+// rsqrt(mean(x^2) + eps) over the group.
+template <int D>
+__device__ __forceinline__ float norm_factor(const Eight &x, float eps)
+{
+    F2 s = mul2(x.a[0], x.a[0]);
+    s = fma2(x.a[1], x.a[1], s);
+    s = fma2(x.b[0], x.b[0], s);
+    s = fma2(x.b[1], x.b[1], s);
+    const float2 p = parts(s);
+    return rsqrtf(group_sum<D / 8>(p.x + p.y) * (1.f / D) + eps);
+}
+
+__device__ __forceinline__ uint4 pack(const Eight &x, float f)
+{
+    const F2 ff = f2(f, f);
+    const float2 a0 = parts(mul2(x.a[0], ff)), a1 = parts(mul2(x.a[1], ff));
+    const float2 b0 = parts(mul2(x.b[0], ff)), b1 = parts(mul2(x.b[1], ff));
+    return make_uint4(pack_bf16x2(a0.x, b0.x), pack_bf16x2(a0.y, b0.y),
+                      pack_bf16x2(a1.x, b1.x), pack_bf16x2(a1.y, b1.y));
+}
+
+// x f as codes and the scale byte of the group's vector.
+template <int D>
+__device__ __forceinline__ uint2 quantise(const Eight &x, float f, int &sb)
+{
+    const float2 a0 = parts(x.a[0]), a1 = parts(x.a[1]), b0 = parts(x.b[0]), b1 = parts(x.b[1]);
+    const float y[8] = {a0.x, b0.x, a0.y, b0.y, a1.x, b1.x, a1.y, b1.y};
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        amax = fmaxf(amax, fabsf(y[j]));
+    amax = group_max<D / 8>(amax) * f;
+    sb = q8_scale_byte(amax);
+    // (a power of two: x (f 2^-e) rounds as (x f) 2^-e does)
+    return q8_encode8(y, f, sb, amax == INFINITY);
+}
+
+// A block takes GROUPS / p.width tokens, p.width groups (a power of two) each.
 template <int D, bool Q8, bool EXTEND>
-__global__ void __launch_bounds__(kThreads) token_write_kernel(const TokenWriteParams p)
+__global__ void __launch_bounds__(kThreads, 3) token_write_kernel(const TokenWriteParams p)
 {
     constexpr int LANES = D / 8;             // lanes of a head vector
-    constexpr int GROUPS = kThreads / LANES;
     __shared__ TokenPlace s_place[kMaxTokens];
     grid_dependency_wait();
-    const int t0 = blockIdx.x * p.per_block;
-    const int nt = min(p.per_block, p.T - t0);
+    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const int at_once = kThreads / LANES >> p.width_shift;
+    const int t0 = blockIdx.x * at_once, tok = group >> p.width_shift;
+    const int nt = min(at_once, p.T - t0);
+    const int width = 1 << p.width_shift, v0 = group & (width - 1);
+    // (a group behind the last token reads that token and writes nothing)
+    const size_t t = (size_t)(t0 + min(tok, nt - 1));
+    const __nv_bfloat16 *q = p.q + t * p.q_stride + lane * 8;
+    const __nv_bfloat16 *k = p.k + t * p.k_stride + lane * 8;
+    const __nv_bfloat16 *v = p.v + t * p.v_stride + lane * 8;
+
+    auto load = [&](const __nv_bfloat16 *src, int h, int H) {
+        return h < H ? __ldcs(reinterpret_cast<const uint4 *>(src + h * D))
+                     : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // the first vectors do not wait for the look-up
+    uint4 rq[kQ], rk[kKv], rv[kKv];
+#pragma unroll
+    for (int u = 0; u < kQ; ++u)
+        rq[u] = load(q, v0 + u * width, p.Hq);
+#pragma unroll
+    for (int u = 0; u < kKv; ++u) {
+        rk[u] = load(k, v0 + u * width, p.Hkv);
+        rv[u] = load(v, v0 + u * width, p.Hkv);
+    }
+    const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    uint4 wq = ones, wk = ones;
+    if (p.q_norm != nullptr)
+        wq = *(reinterpret_cast<const uint4 *>(p.q_norm) + lane);
+    if (p.k_norm != nullptr)
+        wk = *(reinterpret_cast<const uint4 *>(p.k_norm) + lane);
+
     if (threadIdx.x < nt) {
         unsigned bad = 0;
         s_place[threadIdx.x] = place_token<EXTEND>(p, t0 + threadIdx.x, bad);
@@ -118,88 +276,70 @@ __global__ void __launch_bounds__(kThreads) token_write_kernel(const TokenWriteP
     }
     __syncthreads();
     grid_launch_dependents();
+    TokenPlace place{-1, 0, 0};
+    if (tok < nt)
+        place = s_place[tok];
+    const bool live = place.pos >= 0;
+    const size_t slot = ((size_t)place.slot_hi << 32) | place.slot_lo;
+    float4 c01 = make_float4(1.f, 0.f, 1.f, 0.f), c23 = c01;
+    if (p.rope != nullptr && live) {
+        const float4 *cs =
+            reinterpret_cast<const float4 *>(p.rope + (size_t)place.pos * D) + lane * 2;
+        c01 = cs[0];
+        c23 = cs[1];
+    }
 
-    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    const int nv = p.Hq + 2 * p.Hkv;         // vectors of a token: q, k, v heads
-    const int total = nt * nv;
-    // every lane runs the same number of rounds: the shuffles need whole warps
-    for (int i0 = 0; i0 < total; i0 += GROUPS) {
-        const int i = i0 + group;
-        const bool in = i < total;
-        const int tok = in ? i / nv : 0;
-        int h = in ? i - tok * nv : 0;
-        const TokenPlace place = s_place[tok];
-        const bool live = in && place.pos >= 0;
-        const size_t t = (size_t)(t0 + tok);
-        const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;   // q, k, v
-        h -= kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.Hkv;
-        const __nv_bfloat16 *src = kind == 0   ? p.q + t * p.q_stride
-                                   : kind == 1 ? p.k + t * p.k_stride
-                                               : p.v + t * p.v_stride;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (live)
-            raw = *reinterpret_cast<const uint4 *>(src + h * D + lane * 8);
-        float x[8];
-        x[0] = bf16_lo(raw.x); x[1] = bf16_hi(raw.x);
-        x[2] = bf16_lo(raw.y); x[3] = bf16_hi(raw.y);
-        x[4] = bf16_lo(raw.z); x[5] = bf16_hi(raw.z);
-        x[6] = bf16_lo(raw.w); x[7] = bf16_hi(raw.w);
-
-        float ss = 0.f;
+    // query heads; every lane runs the same rounds, as the shuffles need whole warps
+    {
+        const Turn turn = turn_of(c01, c23, unpack(wq));
+        __nv_bfloat16 *dst = p.q_out + (t * p.Hq) * D + lane * 8;
+        for (int h0 = 0; h0 < p.Hq; h0 += kQ * width) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            ss = fmaf(x[j], x[j], ss);
-        ss = group_sum<LANES>(ss);
-        const __nv_bfloat16 *w = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
-        if (w != nullptr) {
-            const uint4 wr = *reinterpret_cast<const uint4 *>(w + lane * 8);
-            const float f = rsqrtf(ss * (1.f / D) + p.norm_eps);
-            x[0] *= f * bf16_lo(wr.x); x[1] *= f * bf16_hi(wr.x);
-            x[2] *= f * bf16_lo(wr.y); x[3] *= f * bf16_hi(wr.y);
-            x[4] *= f * bf16_lo(wr.z); x[5] *= f * bf16_hi(wr.z);
-            x[6] *= f * bf16_lo(wr.w); x[7] *= f * bf16_hi(wr.w);
+            for (int u = 0; u < kQ; ++u) {
+                const int h = h0 + u * width + v0;
+                Eight x = unpack(rq[u]);
+                rq[u] = load(q, h + kQ * width, p.Hq);
+                const float f = p.q_norm != nullptr ? norm_factor<D>(x, p.norm_eps) : 1.f;
+                apply(x, turn, p.rope != nullptr);
+                if (live && h < p.Hq)
+                    *reinterpret_cast<uint4 *>(dst + h * D) = pack(x, f);
+            }
         }
-        if (kind != 2 && p.rope != nullptr && live) {
-            const float4 *cs = reinterpret_cast<const float4 *>(p.rope + (size_t)place.pos * D) +
-                               lane * 2;
-            const float4 c01 = cs[0], c23 = cs[1];
-            rotate(x[0], x[1], c01.x, c01.y);
-            rotate(x[2], x[3], c01.z, c01.w);
-            rotate(x[4], x[5], c23.x, c23.y);
-            rotate(x[6], x[7], c23.z, c23.w);
-        }
-        const size_t slot = ((size_t)place.slot_hi << 32) | place.slot_lo;
-        if constexpr (Q8) {
-            float amax = 0.f;
+    }
+    // K and V heads
+    const Turn turn = turn_of(c01, c23, unpack(wk));
+    for (int h0 = 0; h0 < p.Hkv; h0 += kKv * width) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                amax = fmaxf(amax, fabsf(x[j]));
-            amax = group_max<LANES>(amax);
-            if (kind != 0) {
-                const int sb = q8_scale_byte(amax);
-                const uint2 codes = q8_encode8(x, sb);
-                if (live) {
-                    uint8_t *dst = static_cast<uint8_t *>(kind == 1 ? p.k_pool : p.v_pool);
-                    *reinterpret_cast<uint2 *>(dst + (slot * p.Hkv + h) * D + lane * 8) = codes;
-                    if (lane == 0)
-                        (kind == 1 ? p.k_scale : p.v_scale)[slot * p.Hkv + h] = (uint8_t)sb;
+        for (int u = 0; u < kKv; ++u) {
+            const int h = h0 + u * width + v0;
+            const uint4 vraw = rv[u];
+            Eight x = unpack(rk[u]);
+            rk[u] = load(k, h + kKv * width, p.Hkv);
+            rv[u] = load(v, h + kKv * width, p.Hkv);
+            const float f = p.k_norm != nullptr ? norm_factor<D>(x, p.norm_eps) : 1.f;
+            apply(x, turn, p.rope != nullptr);
+            const bool store = live && h < p.Hkv;
+            const size_t head = slot * p.Hkv + h;
+            if constexpr (Q8) {
+                int sk, sv;
+                const uint2 kc = quantise<D>(x, f, sk);
+                const uint2 vc = quantise<D>(unpack(vraw), 1.f, sv);
+                if (store) {
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.k_pool) + head * D +
+                                               lane * 8) = kc;
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.v_pool) + head * D +
+                                               lane * 8) = vc;
+                    if (lane == 0) {
+                        p.k_scale[head] = (uint8_t)sk;
+                        p.v_scale[head] = (uint8_t)sv;
+                    }
                 }
+            } else if (store) {
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.k_pool) + head * D +
+                                           lane * 8) = pack(x, f);
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.v_pool) + head * D +
+                                           lane * 8) = vraw;
             }
-        }
-        if (kind == 0 || !Q8) {
-            uint4 y = raw;                       // V: unchanged
-            if (kind != 2) {
-                y.x = pack_bf16x2(x[0], x[1]);
-                y.y = pack_bf16x2(x[2], x[3]);
-                y.z = pack_bf16x2(x[4], x[5]);
-                y.w = pack_bf16x2(x[6], x[7]);
-            }
-            __nv_bfloat16 *dst =
-                kind == 0 ? p.q_out + (t * p.Hq + h) * D
-                          : static_cast<__nv_bfloat16 *>(kind == 1 ? p.k_pool : p.v_pool) +
-                                (slot * p.Hkv + h) * D;
-            if (live)
-                *reinterpret_cast<uint4 *>(dst + lane * 8) = y;
         }
     }
 }
@@ -207,9 +347,20 @@ __global__ void __launch_bounds__(kThreads) token_write_kernel(const TokenWriteP
 template <int D, bool Q8, bool EXTEND>
 cudaError_t launch(const TokenWriteParams &params, cudaStream_t stream)
 {
+    constexpr int kGroupsShift = D == 64 ? 5 : 4;       // groups of a block
     TokenWriteParams p = params;
-    p.per_block = EXTEND ? 4 : 1;
-    const unsigned blocks = (unsigned)((p.T + p.per_block - 1) / p.per_block);
+    // As many groups a token as it has vectors of a kind, for few tokens; with
+    // more tokens than fill the GPU a dozen times over, fewer, which then share
+    // the coefficients among more vectors.
+    const int heads = p.Hq > p.Hkv ? p.Hq : p.Hkv;
+    p.width_shift = 0;
+    while (p.width_shift < kGroupsShift && (1 << p.width_shift) < heads)
+        ++p.width_shift;
+    while (p.width_shift > 0 && (heads >> p.width_shift) < 8 &&
+           (p.T >> (kGroupsShift - p.width_shift + 1)) >= kManyBlocks)
+        --p.width_shift;
+    const int at_once = 1 << (kGroupsShift - p.width_shift);
+    const unsigned blocks = (unsigned)((p.T + at_once - 1) / at_once);
     return launch_pdl(token_write_kernel<D, Q8, EXTEND>, dim3(blocks), dim3(kThreads), 0, stream,
                       p);
 }
