@@ -82,6 +82,8 @@ _lib = None
 def lib():
     """Load libpkv.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -157,10 +159,24 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_current_stream = None
+
+
+def _current_raw_stream():
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        # torch's own shortcut past the Stream object (3 us a call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        device = torch.cuda.current_device
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -368,9 +384,10 @@ def paged_kv_extend(d: Dims, q, k_new, v_new, qo_indptr, k_pool, v_pool, kv_indi
 def _rows(x, name: str):
     """(pointer, row stride) of new-token rows [T, H, D] whose heads are packed."""
     T, H, D = x.shape
-    if x.stride(2) != 1 or (H > 1 and x.stride(1) != D):
+    row, head, one = x.stride()
+    if one != 1 or (head != D and H > 1):
         raise ValueError(f"{name} must be [tokens, heads, D] with packed heads")
-    return x.data_ptr(), x.stride(0) if T > 1 else 0
+    return x.data_ptr(), row if T > 1 else 0
 
 
 def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6,
@@ -380,21 +397,23 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
     row stride (slices of one projection's output), q_out [T, Hq, D] for the
     processed queries (None: in place, which needs a packed q), optional [D]
     norm weights, and the RoPE table."""
-    t = Tokens(norm_eps=norm_eps, rope_max_pos=rope_max_pos)
-    if q is not None:
-        t.q, t.q_stride = _rows(q, "q")
-        t.q_out = t.q if q_out is None else _ptr(q_out)
-        t.q_norm = _ptr(q_norm)
-        if q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
-            raise ValueError("q and k must have the same tokens and head size")
-    if k.shape != v.shape:
+    T, Hkv, D = shape = k.shape
+    if shape != v.shape:
         raise ValueError("k and v must have the same shape")
-    t.k, t.k_stride = _rows(k, "k")
-    t.v, t.v_stride = _rows(v, "v")
-    t.k_norm = _ptr(k_norm)
-    t.rope_cos_sin = _ptr(rope_cos_sin)
-    t.shape = (int(k.shape[0]), None if q is None else int(q.shape[1]), int(k.shape[1]),
-               int(k.shape[2]))
+    kp, k_row = _rows(k, "k")
+    vp, v_row = _rows(v, "v")
+    if q is None:
+        Hq = qp = out = q_norm = None
+        q_row = 0
+    else:
+        qT, Hq, qD = q.shape
+        if qT != T or qD != D:
+            raise ValueError("q and k must have the same tokens and head size")
+        qp, q_row = _rows(q, "q")
+        out = qp if q_out is None else _ptr(q_out)
+    t = Tokens(qp, kp, vp, q_row, k_row, v_row, out, _ptr(q_norm), _ptr(k_norm), norm_eps,
+               _ptr(rope_cos_sin), rope_max_pos)
+    t.shape = (T, Hq, Hkv, D)
     t.tensors = (q, k, v, q_out, q_norm, k_norm, rope_cos_sin)
     return t
 
