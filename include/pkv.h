@@ -567,10 +567,10 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
  * call (paged_decode_plan serves both caches).  Scales as the writes above
  * choose them, or any in [127 - 40, 127 + 40]; the output of a row holding
  * others is undefined.  One persistent kernel plus, when num_splits > 1, the
- * piece combine; a batch of more than 2048 rows x kv-head groups (a group: 8,
+ * piece combine; a batch of more than 1024 rows x kv-head groups (a group: 8,
  * 4, 2 or 1 kv heads, the most that divide Hkv) takes several such pairs, one
- * after the other.  PKV_ERR_UNSUPPORTED: Hkv of more than 2048 groups, or
- * max_seq_len x groups past 2^31. */
+ * after the other.  PKV_ERR_UNSUPPORTED: Hkv of more than 1024 groups, or
+ * max_seq_len x groups or num_pages x page_size past 2^31. */
 pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
                                 const void *v_codes, const void *k_scale, const void *v_scale,
                                 const int32_t *kv_indices, const int32_t *kv_indptr,

@@ -1130,6 +1130,9 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
     const int most = (int)(by_weight < by_rows ? by_weight : by_rows);
     if (most < 1)
         return PKV_ERR_UNSUPPORTED;
+    // the kernel counts a pool's token slots in 31 bits
+    if ((long long)dims->num_pages * dims->page_size >= (1ll << 31))
+        return PKV_ERR_UNSUPPORTED;
     char *ws = static_cast<char *>(workspace);
     int32_t *plan = reinterpret_cast<int32_t *>(ws + L.plan_off);
     const bool one = dims->B <= most;

@@ -273,8 +273,8 @@ struct FusedParams {
 };
 
 // Rows x kv-head groups of one launch over the 8-bit cache (pkv_q8_decode.cu),
-// whose ring of stages needs the room of the other half's prefix sums.
-constexpr int kQ8MaxRows = 2048;
+// whose ring of stages needs the room of more prefix sums.
+constexpr int kQ8MaxRows = 1024;
 
 // Threads of a plan block.
 constexpr int kPlanThreads = 256;

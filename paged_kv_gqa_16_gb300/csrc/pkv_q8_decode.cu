@@ -35,14 +35,17 @@
 //    stage and have sums of their own, joined in pairs through shared memory at
 //    the end of a piece.  A warp takes two stages at a time: the products and
 //    exponentials of one overlap those of the other.
-//  - Copies.  Pages of a multiple of 8 tokens come as TMA boxes of {D bytes,
-//    8 or 16 tokens, HPC heads}, which lie head by head in the stage, swizzled
-//    so that eight tokens' vectors of a head are in different banks: one copy
-//    a page and pool.  (One copy a token, as the bf16 decode makes them, sets
-//    the pace here: 86 us of copies alone for 322 MB, serving batch of 128,
-//    against 47.5 us at the measured copy bandwidth.)  A box may reach over
-//    the piece's ends; those tokens weigh nothing.  Other page sizes take one
-//    copy a token into padded rows.
+//  - Copies.  BOX: pages of a multiple of 8 tokens come as TMA boxes of
+//    {128 bytes, 8 or 16 tokens, HPC D / 128}: 128-byte rows (a head of D = 128,
+//    two of D = 64), head by head in the stage and swizzled so that eight
+//    tokens' vectors of a head are in different banks, one copy a page and
+//    pool.  (One bulk copy a token, as the bf16 decode makes them, sets the pace
+//    here: 86 us of copies alone for 322 MB, the serving batch of 128, against
+//    47.5 us at the measured copy bandwidth.)  LINE: other pages, and tokens of
+//    less than 256 bytes (the copy engine takes 6 to 8 cycles a row), come in
+//    16-byte asynchronous copies by the producers' lanes, token by token in the
+//    stage, swizzled the same way.  A box may reach over the piece's ends; those
+//    tokens weigh nothing.
 #include <cmath>
 
 #include "pkv_partition.cuh"
@@ -53,29 +56,31 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 8;                 // consumer warps
-constexpr int kProducers = 2;             // producer warps, a stage each in turn
 constexpr float kRaise = 8.f;             // how far a score may exceed its base
+constexpr int kBoxBytes = 256;            // a token's bytes of HPC heads from which boxes are used
 
 struct Q8Params {
     FusedParams f;
-    // the pools as {D, tokens, Hkv} bytes with boxes {D, box tokens, HPC}
+    // BOX: the pools as {128, tokens, Hkv D / 128} bytes in boxes of
+    // {128, 1 << box_shift, HPC D / 128}
     CUtensorMap map_k, map_v;
-    int box_shift;                        // log2 of a box's tokens (TILED)
+    int box_shift;
 };
 
-template <int D, int HPC, int NT, bool TILED>
+template <int D, int HPC, int NT, bool BOX>
 struct Q8Cfg {
     static constexpr int kWph = kWarps / HPC;         // warps of a kv head
     static constexpr int kTok = 16 * kWph;            // tokens of a stage
     // stages a warp takes at a time: two chains of products and exponentials
     // to overlap, where the registers allow it
     static constexpr int kTake = NT == 1 ? 2 : 1;
+    // producer warps, a stage each in turn: LINE has two thousand copies a stage
+    static constexpr int kProducers = BOX ? 2 : D == 64 ? 4 : 3;
     static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kRowBytes = HPC * D;         // one token, HPC kv heads
-    // rows: an odd number of 16-byte units, so that eight tokens' vectors of
-    // one head lie in different banks
-    static constexpr int kPitch = TILED ? kRowBytes : kRowBytes + 16;
-    static constexpr int kStageBytes = 2 * kTok * kPitch;
+    static constexpr int kHeadsRow = 128 / D;         // heads of a box's 128-byte row
+    static_assert(!BOX || HPC % kHeadsRow == 0, "whole rows");
+    static constexpr int kStageBytes = 2 * kTok * kRowBytes;
     static constexpr int kScaleBytes = 2 * kTok * 8;  // 8 bytes a token, K then V
     // joining parts: half of them leave half of their registers, a slot a warp
     static constexpr int kJoinFloats = NT * (D / 16 * 2 + 2);
@@ -83,11 +88,11 @@ struct Q8Cfg {
     static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 16;
     static constexpr int kStagesFit =
         (kSmemLimit - kFixedBytes) / (kStageBytes + kScaleBytes + 16);
-    // An even number of stages: a slot then always belongs to the same producer
-    // warp.  With an odd one a producer could reach a slot before the other had
-    // filled it for its previous use, and take the parity of the use before
-    // that for its own.
-    static constexpr int kStages = kStagesFit > 10 ? 10 : kStagesFit / 2 * 2;
+    // A multiple of the producers: a slot then always belongs to the same one.
+    // Otherwise a producer could reach a slot before another had filled it for
+    // its previous use, and take the parity of the use before that for its own.
+    static constexpr int kStages =
+        (kStagesFit > 10 ? 10 : kStagesFit) / kProducers * kProducers;
     static_assert(kStages >= 4 && kStages % kProducers == 0, "a slot has one producer");
     static constexpr int kScaleOffset = kStages * kStageBytes;
     static constexpr int kJoinOffset = kScaleOffset + kStages * kScaleBytes;
@@ -96,8 +101,8 @@ struct Q8Cfg {
     static constexpr int kPrefixOffset = kAbortOffset + 16;
     static constexpr int kSmemBytes = kPrefixOffset + (kQ8MaxRows + 1) * 4;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
-    static_assert(!TILED || kStageBytes % 1024 == 0, "swizzled boxes");
-    static_assert(kStageBytes % 16 == 0 && kJoinBytes % 16 == 0, "alignment");
+    static_assert(kStageBytes % 1024 == 0, "swizzled rows");
+    static_assert(kJoinBytes % 16 == 0, "alignment");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -144,6 +149,14 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
                  : "memory");
 }
 
+// 16 bytes global -> shared.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint64_t policy)
+{
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(src), "l"(policy)
+                 : "memory");
+}
+
 // Four or eight bytes global -> shared, of which the first `bytes` are read
 // (the others are zero).
 template <int SIZE>
@@ -154,23 +167,24 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src, int bytes)
                  : "memory");
 }
 
-// Box {D bytes, tokens, heads} at (0, token, head) of a tensor map.
+// The box at (0, token, 128-byte row of the token) of a tensor map.
 __device__ __forceinline__ void box_copy_g2s(void *dst, const CUtensorMap *map, int token,
-                                             int head, uint64_t *bar, uint64_t policy)
+                                             int row, uint64_t *bar, uint64_t policy)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(head), "r"(smem_addr(bar)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(row), "r"(smem_addr(bar)),
         "l"(policy)
         : "memory");
 }
 
-template <int D, int HPC, int NT, bool TILED>
-__global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
+template <int D, int HPC, int NT, bool BOX>
+__global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
     decode_q8_kernel(const __grid_constant__ Q8Params params)
 {
-    using C = Q8Cfg<D, HPC, NT, TILED>;
+    using C = Q8Cfg<D, HPC, NT, BOX>;
+    constexpr int kProducers = C::kProducers;
     constexpr int NST = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
     const FusedParams &p = params.f;
@@ -184,10 +198,16 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
     const int cta = blockIdx.x;
     const int Bv = p.Bv;
     const int box = 1 << params.box_shift;
+    // LINE: byte b of token t's row, 16-byte units permuted within 128 bytes so
+    // that the units of eight tokens at one column are in different banks
+    auto line_addr = [](int t, int b) {
+        return (uint32_t)(t * C::kRowBytes + b) ^
+               (uint32_t)((C::kRowBytes >= 128 ? t : t >> 1) & 7) << 4;
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&full[i], 64);     // every producer lane, and its scale copies
+            mbar_init(&full[i], 33);     // a producer warp, and each of its lanes' copies
             mbar_init(&empty[i], kWarps);
         }
         fence_mbar_init();
@@ -253,15 +273,15 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
 
     if (warp >= kWarps) {
         // ======================= producer warps ===========================
-        // Stage i belongs to warp i % kProducers.  Lanes 0-15 copy K, 16-31 V:
-        // TILED, a box each of the stage's kTok / box; else a token each of 16.
+        // Stage i belongs to warp i % kProducers.  BOX: lane l < 16 copies the
+        // stage's box l of K, lane 16 + l that of V.  LINE: lane l looks up tokens
+        // l, 32 + l, ...; the copies take their slots from it.
         const int pw = warp - kWarps;
         const uint64_t policy = policy_evict_first();
-        const int my_t = lane & 15;
+        const int my_box = lane & 15;
         const bool my_v = lane >= 16;
-        const uint8_t *scales = my_v ? p.v_scale : p.k_scale;
         const size_t scale_bytes = (size_t)p.num_pages * p.page_size * p.Hkv;
-        constexpr int IDS = TILED ? 1 : C::kWph;      // page ids a lane holds for a stage
+        constexpr int IDS = BOX ? 1 : (C::kTok + 31) / 32;   // page ids a lane holds
         int it = 0;
         bool aborted = false;
         auto page_of_tok = [&](int t) {
@@ -291,12 +311,12 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                                  : lane == 6 ? start : end;
                 }
             }
-            const int ta = TILED ? t0 & -box : t0;     // a piece's first stage starts here
+            const int ta = BOX ? t0 & -box : t0;     // a piece's first stage starts here
             // the table's entry for this lane's box (token) of the stage at tok
-            auto load_id = [&](int tok, int sub) {
-                const int t = TILED ? tok + (my_t << params.box_shift) : tok + sub * 16 + my_t;
-                const bool there = t < t1 && (!TILED || (my_t << params.box_shift) < C::kTok);
-                const int pi = page_of_tok(there ? t : 0);
+            auto load_id = [&](int tok, int k) {
+                const int at = BOX ? my_box << params.box_shift : k * 32 + lane;
+                const bool there = at < C::kTok && tok + at < t1;
+                const int pi = page_of_tok(there ? tok + at : 0);
                 return there && pi < npg ? __ldg(p.kv_indices + pg0 + pi) : 0;
             };
             int ids[IDS];
@@ -331,68 +351,101 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                 unsigned char *stage = smem + st * C::kStageBytes;
                 unsigned char *sc0 = smem + C::kScaleOffset + st * C::kScaleBytes;
                 const int nvalid = min(C::kTok, t1 - tok);
-                if constexpr (TILED) {
+                // a page id of a token that is there, checked
+                auto checked = [&](int page, bool there) {
+                    if (page < 0 || page >= p.num_pages) {
+                        if (there)
+                            atomicOr(p.status, kFlagBadPage);
+                        page = 0;
+                    }
+                    return page;
+                };
+                // a token's HPC scale bytes of one pool
+                auto copy_scale = [&](const uint8_t *scales, int row, size_t head) {
+                    unsigned char *sc = sc0 + row * 8;
+                    if constexpr (HPC == 8) {
+                        cp_async<8>(sc, scales + head, 8);
+                    } else if constexpr (HPC == 4) {
+                        cp_async<4>(sc, scales + head, 4);
+                    } else {
+                        // the aligned word around the HPC bytes, and where they are in it
+                        const size_t word = head & ~(size_t)3;
+                        const size_t left = scale_bytes - word;
+                        cp_async<4>(sc, scales + word, left < 4 ? (int)left : 4);
+                        sc[4] = (unsigned char)(head & 3);
+                    }
+                };
+                if constexpr (BOX) {
                     const int boxes = (nvalid + box - 1) >> params.box_shift;
                     if (lane == 0)
                         mbar_expect_tx(&full[st],
                                        (uint32_t)(boxes * box) * (2u * C::kRowBytes));
-                    int page = ids[0];
-                    const int tb = tok + (my_t << params.box_shift);
-                    if (my_t < boxes) {
-                        if (page < 0 || page >= p.num_pages) {
-                            atomicOr(p.status, kFlagBadPage);
-                            page = 0;
-                        }
-                        box_copy_g2s(stage + ((my_v ? C::kTok : 0) + (my_t << params.box_shift)) *
-                                                 C::kRowBytes,
+                    const int at = my_box << params.box_shift, tb = tok + at;
+                    const int page = checked(ids[0], my_box < boxes);
+                    if (my_box < boxes)
+                        box_copy_g2s(stage + ((my_v ? C::kTok : 0) + at) * C::kRowBytes,
                                      my_v ? &params.map_v : &params.map_k,
                                      page * p.page_size + (tb - page_of_tok(tb) * p.page_size),
-                                     hg * HPC, &full[st], policy);
-                    }
-                    ids[0] = page;
-                } else {
-                    if (lane == 0)
-                        mbar_expect_tx(&full[st], (uint32_t)(nvalid * 2 * C::kRowBytes));
-                }
+                                     hg * (HPC / C::kHeadsRow), &full[st], policy);
+                    // scales: 16 tokens of K (lanes 0-15) and of V at a time
 #pragma unroll
-                for (int sub = 0; sub < C::kWph; ++sub) {
-                    if (sub * 16 >= nvalid)
-                        break;
-                    const int row = sub * 16 + my_t, t = tok + row;
-                    const bool there = t < t1;
-                    int page = TILED ? __shfl_sync(kFull, ids[0],
-                                                   (row >> params.box_shift) + (lane & 16))
-                                     : ids[TILED ? 0 : sub];
-                    const int srow = (my_v ? C::kTok : 0) + row;
-                    if (there) {
-                        if (!TILED && (page < 0 || page >= p.num_pages)) {
-                            atomicOr(p.status, kFlagBadPage);
-                            page = 0;
+                    for (int sub = 0; sub < C::kTok; sub += 16) {
+                        if (sub >= nvalid)
+                            break;
+                        const int row = sub + my_box, t = tok + row;
+                        const int pg = __shfl_sync(kFull, page,
+                                                   (row >> params.box_shift) + (lane & 16));
+                        if (t < t1)
+                            copy_scale(my_v ? p.v_scale : p.k_scale, (my_v ? C::kTok : 0) + row,
+                                       ((size_t)pg * p.page_size +
+                                        (t - page_of_tok(t) * p.page_size)) * (size_t)p.Hkv +
+                                           (size_t)hg * HPC);
+                    }
+                } else {
+                    constexpr int CH = C::kRowBytes / 16;      // 16-byte lines of a token
+                    const size_t line0 = (size_t)hg * C::kRowBytes;
+                    const unsigned tok_bytes = (unsigned)(p.Hkv * D);
+#pragma unroll
+                    for (int k = 0; k < IDS; ++k) {
+                        if (k * 32 >= nvalid)
+                            break;
+                        const int row = k * 32 + lane, t = tok + row;
+                        const bool there = row < nvalid;
+                        const int page = checked(ids[k], there);
+                        const int slot = page * p.page_size +
+                                         (there ? t - page_of_tok(t) * p.page_size : 0);
+                        if (there) {
+                            const size_t head = (size_t)slot * p.Hkv + (size_t)hg * HPC;
+                            copy_scale(p.k_scale, row, head);
+                            copy_scale(p.v_scale, C::kTok + row, head);
                         }
-                        const size_t head =
-                            ((size_t)page * p.page_size + (t - page_of_tok(t) * p.page_size)) *
-                                (size_t)p.Hkv +
-                            (size_t)hg * HPC;
-                        if constexpr (!TILED)
-                            bulk_copy_g2s_hint(stage + srow * C::kPitch,
-                                               (my_v ? p.v_codes : p.k_codes) + head * D,
-                                               C::kRowBytes, &full[st], policy);
-                        unsigned char *sc = sc0 + srow * 8;
-                        if constexpr (HPC == 8) {
-                            cp_async<8>(sc, scales + head, 8);
-                        } else if constexpr (HPC == 4) {
-                            cp_async<4>(sc, scales + head, 4);
-                        } else {
-                            // the aligned word around the HPC bytes, and where they are in it
-                            const size_t word = head & ~(size_t)3;
-                            const size_t left = scale_bytes - word;
-                            cp_async<4>(sc, scales + word, left < 4 ? (int)left : 4);
-                            sc[4] = (unsigned char)(head & 3);
+                        // 32 lines at a time, 32 / CH tokens' (or part of one): line
+                        // 32 j + lane lies at byte 16 (32 j + lane) of these tokens'
+                        // rows, its swizzle that of the lane and of j (no carry)
+                        constexpr int ROUNDS = (C::kTok < 32 ? C::kTok : 32) * CH / 32;
+                        constexpr int HALF = C::kRowBytes >= 128 ? 0 : 1;
+                        const uint32_t lane_key = (uint32_t)((lane / CH) >> HALF & 7) << 4;
+                        const uint32_t to = smem_addr(stage) + k * 32 * C::kRowBytes;
+#pragma unroll
+                        for (int j = 0; j < ROUNDS; ++j) {
+                            const int from = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
+                            const unsigned s_ = (unsigned)__shfl_sync(kFull, slot, from);
+                            if (k * 32 + from < nvalid) {
+                                const size_t off = (size_t)s_ * tok_bytes + (line0 + ch * 16);
+                                const uint32_t dst =
+                                    to + j * 512 +
+                                    ((lane * 16u) ^ lane_key ^
+                                     (uint32_t)((j * 32 / CH) >> HALF & 7) << 4);
+                                cp_async16(dst, p.k_codes + off, policy);
+                                cp_async16(dst + C::kTok * C::kRowBytes, p.v_codes + off, policy);
+                            }
                         }
                     }
                 }
                 cp_async_arrive(&full[st]);
-                mbar_arrive(&full[st]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&full[st]);
 #pragma unroll
                 for (int k = 0; k < IDS; ++k)
                     ids[k] = next[k];
@@ -416,20 +469,32 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
     // 16-byte column l / 16 of each two.  For V the tokens are in the order in
     // which the weights' operand has them: 2c, 2c + 1, 2c + 8, 2c + 9 of c = 0..3.
     auto token_addr = [&](int t) {
-        const uint32_t col = (uint32_t)(lane >> 4) * 16;
-        if constexpr (TILED) {
-            const int row = ((((t >> params.box_shift) * HPC + hw) << params.box_shift) |
-                             (t & (box - 1)));
-            return (uint32_t)(row * D) + (col ^ (uint32_t)(D == 128 ? row & 7 : (row >> 1) & 3) << 4);
+        uint32_t col = (uint32_t)(lane >> 4) * 16;
+        if constexpr (BOX) {
+            constexpr int HR = C::kHeadsRow;
+            const int row = ((((t >> params.box_shift) * (HPC / HR) + hw / HR)
+                              << params.box_shift) | (t & (box - 1)));
+            col += (uint32_t)(hw % HR) * D;
+            return (uint32_t)(row * 128) + (col ^ (uint32_t)(row & 7) << 4);
         } else {
-            return (uint32_t)(t * C::kPitch + hw * D) + col;
+            return line_addr(t, hw * D + (int)col);
         }
     };
-    // the 32-byte column i of a row whose first is at `addr` (TILED: the
-    // swizzle is in the same bits)
-    auto column = [](uint32_t addr, int i) { return TILED ? addr ^ (i * 32u) : addr + i * 32u; };
+    // the 32-byte column i of a row whose first is at `addr`: the swizzle is in
+    // the same bits
+    auto column = [](uint32_t addr, int i) { return addr ^ (i * 32u); };
     const uint32_t k_off = smem_s + token_addr(tg * 16 + (lane & 15));
-    const uint32_t v_off = k_off + C::kTok * C::kPitch;
+    const uint32_t v_off = k_off + C::kTok * C::kRowBytes;
+    // lane (g, c)'s elements of head 8 nt + g of row r
+    auto load_q = [&](uint2 (&raw)[D / 16], int r, int nt) {
+        const int h = nt * 8 + g;
+        const __nv_bfloat16 *src =
+            p.q + ((size_t)(r % p.B) * p.Hq + (size_t)(r / p.B * HPC + hw) * p.n_rep + h) * D;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+            raw[j] = h < p.n_rep ? __ldg(reinterpret_cast<const uint2 *>(src) + j * 4 + c)
+                                 : make_uint2(0u, 0u);
+    };
     int it = 0;
     bool aborted = false;
 
@@ -449,17 +514,13 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
         float cq[NT][2];                   // factors of heads 2c, 2c + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + g;
             uint2 raw[D / 16];
+            load_q(raw, r, nt);
             float amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                raw[j] = h < p.n_rep
-                             ? __ldg(reinterpret_cast<const uint2 *>(p.q + (qrow0 + h) * D) + j * 4 + c)
-                             : make_uint2(0u, 0u);
+            for (int j = 0; j < D / 16; ++j)
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(raw[j].x)), fabsf(bf16_hi(raw[j].x))),
                                          fmaxf(fabsf(bf16_lo(raw[j].y)), fabsf(bf16_hi(raw[j].y)))));
-            }
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
             // 2^-n, n the exponent of amax, both powers kept in the normal range
@@ -486,10 +547,10 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                 oacc[nt][j][0] = oacc[nt][j][1] = oacc[nt][j][2] = oacc[nt][j][3] = 0.f;
         }
 
-        for (int tok = TILED ? t0 & -box : t0; tok < t1;) {
+        for (int tok = BOX ? t0 & -box : t0; tok < t1;) {
             constexpr int U = C::kTake;
-            // this turn's stages: U, or one before the piece's end
-            const int take = U == 2 && tok + C::kTok < t1 ? 2 : 1;
+            // this turn's stages: U, or as many as the piece has left
+            const int take = U == 1 ? 1 : min(U, (t1 - tok + C::kTok - 1) / C::kTok);
             uint32_t stage[U];
             const unsigned char *sc[U];
 #pragma unroll
@@ -510,7 +571,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                 }
             }
             // tokens [v0, v1) of this warp's 16 of the first stage belong to the
-            // piece, [v0, v1) - kTok of the second (none of a stage not taken)
+            // piece, [v0, v1) - u kTok of stage u (none of a stage not taken)
             const int v0 = t0 - tok - tg * 16, v1 = t1 - tok - tg * 16;
             if (!aborted && v1 > 0 && v0 < 16 + (U - 1) * C::kTok) {
                 // S^T = K q, in two sums: a word of four codes gives two pairs of f16,
@@ -596,8 +657,9 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             float mx = fmaxf(y[nt][0][e], y[nt][0][e + 2]);
-                            if (U == 2)
-                                mx = fmaxf(mx, fmaxf(y[nt][U - 1][e], y[nt][U - 1][e + 2]));
+#pragma unroll
+                            for (int u = 1; u < U; ++u)
+                                mx = fmaxf(mx, fmaxf(y[nt][u][e], y[nt][u][e + 2]));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
@@ -657,11 +719,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
                     }
             }
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&empty[it % NST]);
-                if (U == 2 && take == 2)
-                    mbar_arrive(&empty[(it + 1) % NST]);
-            }
+            if (lane < take)
+                mbar_arrive(&empty[(it + lane) % NST]);
             tok += take * C::kTok;
             it += take;
         }
@@ -755,49 +814,48 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, TILED>::kThreads, 1)
     grid_launch_dependents();
 }
 
-template <int D, int HPC, int NT, bool TILED>
+template <int D, int HPC, int NT, bool BOX>
 cudaError_t launch(const Q8Params &p, int grid, cudaStream_t stream)
 {
-    using C = Q8Cfg<D, HPC, NT, TILED>;
+    using C = Q8Cfg<D, HPC, NT, BOX>;
     static DeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        cudaError_t r = cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, TILED>,
+        cudaError_t r = cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, BOX>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemBytes);
         if (r != cudaSuccess)
             return r;
-        return cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, TILED>,
+        return cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, BOX>,
                                     cudaFuncAttributePreferredSharedMemoryCarveout,
                                     cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(decode_q8_kernel<D, HPC, NT, TILED>, dim3(grid), dim3(C::kThreads),
+    return launch_pdl(decode_q8_kernel<D, HPC, NT, BOX>, dim3(grid), dim3(C::kThreads),
                       C::kSmemBytes, stream, p);
 }
 
-// Boxes of 16 tokens (8 where a page is not a multiple of 16) if the pages
-// hold whole boxes and a token's index fits the copy's 32-bit coordinate.
-template <int D>
+// Boxes of 16 tokens (8 where a page is not a multiple of 16) if pages hold
+// whole boxes and a driver encodes them.
+template <int D, int HPC>
 bool box_maps(Q8Params &q)
 {
     const FusedParams &p = q.f;
-    const long long tokens = (long long)p.num_pages * p.page_size;
-    if (p.page_size % 8 != 0 || tokens >= (1ll << 31))
+    if (p.page_size % 8 != 0)
         return false;
     q.box_shift = p.page_size % 16 == 0 ? 4 : 3;
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr)
         return false;
-    const cuuint64_t dims[3] = {D, (cuuint64_t)tokens, (cuuint64_t)p.Hkv};
-    const cuuint64_t strides[2] = {(cuuint64_t)p.Hkv * D, D};
-    const cuuint32_t box[3] = {D, 1u << q.box_shift, (cuuint32_t)p.hpc};
+    const cuuint64_t tok_bytes = (cuuint64_t)p.Hkv * D;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)p.num_pages * p.page_size, tok_bytes / 128};
+    const cuuint64_t strides[2] = {tok_bytes, 128};
+    const cuuint32_t box[3] = {128, 1u << q.box_shift, HPC * D / 128};
     const cuuint32_t steps[3] = {1, 1, 1};
     for (int v = 0; v < 2; ++v)
         if (encode(v ? &q.map_v : &q.map_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                    const_cast<uint8_t *>(v ? p.v_codes : p.k_codes), dims, strides, box, steps,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;
@@ -807,12 +865,13 @@ bool box_maps(Q8Params &q)
 template <int D, int HPC>
 cudaError_t launch_nt(Q8Params &q, int grid, cudaStream_t stream)
 {
-    const bool tiled = box_maps<D>(q);
-    if (q.f.n_rep <= 8)
-        return tiled ? launch<D, HPC, 1, true>(q, grid, stream)
-                     : launch<D, HPC, 1, false>(q, grid, stream);
-    return tiled ? launch<D, HPC, 2, true>(q, grid, stream)
-                 : launch<D, HPC, 2, false>(q, grid, stream);
+    if constexpr (HPC * D >= kBoxBytes) {
+        if (box_maps<D, HPC>(q))
+            return q.f.n_rep <= 8 ? launch<D, HPC, 1, true>(q, grid, stream)
+                                  : launch<D, HPC, 2, true>(q, grid, stream);
+    }
+    return q.f.n_rep <= 8 ? launch<D, HPC, 1, false>(q, grid, stream)
+                          : launch<D, HPC, 2, false>(q, grid, stream);
 }
 
 template <int D>
