@@ -271,7 +271,9 @@ pkv_status launch_persistent(const pkv_dims *dims, const void *q, const void *k_
     c.Bv = L.Bv;
     c.Hq = dims->Hq;
     c.HQV = L.HQV;
-    c.planned = planned ? 1 : 0;
+    c.plan = p.plan;
+    c.grid = num_splits;
+    c.page_size = dims->page_size;
     if (adv != nullptr)
         c.adv = *adv;
     return launch_status(
@@ -1170,7 +1172,9 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
         c.Bv = p.Bv;
         c.Hq = d.Hq;
         c.HQV = L.HQV;
-        c.planned = p.plan != nullptr ? 1 : 0;
+        c.plan = p.plan;
+        c.grid = num_splits;
+        c.page_size = d.page_size;
         st = launch_status(
             pkv::launch_piece_combine(c, d.D, num_splits, (cudaStream_t)stream));
         if (st != PKV_OK)

@@ -247,8 +247,7 @@ __global__ void __launch_bounds__(FusedCfg<D, HPC>::kThreads, 1)
     int plan_r0 = 0, plan_wb = 0, plan_w0 = 0, plan_w1 = 0, plan_pg0 = 0, plan_npg = 0;
     if (p.plan != nullptr) {
         const int32_t *pe = plan_entry(p.plan, Bv, cta);
-        const int hdr_grid = p.plan[2], hdr_bv = p.plan[3];
-        const int hdr_b = p.plan[4], hdr_ps = p.plan[5];
+        const bool fits = plan_fits(p.plan, (int)gridDim.x, Bv, p.B, p.page_size);
         int e_lo = 0, e_hi = 0, e_start = 0, e_end = 0;
         if (warp == HPC) {
             const int ew = lane < 8 ? pe[lane] : 0;
@@ -267,8 +266,7 @@ __global__ void __launch_bounds__(FusedCfg<D, HPC>::kThreads, 1)
                 prefix[i] = p.plan[kPlanHeaderInts + i];
             plan_r0 = pe[0];
         }
-        planned = hdr_grid == (int)gridDim.x && hdr_bv == Bv && hdr_b == p.B &&
-                  hdr_ps == p.page_size;
+        planned = fits;
         if (planned && warp == HPC && plan_r0 >= 0) {
             // Early start: the first row's q block and first stage go out now,
             // from this block's entry alone; the compute warps meanwhile copy
@@ -836,9 +834,11 @@ __global__ void __launch_bounds__(WPH > 8 ? 32 * WPH : 256)
     }
     // With a plan, each row's first block and piece count were written by the
     // plan kernel, which completed before the decode grid passed its own
-    // wait: read them while the decode grid finishes.  Without one the decode
+    // wait: read them while the decode grid finishes.  Without one (or with one
+    // of another grid or shape, which the decode grid does not use) the decode
     // grid writes them: read them after the wait.
-    if (p.planned && live) {
+    const bool planned = p.plan != nullptr && plan_fits(p.plan, p.grid, p.Bv, p.B, p.page_size);
+    if (planned && live) {
         first = p.row_info[2 * r];
         n = p.row_info[2 * r + 1];
     }
@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(WPH > 8 ? 32 * WPH : 256)
         advance_block(p.adv);
         return;
     }
-    if (!p.planned && live) {
+    if (!planned && live) {
         first = p.row_info[2 * r];
         n = p.row_info[2 * r + 1];
     }

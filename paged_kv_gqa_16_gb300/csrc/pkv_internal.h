@@ -7,7 +7,6 @@
 #include <cstdint>
 #include <mutex>
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -72,9 +71,6 @@ inline cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, size_t smem, cuda
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, p...);
 }
-
-// cuTensorMapEncodeTiled, or nullptr when the driver has none (pkv_prefill.cu).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 struct AppendParams {
     __nv_bfloat16 *q;
@@ -293,7 +289,10 @@ struct PieceCombineParams {
     const int32_t *row_info;
     __nv_bfloat16 *out;
     int B, Bv, Hq, HQV;
-    int planned;           // row_info written by the plan kernel (read before the wait)
+    // a planned call's plan: if it is of this grid and shape, row_info is the
+    // plan's and may be read before the decode grid has completed
+    const int32_t *plan;
+    int grid, page_size;
     // paged_decode_step_advance: one extra block runs the metadata advance
     // (adv.seq_lens == nullptr: none)
     AdvanceParams adv;

@@ -142,4 +142,11 @@ __device__ __forceinline__ const int32_t *plan_entry(const int32_t *plan, int Bv
     return plan + kPlanHeaderInts + ((Bv + 1 + 3) & ~3) + (size_t)c * kPlanEntryInts;
 }
 
+// Whether a plan is of this grid and shape.
+__device__ __forceinline__ bool plan_fits(const int32_t *plan, int grid, int Bv, int B,
+                                          int page_size)
+{
+    return plan[2] == grid && plan[3] == Bv && plan[4] == B && plan[5] == page_size;
+}
+
 } // namespace pkv

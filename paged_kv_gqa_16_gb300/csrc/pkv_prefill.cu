@@ -42,6 +42,7 @@
 // Every mbarrier wait is time-bounded; tensor memory is allocated at the
 // start and released on every path.
 #include <cmath>
+#include <cudaTypedefs.h>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -1398,6 +1399,8 @@ cudaError_t launch_prefill_d(const PrefillParams &p, int sms, cudaStream_t strea
 
 } // namespace
 
+namespace {
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (the
 // library links the runtime only); nullptr when the driver has none.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
@@ -1413,8 +1416,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     }();
     return fn;
 }
-
-namespace {
 
 // A bf16 tensor [rows, mid, D] as the 3-D tiled tensor {D, mid, rows} with
 // a box of {64, box_mid, box_rows}, 128-byte swizzled.

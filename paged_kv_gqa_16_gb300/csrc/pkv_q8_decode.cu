@@ -35,17 +35,16 @@
 //    stage and have sums of their own, joined in pairs through shared memory at
 //    the end of a piece.  A warp takes two stages at a time: the products and
 //    exponentials of one overlap those of the other.
-//  - Copies.  BOX: pages of a multiple of 8 tokens come as TMA boxes of
-//    {128 bytes, 8 or 16 tokens, HPC D / 128}: 128-byte rows (a head of D = 128,
-//    two of D = 64), head by head in the stage and swizzled so that eight
-//    tokens' vectors of a head are in different banks, one copy a page and
-//    pool.  (One bulk copy a token, as the bf16 decode makes them, sets the pace
-//    here: 86 us of copies alone for 322 MB, the serving batch of 128, against
-//    47.5 us at the measured copy bandwidth.)  LINE: other pages, and tokens of
-//    less than 256 bytes (the copy engine takes 6 to 8 cycles a row), come in
-//    16-byte asynchronous copies by the producers' lanes, token by token in the
-//    stage, swizzled the same way.  A box may reach over the piece's ends; those
-//    tokens weigh nothing.
+//  - Copies.  The producers' lanes copy 16 bytes each (cp.async), 32 lines of
+//    consecutive tokens' rows at a time, and permute the 16-byte units of a row
+//    so that eight tokens' vectors of a head are in different banks.  It serves
+//    every page size and head count alike.  Copies by the copy engine were
+//    slower: one bulk copy a token, as the bf16 decode makes them, sets the pace
+//    at 1 KB a copy (86 us of copies alone for 322 MB, the serving batch of 128,
+//    against 47.5 us at the measured copy bandwidth; at 64 bytes a copy, seven
+//    times this kernel's time); boxes of 16 tokens x 128 bytes x heads took
+//    59.4 us for that batch against 58.3, 20.4 against 20.0 for a row of 32,768
+//    tokens, 54.5 against 44.4 for one kv head of 128, and no odd pages.
 #include <cmath>
 
 #include "pkv_partition.cuh"
@@ -57,29 +56,20 @@ namespace {
 
 constexpr int kWarps = 8;                 // consumer warps
 constexpr float kRaise = 8.f;             // how far a score may exceed its base
-constexpr int kBoxBytes = 256;            // a token's bytes of HPC heads from which boxes are used
 
-struct Q8Params {
-    FusedParams f;
-    // BOX: the pools as {128, tokens, Hkv D / 128} bytes in boxes of
-    // {128, 1 << box_shift, HPC D / 128}
-    CUtensorMap map_k, map_v;
-    int box_shift;
-};
-
-template <int D, int HPC, int NT, bool BOX>
+template <int D, int HPC, int NT>
 struct Q8Cfg {
     static constexpr int kWph = kWarps / HPC;         // warps of a kv head
     static constexpr int kTok = 16 * kWph;            // tokens of a stage
     // stages a warp takes at a time: two chains of products and exponentials
     // to overlap, where the registers allow it
     static constexpr int kTake = NT == 1 ? 2 : 1;
-    // producer warps, a stage each in turn: LINE has two thousand copies a stage
-    static constexpr int kProducers = BOX ? 2 : D == 64 ? 4 : 3;
+    // producer warps, a stage each in turn (of 2, 3 and 4, as far as the stages
+    // are a multiple: 66.4 us with 4 and four stages, 58.3 with 3 and six for the
+    // serving batch at D = 128; one kv head of 64: 69 us with 3, 52 with 4)
+    static constexpr int kProducers = D == 64 ? 4 : 3;
     static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kRowBytes = HPC * D;         // one token, HPC kv heads
-    static constexpr int kHeadsRow = 128 / D;         // heads of a box's 128-byte row
-    static_assert(!BOX || HPC % kHeadsRow == 0, "whole rows");
     static constexpr int kStageBytes = 2 * kTok * kRowBytes;
     static constexpr int kScaleBytes = 2 * kTok * 8;  // 8 bytes a token, K then V
     // joining parts: half of them leave half of their registers, a slot a warp
@@ -135,13 +125,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
     return d;
 }
 
-__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
-                 "r"(bytes)
-                 : "memory");
-}
-
 // This thread's earlier cp.async copies arrive on `bar` when they have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 {
@@ -167,27 +150,14 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src, int bytes)
                  : "memory");
 }
 
-// The box at (0, token, 128-byte row of the token) of a tensor map.
-__device__ __forceinline__ void box_copy_g2s(void *dst, const CUtensorMap *map, int token,
-                                             int row, uint64_t *bar, uint64_t policy)
+template <int D, int HPC, int NT>
+__global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
+    decode_q8_kernel(const __grid_constant__ FusedParams p)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(row), "r"(smem_addr(bar)),
-        "l"(policy)
-        : "memory");
-}
-
-template <int D, int HPC, int NT, bool BOX>
-__global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
-    decode_q8_kernel(const __grid_constant__ Q8Params params)
-{
-    using C = Q8Cfg<D, HPC, NT, BOX>;
+    using C = Q8Cfg<D, HPC, NT>;
     constexpr int kProducers = C::kProducers;
     constexpr int NST = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
-    const FusedParams &p = params.f;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOffset);
     uint64_t *empty = full + NST;
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kAbortOffset);
@@ -197,8 +167,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
     const int Bv = p.Bv;
-    const int box = 1 << params.box_shift;
-    // LINE: byte b of token t's row, 16-byte units permuted within 128 bytes so
+    // byte b of token t's row, 16-byte units permuted within 128 bytes so
     // that the units of eight tokens at one column are in different banks
     auto line_addr = [](int t, int b) {
         return (uint32_t)(t * C::kRowBytes + b) ^
@@ -218,8 +187,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
     // the partition, from the step's plan or computed here (as in pkv_fused.cu)
     bool planned = false;
     if (p.plan != nullptr) {
-        planned = p.plan[2] == (int)gridDim.x && p.plan[3] == Bv && p.plan[4] == p.B &&
-                  p.plan[5] == p.page_size;
+        planned = plan_fits(p.plan, (int)gridDim.x, Bv, p.B, p.page_size);
         for (int i = threadIdx.x; i <= Bv; i += C::kThreads)
             prefix[i] = p.plan[kPlanHeaderInts + i];
         __syncthreads();
@@ -273,15 +241,13 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
 
     if (warp >= kWarps) {
         // ======================= producer warps ===========================
-        // Stage i belongs to warp i % kProducers.  BOX: lane l < 16 copies the
-        // stage's box l of K, lane 16 + l that of V.  LINE: lane l looks up tokens
-        // l, 32 + l, ...; the copies take their slots from it.
+        // Stage i belongs to warp i % kProducers.  Lane l looks up the stage's
+        // tokens l, 32 + l, ... and copies their scales; the copies of the codes
+        // take the tokens' slots from it.
         const int pw = warp - kWarps;
         const uint64_t policy = policy_evict_first();
-        const int my_box = lane & 15;
-        const bool my_v = lane >= 16;
         const size_t scale_bytes = (size_t)p.num_pages * p.page_size * p.Hkv;
-        constexpr int IDS = BOX ? 1 : (C::kTok + 31) / 32;   // page ids a lane holds
+        constexpr int IDS = (C::kTok + 31) / 32;      // page ids a lane holds
         int it = 0;
         bool aborted = false;
         auto page_of_tok = [&](int t) {
@@ -311,20 +277,20 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
                                  : lane == 6 ? start : end;
                 }
             }
-            const int ta = BOX ? t0 & -box : t0;     // a piece's first stage starts here
-            // the table's entry for this lane's box (token) of the stage at tok
+            // the table's entry for this lane's token k of the stage at tok
             auto load_id = [&](int tok, int k) {
-                const int at = BOX ? my_box << params.box_shift : k * 32 + lane;
+                const int at = k * 32 + lane;
                 const bool there = at < C::kTok && tok + at < t1;
                 const int pi = page_of_tok(there ? tok + at : 0);
                 return there && pi < npg ? __ldg(p.kv_indices + pg0 + pi) : 0;
             };
+            // the ids of this warp's next stage are loaded a stage ahead
             int ids[IDS];
-            int skip = (pw - it % kProducers + kProducers) % kProducers;   // to its first stage
+            const int skip = (pw - it % kProducers + kProducers) % kProducers;
 #pragma unroll
             for (int k = 0; k < IDS; ++k)
-                ids[k] = load_id(ta + skip * C::kTok, k);
-            for (int tok = ta; tok < t1; tok += C::kTok, ++it) {
+                ids[k] = load_id(t0 + skip * C::kTok, k);
+            for (int tok = t0; tok < t1; tok += C::kTok, ++it) {
                 if (it % kProducers != pw)
                     continue;
                 const int st = it % NST;
@@ -375,70 +341,42 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
                         sc[4] = (unsigned char)(head & 3);
                     }
                 };
-                if constexpr (BOX) {
-                    const int boxes = (nvalid + box - 1) >> params.box_shift;
-                    if (lane == 0)
-                        mbar_expect_tx(&full[st],
-                                       (uint32_t)(boxes * box) * (2u * C::kRowBytes));
-                    const int at = my_box << params.box_shift, tb = tok + at;
-                    const int page = checked(ids[0], my_box < boxes);
-                    if (my_box < boxes)
-                        box_copy_g2s(stage + ((my_v ? C::kTok : 0) + at) * C::kRowBytes,
-                                     my_v ? &params.map_v : &params.map_k,
-                                     page * p.page_size + (tb - page_of_tok(tb) * p.page_size),
-                                     hg * (HPC / C::kHeadsRow), &full[st], policy);
-                    // scales: 16 tokens of K (lanes 0-15) and of V at a time
+                constexpr int CH = C::kRowBytes / 16;      // 16-byte lines of a token
+                const size_t line0 = (size_t)hg * C::kRowBytes;
+                const unsigned tok_bytes = (unsigned)(p.Hkv * D);
 #pragma unroll
-                    for (int sub = 0; sub < C::kTok; sub += 16) {
-                        if (sub >= nvalid)
-                            break;
-                        const int row = sub + my_box, t = tok + row;
-                        const int pg = __shfl_sync(kFull, page,
-                                                   (row >> params.box_shift) + (lane & 16));
-                        if (t < t1)
-                            copy_scale(my_v ? p.v_scale : p.k_scale, (my_v ? C::kTok : 0) + row,
-                                       ((size_t)pg * p.page_size +
-                                        (t - page_of_tok(t) * p.page_size)) * (size_t)p.Hkv +
-                                           (size_t)hg * HPC);
+                for (int k = 0; k < IDS; ++k) {
+                    if (k * 32 >= nvalid)
+                        break;
+                    const int row = k * 32 + lane, t = tok + row;
+                    const bool there = row < nvalid;
+                    const int page = checked(ids[k], there);
+                    const int slot = page * p.page_size +
+                                     (there ? t - page_of_tok(t) * p.page_size : 0);
+                    if (there) {
+                        const size_t head = (size_t)slot * p.Hkv + (size_t)hg * HPC;
+                        copy_scale(p.k_scale, row, head);
+                        copy_scale(p.v_scale, C::kTok + row, head);
                     }
-                } else {
-                    constexpr int CH = C::kRowBytes / 16;      // 16-byte lines of a token
-                    const size_t line0 = (size_t)hg * C::kRowBytes;
-                    const unsigned tok_bytes = (unsigned)(p.Hkv * D);
+                    // 32 lines at a time, 32 / CH tokens' (or part of one): line
+                    // 32 j + lane lies at byte 16 (32 j + lane) of these tokens'
+                    // rows, its swizzle that of the lane and of j (no carry)
+                    constexpr int ROUNDS = (C::kTok < 32 ? C::kTok : 32) * CH / 32;
+                    constexpr int HALF = C::kRowBytes >= 128 ? 0 : 1;
+                    const uint32_t lane_key = (uint32_t)((lane / CH) >> HALF & 7) << 4;
+                    const uint32_t to = smem_addr(stage) + k * 32 * C::kRowBytes;
 #pragma unroll
-                    for (int k = 0; k < IDS; ++k) {
-                        if (k * 32 >= nvalid)
-                            break;
-                        const int row = k * 32 + lane, t = tok + row;
-                        const bool there = row < nvalid;
-                        const int page = checked(ids[k], there);
-                        const int slot = page * p.page_size +
-                                         (there ? t - page_of_tok(t) * p.page_size : 0);
-                        if (there) {
-                            const size_t head = (size_t)slot * p.Hkv + (size_t)hg * HPC;
-                            copy_scale(p.k_scale, row, head);
-                            copy_scale(p.v_scale, C::kTok + row, head);
-                        }
-                        // 32 lines at a time, 32 / CH tokens' (or part of one): line
-                        // 32 j + lane lies at byte 16 (32 j + lane) of these tokens'
-                        // rows, its swizzle that of the lane and of j (no carry)
-                        constexpr int ROUNDS = (C::kTok < 32 ? C::kTok : 32) * CH / 32;
-                        constexpr int HALF = C::kRowBytes >= 128 ? 0 : 1;
-                        const uint32_t lane_key = (uint32_t)((lane / CH) >> HALF & 7) << 4;
-                        const uint32_t to = smem_addr(stage) + k * 32 * C::kRowBytes;
-#pragma unroll
-                        for (int j = 0; j < ROUNDS; ++j) {
-                            const int from = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
-                            const unsigned s_ = (unsigned)__shfl_sync(kFull, slot, from);
-                            if (k * 32 + from < nvalid) {
-                                const size_t off = (size_t)s_ * tok_bytes + (line0 + ch * 16);
-                                const uint32_t dst =
-                                    to + j * 512 +
-                                    ((lane * 16u) ^ lane_key ^
-                                     (uint32_t)((j * 32 / CH) >> HALF & 7) << 4);
-                                cp_async16(dst, p.k_codes + off, policy);
-                                cp_async16(dst + C::kTok * C::kRowBytes, p.v_codes + off, policy);
-                            }
+                    for (int j = 0; j < ROUNDS; ++j) {
+                        const int from = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
+                        const unsigned s_ = (unsigned)__shfl_sync(kFull, slot, from);
+                        if (k * 32 + from < nvalid) {
+                            const size_t off = (size_t)s_ * tok_bytes + (line0 + ch * 16);
+                            const uint32_t dst =
+                                to + j * 512 +
+                                ((lane * 16u) ^ lane_key ^
+                                 (uint32_t)((j * 32 / CH) >> HALF & 7) << 4);
+                            cp_async16(dst, p.k_codes + off, policy);
+                            cp_async16(dst + C::kTok * C::kRowBytes, p.v_codes + off, policy);
                         }
                     }
                 }
@@ -466,24 +404,12 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
     const int g = lane >> 2, c = lane & 3;
     const uint32_t smem_s = smem_addr(smem);
     // Matrix loads: lane l addresses token l % 16 of the warp's 16 and the
-    // 16-byte column l / 16 of each two.  For V the tokens are in the order in
-    // which the weights' operand has them: 2c, 2c + 1, 2c + 8, 2c + 9 of c = 0..3.
-    auto token_addr = [&](int t) {
-        uint32_t col = (uint32_t)(lane >> 4) * 16;
-        if constexpr (BOX) {
-            constexpr int HR = C::kHeadsRow;
-            const int row = ((((t >> params.box_shift) * (HPC / HR) + hw / HR)
-                              << params.box_shift) | (t & (box - 1)));
-            col += (uint32_t)(hw % HR) * D;
-            return (uint32_t)(row * 128) + (col ^ (uint32_t)(row & 7) << 4);
-        } else {
-            return line_addr(t, hw * D + (int)col);
-        }
-    };
+    // 16-byte column l / 16 of each two.
     // the 32-byte column i of a row whose first is at `addr`: the swizzle is in
     // the same bits
     auto column = [](uint32_t addr, int i) { return addr ^ (i * 32u); };
-    const uint32_t k_off = smem_s + token_addr(tg * 16 + (lane & 15));
+    const uint32_t k_off =
+        smem_s + line_addr(tg * 16 + (lane & 15), hw * D + (lane >> 4) * 16);
     const uint32_t v_off = k_off + C::kTok * C::kRowBytes;
     // lane (g, c)'s elements of head 8 nt + g of row r
     auto load_q = [&](uint2 (&raw)[D / 16], int r, int nt) {
@@ -547,7 +473,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
                 oacc[nt][j][0] = oacc[nt][j][1] = oacc[nt][j][2] = oacc[nt][j][3] = 0.f;
         }
 
-        for (int tok = BOX ? t0 & -box : t0; tok < t1;) {
+        for (int tok = t0; tok < t1;) {
             constexpr int U = C::kTake;
             // this turn's stages: U, or as many as the piece has left
             const int take = U == 1 ? 1 : min(U, (t1 - tok + C::kTok - 1) / C::kTok);
@@ -771,13 +697,11 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
         if (tg != 0)
             continue;
         // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + 2g + (e >> 1)
-        const int first = block_of(lo, T, G);
-        const int last = block_of(hi - 1, T, G);
+        const bool whole = t0 == 0 && t1 == hi - lo;
         if (t0 == 0 && warp == 0 && lane == 0 && !planned) {
-            p.row_info[2 * r] = first;
-            p.row_info[2 * r + 1] = last - first + 1;
+            p.row_info[2 * r] = cta;
+            p.row_info[2 * r + 1] = whole ? 1 : block_of(hi - 1, T, G) - cta + 1;
         }
-        const bool whole = first == last;
         const size_t slot0 = (size_t)(cta + r) * (HPC * p.n_rep) + (size_t)hw * p.n_rep;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -814,78 +738,45 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT, BOX>::kThreads, 1)
     grid_launch_dependents();
 }
 
-template <int D, int HPC, int NT, bool BOX>
-cudaError_t launch(const Q8Params &p, int grid, cudaStream_t stream)
+template <int D, int HPC, int NT>
+cudaError_t launch(const FusedParams &p, int grid, cudaStream_t stream)
 {
-    using C = Q8Cfg<D, HPC, NT, BOX>;
+    using C = Q8Cfg<D, HPC, NT>;
     static DeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        cudaError_t r = cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, BOX>,
+        cudaError_t r = cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemBytes);
         if (r != cudaSuccess)
             return r;
-        return cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT, BOX>,
+        return cudaFuncSetAttribute(decode_q8_kernel<D, HPC, NT>,
                                     cudaFuncAttributePreferredSharedMemoryCarveout,
                                     cudaSharedmemCarveoutMaxShared);
     });
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(decode_q8_kernel<D, HPC, NT, BOX>, dim3(grid), dim3(C::kThreads),
-                      C::kSmemBytes, stream, p);
-}
-
-// Boxes of 16 tokens (8 where a page is not a multiple of 16) if pages hold
-// whole boxes and a driver encodes them.
-template <int D, int HPC>
-bool box_maps(Q8Params &q)
-{
-    const FusedParams &p = q.f;
-    if (p.page_size % 8 != 0)
-        return false;
-    q.box_shift = p.page_size % 16 == 0 ? 4 : 3;
-    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-    if (encode == nullptr)
-        return false;
-    const cuuint64_t tok_bytes = (cuuint64_t)p.Hkv * D;
-    const cuuint64_t dims[3] = {128, (cuuint64_t)p.num_pages * p.page_size, tok_bytes / 128};
-    const cuuint64_t strides[2] = {tok_bytes, 128};
-    const cuuint32_t box[3] = {128, 1u << q.box_shift, HPC * D / 128};
-    const cuuint32_t steps[3] = {1, 1, 1};
-    for (int v = 0; v < 2; ++v)
-        if (encode(v ? &q.map_v : &q.map_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-                   const_cast<uint8_t *>(v ? p.v_codes : p.k_codes), dims, strides, box, steps,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return false;
-    return true;
+    return launch_pdl(decode_q8_kernel<D, HPC, NT>, dim3(grid), dim3(C::kThreads), C::kSmemBytes,
+                      stream, p);
 }
 
 template <int D, int HPC>
-cudaError_t launch_nt(Q8Params &q, int grid, cudaStream_t stream)
+cudaError_t launch_nt(const FusedParams &p, int grid, cudaStream_t stream)
 {
-    if constexpr (HPC * D >= kBoxBytes) {
-        if (box_maps<D, HPC>(q))
-            return q.f.n_rep <= 8 ? launch<D, HPC, 1, true>(q, grid, stream)
-                                  : launch<D, HPC, 2, true>(q, grid, stream);
-    }
-    return q.f.n_rep <= 8 ? launch<D, HPC, 1, false>(q, grid, stream)
-                          : launch<D, HPC, 2, false>(q, grid, stream);
+    return p.n_rep <= 8 ? launch<D, HPC, 1>(p, grid, stream) : launch<D, HPC, 2>(p, grid, stream);
 }
 
 template <int D>
-cudaError_t launch_d(Q8Params &q, int grid, cudaStream_t stream)
+cudaError_t launch_d(const FusedParams &p, int grid, cudaStream_t stream)
 {
-    switch (q.f.hpc) {
+    switch (p.hpc) {
     case 8:
-        return launch_nt<D, 8>(q, grid, stream);
+        return launch_nt<D, 8>(p, grid, stream);
     case 4:
-        return launch_nt<D, 4>(q, grid, stream);
+        return launch_nt<D, 4>(p, grid, stream);
     case 2:
-        return launch_nt<D, 2>(q, grid, stream);
+        return launch_nt<D, 2>(p, grid, stream);
     default:
-        return launch_nt<D, 1>(q, grid, stream);
+        return launch_nt<D, 1>(p, grid, stream);
     }
 }
 
@@ -893,10 +784,9 @@ cudaError_t launch_d(Q8Params &q, int grid, cudaStream_t stream)
 
 cudaError_t launch_decode_q8(const FusedParams &params, int D, int grid, cudaStream_t stream)
 {
-    Q8Params q{};
-    q.f = params;
-    q.f.handoff_wait_ns = handoff_wait_ns();
-    return D == 64 ? launch_d<64>(q, grid, stream) : launch_d<128>(q, grid, stream);
+    FusedParams p = params;
+    p.handoff_wait_ns = handoff_wait_ns();
+    return D == 64 ? launch_d<64>(p, grid, stream) : launch_d<128>(p, grid, stream);
 }
 
 } // namespace pkv

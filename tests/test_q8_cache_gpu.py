@@ -307,3 +307,149 @@ def test_norm_write_then_bf16_decode_step():
         w = torch.softmax(torch.einsum("grd,lgd->grl", q_out[b].cpu().double().view(2, 4, 128), kk) * c.scale, -1)
         size = torch.einsum("grl,lgd->grd", w, vv.abs()).reshape(8, 128)
         assert bool(((out[b].cpu().double() - want).abs() <= bound + size * 2.0 ** -7).all())
+
+
+# ------------------------------------------------------------- plans and errors
+def _ws(c, S):
+    return pkv.alloc_workspace(c.d, S, DEV)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(32, 8, 128, 16), (8, 2, 64, 16), (5, 1, 64, 7), (48, 16, 128, 16)])
+def test_planned_calls_give_the_same_bits(Hq, Hkv, D, ps):
+    """On a plan made by paged_decode_plan, by this decode, and by the bf16
+    decode; and the bf16 decode on this decode's plan."""
+    c = Cache([700, 0, 33, 64, 1, 2000], Hq, Hkv, D, ps, seed=D + Hkv).fill()
+    c.k16.normal_()
+    c.v16.normal_()
+    q = _q(c)
+    for S in (pkv.plan(c.d)[0], 3, 1):
+        want, _ = c.decode(q, S)
+        want16 = torch.empty_like(want)
+        ws = _ws(c, S)
+        pkv.paged_decode_attn(c.d, q, c.k16, c.v16, *c.rows, S, ws, want16)
+        for make in ("bf16", "plan", "q8"):
+            ws = _ws(c, S)
+            out = torch.full_like(want, float("nan"))
+            if make == "bf16":
+                pkv.paged_decode_attn(c.d, q, c.k16, c.v16, *c.rows, S, ws, out)
+            elif make == "plan":
+                pkv.paged_decode_plan(c.d, *c.rows, S, ws)
+            else:
+                pkv.paged_decode_attn_q8(c.d, q, *c.q8, *c.rows, S, ws, out)
+            out.fill_(float("nan"))
+            pkv.paged_decode_attn_q8_planned(c.d, q, *c.q8, *c.rows, S, ws, out)
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16)), make
+            out.fill_(float("nan"))
+            pkv.paged_decode_attn_planned(c.d, q, c.k16, c.v16, *c.rows, S, ws, out)
+            assert torch.equal(out.view(torch.int16), want16.view(torch.int16)), make
+            assert pkv.status_word(ws) == 0
+
+
+def test_planned_call_on_another_shapes_plan():
+    """A plan for another grid or batch is not used, nor what it left for the
+    join of the pieces."""
+    c, other = (Cache(lens, 8, 2, 64, 16, seed=3).fill() for lens in ([300, 40], [10, 500, 77]))
+    c.k16.normal_()
+    c.v16.normal_()
+    S = pkv.plan(c.d)[0]
+    q = _q(c)
+    want, _ = c.decode(q, S)
+    ws, want16 = _ws(c, S), torch.empty_like(want)
+    pkv.paged_decode_attn(c.d, q, c.k16, c.v16, *c.rows, S, ws, want16)
+    for splits in (S, 64):
+        ws, out = pkv.alloc_workspace(other.d, 64, DEV), torch.empty_like(want)
+        pkv.paged_decode_plan(other.d, *other.rows, splits, ws)
+        pkv.paged_decode_attn_q8_planned(c.d, q, *c.q8, *c.rows, S, ws, out)
+        assert torch.equal(out, want)
+        ws = pkv.alloc_workspace(other.d, 64, DEV)
+        pkv.paged_decode_plan(other.d, *other.rows, splits, ws)
+        pkv.paged_decode_attn_planned(c.d, q, c.k16, c.v16, *c.rows, S, ws, out)
+        assert torch.equal(out, want16)
+
+
+def test_not_a_number_is_not_lost_in_the_join():
+    """A NaN key or value in one piece of a row that many blocks share."""
+    c = Cache([3000, 50], 8, 2, 64, 16, seed=12).fill()
+    q = _q(c)
+    ok, _ = c.decode(q)
+    at = c.places(0, 1234, 1235)
+    c.kc[at[0][0], at[1][0], 1, 7] = 0x7F
+    bad, _ = c.decode(q)
+    assert bool(torch.isnan(bad[0, 4:].float()).all())                # kv head 1 serves heads 4-7
+    assert torch.equal(bad[0, :4], ok[0, :4]) and torch.equal(bad[1], ok[1])
+    c.kc[at[0][0], at[1][0], 1, 7] = 0
+    c.vc[at[0][0], at[1][0], 0, 9] = 0xFF
+    bad, _ = c.decode(q)
+    nan = torch.isnan(bad[0, :4].float())
+    assert bool(nan[:, 9].all()) and int(nan.sum()) == 4
+    # an infinite query makes its own head NaN and no other
+    c.vc[at[0][0], at[1][0], 0, 9] = 0
+    ok, _ = c.decode(q)
+    q[0, 2, 5] = float("inf")
+    bad, _ = c.decode(q)
+    assert bool(torch.isnan(bad[0, 2].float()).all())
+    assert torch.equal(bad[0, [0, 1, 3]], ok[0, [0, 1, 3]]) and torch.equal(bad[1], ok[1])
+
+
+def test_handoff_timeout_sets_flag_and_the_next_call_is_right():
+    c = Cache([5000, 100], 32, 8, 128, 16, seed=13).fill()
+    q = _q(c)
+    want, _ = c.decode(q)
+    try:
+        pkv.testing_set_handoff_wait_ns(0)
+        _, status = c.decode(q)
+        assert status & pkv.FLAG_TIMEOUT
+    finally:
+        pkv.testing_set_handoff_wait_ns(pkv.DEFAULT_HANDOFF_WAIT_NS)
+    out, status = c.decode(q)
+    assert status == 0 and torch.equal(out, want)
+
+
+def test_two_streams_at_once():
+    """Two caches written and read on two streams, each with its own workspace."""
+    cases = [Cache([900, 41, 7], 16, 4, 128, 16, seed=s).fill() for s in (1, 2)]
+    qs = [_q(c) for c in cases]
+    want = [c.decode(q)[0] for c, q in zip(cases, qs)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    S = [pkv.plan(c.d)[0] for c in cases]
+    ws = [_ws(c, s) for c, s in zip(cases, S)]
+    outs = [[torch.empty_like(w) for _ in range(20)] for w in want]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for n, c in enumerate(cases):
+            pkv.paged_decode_attn_q8(c.d, qs[n], *c.q8, *c.rows, S[n], ws[n], outs[n][i], stream=streams[n])
+    torch.cuda.synchronize()
+    for n in range(2):
+        assert all(torch.equal(o, want[n]) for o in outs[n])
+
+
+def test_two_graphs_share_a_workspace():
+    c = Cache([900, 41, 7], 16, 4, 64, 16, seed=5).fill()
+    S = pkv.plan(c.d)[0]
+    ws = _ws(c, S)
+    q = [_q(c), _q(c)]
+    want = [c.decode(x)[0] for x in q]
+    out = [torch.empty_like(w) for w in want]
+    graphs = []
+    for x, o in zip(q, out):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pkv.paged_decode_attn_q8(c.d, x, *c.q8, *c.rows, S, ws, o)
+        graphs.append(g)
+    for _ in range(3):
+        for g, o in zip(graphs, out):
+            o.zero_()
+            g.replay()
+    assert all(torch.equal(o, w) for o, w in zip(out, want))
+
+
+def test_shared_pages_and_the_same_page_twice():
+    """Rows that share a prefix's pages, and a row that names one page twice."""
+    c = Cache([64, 64, 48], 8, 2, 64, 16, seed=8).fill()
+    c.kv_indices[4:6] = c.kv_indices[0:2]
+    c.kv_indices[10] = c.kv_indices[9]
+    c.table.copy_(c.kv_indices.cpu())
+    q = _q(c)
+    out, status = c.decode(q)
+    assert status == 0
+    c.check_decode(q, out)
