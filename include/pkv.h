@@ -563,19 +563,29 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
                             uint32_t *status, pkv_stream_t stream);
 
 /* paged_decode_attn over an 8-bit cache: q and out bf16 [B, Hq, D], fp32
- * softmax, num_splits, workspace, flags and the plan left behind as for that
- * call (paged_decode_plan serves both caches).  Scales as the writes above
- * choose them, or any in [127 - 40, 127 + 40]; the output of a row holding
- * others is undefined.  One persistent kernel plus, when num_splits > 1, the
- * piece combine; a batch of more than 1024 rows x kv-head groups (a group: 8,
- * 4, 2 or 1 kv heads, the most that divide Hkv) takes several such pairs, one
- * after the other.  PKV_ERR_UNSUPPORTED: Hkv of more than 1024 groups, or
- * max_seq_len x groups or num_pages x page_size past 2^31. */
+ * softmax, num_splits, workspace and flags as for that call.  Scales as the
+ * writes above choose them, or any in [127 - 40, 127 + 40]; the output of a row
+ * holding others is undefined.  A NaN code reaches the outputs that read it, an
+ * infinite query element its head's.  One persistent kernel plus, when
+ * num_splits > 1, the piece combine; a batch of more than 1024 rows x kv-head
+ * groups (a group: 8, 4, 2 or 1 kv heads, the most that divide Hkv) takes
+ * several such pairs, one after the other.  PKV_ERR_UNSUPPORTED: Hkv of more
+ * than 1024 groups, or max_seq_len x groups or num_pages x page_size past 2^31.
+ * A call of one pair leaves its partition in the workspace as the step's plan
+ * for paged_decode_attn_q8_planned. */
 pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
                                 const void *v_codes, const void *k_scale, const void *v_scale,
                                 const int32_t *kv_indices, const int32_t *kv_indptr,
                                 const int32_t *seq_lens, int num_splits, void *workspace,
                                 size_t ws_bytes, void *out, pkv_stream_t stream);
+
+/* paged_decode_plan for the decode over an 8-bit cache, which weighs rows
+ * otherwise: neither decode uses the other's plan (a planned call then computes
+ * its partition itself, with the same results). */
+pkv_status paged_decode_plan_q8(const pkv_dims *dims, const int32_t *kv_indices,
+                                const int32_t *kv_indptr, const int32_t *seq_lens,
+                                int num_splits, void *workspace, size_t ws_bytes,
+                                pkv_stream_t stream);
 
 /* paged_decode_attn_q8 on the workspace's plan, under the conditions of
  * paged_decode_attn_planned; the same results, bit for bit. */

@@ -73,7 +73,10 @@ int log2_exact(int x)
     return s;
 }
 
-// Workspace: [header 256 B | row info, persistent path: Bv x 2 int32 |
+// Workspace: [header 256 B | row info, persistent path: Bv x 2 int32 | the same
+//             of the 8-bit cache's decode (whose partition differs, and which
+//             must leave the row info of a bf16 plan as it is, and the other way
+//             round) |
 //             the per-step plan, persistent path | rotated-q scratch
 //             [B, Hq, D] bf16 | one-page-per-row table of
 //             the contiguous-cache call, (2B + 1) int32 | partials].
@@ -82,7 +85,7 @@ int log2_exact(int x)
 // persistent path.  Every region starts on a 256-byte boundary.
 struct Layout {
     int hpc, Bv, HQV;
-    size_t rowinfo_off, plan_off, qscratch_off, table_off, split_ml_off, split_o_off,
+    size_t rowinfo_off, rowinfo_q8_off, plan_off, qscratch_off, table_off, split_ml_off, split_o_off,
         piece_ml_off, piece_o_off, total;
 };
 
@@ -93,7 +96,8 @@ Layout layout_for(const pkv_dims *d, int num_splits)
     L.Bv = d->B * (d->Hkv / L.hpc);
     L.HQV = L.hpc * (d->Hq / d->Hkv);
     L.rowinfo_off = kHeaderBytes;
-    L.plan_off = L.rowinfo_off + round_up((size_t)L.Bv * 2 * sizeof(int32_t), 256);
+    L.rowinfo_q8_off = L.rowinfo_off + round_up((size_t)L.Bv * 2 * sizeof(int32_t), 256);
+    L.plan_off = L.rowinfo_q8_off + round_up((size_t)L.Bv * 2 * sizeof(int32_t), 256);
     // the per-step plan, for shapes the persistent path serves
     const size_t plan = L.Bv <= pkv::kFusedMaxRows
                             ? pkv::plan_words(L.Bv, num_splits) * sizeof(int32_t) : 0;
@@ -207,13 +211,13 @@ pkv_status launch_combine_split(const pkv_dims *dims, int num_splits, void *work
 // The persistent path's parameters (shape, tables, workspace regions).
 pkv::FusedParams persistent_params(const pkv_dims *dims, const Layout &L, char *ws,
                                    const int32_t *kv_indices, const int32_t *kv_indptr,
-                                   const int32_t *seq_lens)
+                                   const int32_t *seq_lens, bool q8 = false)
 {
     pkv::FusedParams p{};
     p.kv_indices = kv_indices;
     p.kv_indptr = kv_indptr;
     p.seq_lens = seq_lens;
-    p.row_info = reinterpret_cast<int32_t *>(ws + L.rowinfo_off);
+    p.row_info = reinterpret_cast<int32_t *>(ws + (q8 ? L.rowinfo_q8_off : L.rowinfo_off));
     p.status = reinterpret_cast<uint32_t *>(ws);
     p.B = dims->B;
     p.Hq = dims->Hq;
@@ -225,7 +229,7 @@ pkv::FusedParams persistent_params(const pkv_dims *dims, const Layout &L, char *
     p.num_indices = dims->num_indices;
     p.max_seq_len = dims->max_seq_len;
     p.Bv = L.Bv;
-    p.row_cost = pkv::kFusedRowCost;
+    p.row_cost = q8 ? pkv::kQ8RowCost : pkv::kFusedRowCost;
     p.hpc = L.hpc;
     return p;
 }
@@ -274,6 +278,7 @@ pkv_status launch_persistent(const pkv_dims *dims, const void *q, const void *k_
     c.plan = p.plan;
     c.grid = num_splits;
     c.page_size = dims->page_size;
+    c.row_cost = p.row_cost;
     if (adv != nullptr)
         c.adv = *adv;
     return launch_status(
@@ -597,9 +602,11 @@ pkv_status paged_decode_attn_planned(const pkv_dims *dims, const void *q, const 
                             num_splits, workspace, ws_bytes, out, stream, true);
 }
 
-pkv_status paged_decode_plan(const pkv_dims *dims, const int32_t *kv_indices,
-                             const int32_t *kv_indptr, const int32_t *seq_lens, int num_splits,
-                             void *workspace, size_t ws_bytes, pkv_stream_t stream)
+static int q8_rows(const pkv_dims *dims, int hpc);
+
+static pkv_status plan_impl(const pkv_dims *dims, const int32_t *kv_indices,
+                            const int32_t *kv_indptr, const int32_t *seq_lens, int num_splits,
+                            void *workspace, size_t ws_bytes, pkv_stream_t stream, bool q8)
 {
     pkv_status st = check_dims(dims);
     if (st != PKV_OK)
@@ -618,13 +625,31 @@ pkv_status paged_decode_plan(const pkv_dims *dims, const int32_t *kv_indices,
         return PKV_ERR_INVALID_ARG;
     if (ws_bytes < need)
         return PKV_ERR_WORKSPACE_TOO_SMALL;
-    if (!fused_path_ok(dims))
-        return PKV_OK;                     // other shapes compute their split per call
     const Layout L = layout_for(dims, num_splits);
+    if (q8 ? dims->B > q8_rows(dims, L.hpc) : !fused_path_ok(dims))
+        return PKV_OK;                     // other shapes compute their split per call
     char *ws = static_cast<char *>(workspace);
-    const pkv::FusedParams p = persistent_params(dims, L, ws, kv_indices, kv_indptr, seq_lens);
+    const pkv::FusedParams p =
+        persistent_params(dims, L, ws, kv_indices, kv_indptr, seq_lens, q8);
     return launch_status(pkv::launch_decode_plan(
         p, num_splits, reinterpret_cast<int32_t *>(ws + L.plan_off), (cudaStream_t)stream));
+}
+
+pkv_status paged_decode_plan(const pkv_dims *dims, const int32_t *kv_indices,
+                             const int32_t *kv_indptr, const int32_t *seq_lens, int num_splits,
+                             void *workspace, size_t ws_bytes, pkv_stream_t stream)
+{
+    return plan_impl(dims, kv_indices, kv_indptr, seq_lens, num_splits, workspace, ws_bytes,
+                     stream, false);
+}
+
+pkv_status paged_decode_plan_q8(const pkv_dims *dims, const int32_t *kv_indices,
+                                const int32_t *kv_indptr, const int32_t *seq_lens,
+                                int num_splits, void *workspace, size_t ws_bytes,
+                                pkv_stream_t stream)
+{
+    return plan_impl(dims, kv_indices, kv_indptr, seq_lens, num_splits, workspace, ws_bytes,
+                     stream, true);
 }
 
 static pkv_status decode_step_impl(const pkv_dims *dims, const void *q, const void *k_new,
@@ -1109,6 +1134,17 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
     return launch_status(pkv::launch_read_q8(p, dims->D, (cudaStream_t)stream));
 }
 
+// Rows that one launch over the 8-bit cache takes: its rows x kv-head groups
+// have their prefix sums in shared memory, and their weights in 31 bits.
+static int q8_rows(const pkv_dims *dims, int hpc)
+{
+    const int groups = dims->Hkv / hpc;
+    const long long by_weight =
+        ((1ll << 31) - 1) / ((long long)dims->max_seq_len + pkv::kQ8RowCost) / groups;
+    const long long by_rows = pkv::kQ8MaxRows / groups;
+    return (int)(by_weight < by_rows ? by_weight : by_rows);
+}
+
 static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void *k_codes,
                                  const void *v_codes, const void *k_scale, const void *v_scale,
                                  const int32_t *kv_indices, const int32_t *kv_indptr,
@@ -1124,12 +1160,7 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
         return PKV_ERR_INVALID_ARG;
     const Layout L = layout_for(dims, num_splits);
     const int groups = dims->Hkv / L.hpc;
-    // rows of one launch: its rows x kv-head groups have their prefix sums in
-    // shared memory, and their weights in 31 bits
-    const long long by_weight =
-        ((1ll << 31) - 1) / ((long long)dims->max_seq_len + pkv::kFusedRowCost) / groups;
-    const long long by_rows = pkv::kQ8MaxRows / groups;
-    const int most = (int)(by_weight < by_rows ? by_weight : by_rows);
+    const int most = q8_rows(dims, L.hpc);
     if (most < 1)
         return PKV_ERR_UNSUPPORTED;
     // the kernel counts a pool's token slots in 31 bits
@@ -1142,7 +1173,7 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
         pkv_dims d = *dims;
         d.B = dims->B - b0 < most ? dims->B - b0 : most;
         pkv::FusedParams p =
-            persistent_params(&d, L, ws, kv_indices, kv_indptr + b0, seq_lens + b0);
+            persistent_params(&d, L, ws, kv_indices, kv_indptr + b0, seq_lens + b0, true);
         p.Bv = d.B * groups;
         p.q = static_cast<const __nv_bfloat16 *>(q) + (size_t)b0 * d.Hq * d.D;
         p.out = static_cast<__nv_bfloat16 *>(out) + (size_t)b0 * d.Hq * d.D;
@@ -1175,6 +1206,7 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
         c.plan = p.plan;
         c.grid = num_splits;
         c.page_size = d.page_size;
+        c.row_cost = p.row_cost;
         st = launch_status(
             pkv::launch_piece_combine(c, d.D, num_splits, (cudaStream_t)stream));
         if (st != PKV_OK)

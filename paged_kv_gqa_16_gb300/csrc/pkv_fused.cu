@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(FusedCfg<D, HPC>::kThreads, 1)
     int plan_r0 = 0, plan_wb = 0, plan_w0 = 0, plan_w1 = 0, plan_pg0 = 0, plan_npg = 0;
     if (p.plan != nullptr) {
         const int32_t *pe = plan_entry(p.plan, Bv, cta);
-        const bool fits = plan_fits(p.plan, (int)gridDim.x, Bv, p.B, p.page_size);
+        const bool fits = plan_fits(p.plan, (int)gridDim.x, Bv, p.B, p.page_size, p.row_cost);
         int e_lo = 0, e_hi = 0, e_start = 0, e_end = 0;
         if (warp == HPC) {
             const int ew = lane < 8 ? pe[lane] : 0;
@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(FusedCfg<D, HPC>::kThreads, 1)
             p.plan_out[3] = Bv;
             p.plan_out[4] = p.B;
             p.plan_out[5] = p.page_size;
+            p.plan_out[6] = p.row_cost;
         }
     }
     if (cta >= G) {
@@ -763,6 +764,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const FusedPa
             plan[3] = Bv;
             plan[4] = p.B;
             plan[5] = p.page_size;
+            plan[6] = p.row_cost;
         }
     }
     int32_t *e = const_cast<int32_t *>(plan_entry(plan, Bv, cta));
@@ -834,14 +836,15 @@ __global__ void __launch_bounds__(WPH > 8 ? 32 * WPH : 256)
     }
     // With a plan, each row's first block and piece count were written by the
     // plan kernel, which completed before the decode grid passed its own
-    // wait: read them while the decode grid finishes.  Without one (or with one
-    // of another grid or shape, which the decode grid does not use) the decode
-    // grid writes them: read them after the wait.
-    const bool planned = p.plan != nullptr && plan_fits(p.plan, p.grid, p.Bv, p.B, p.page_size);
-    if (planned && live) {
+    // wait: read them while the decode grid finishes.  Without one the decode
+    // grid writes them, and with one of another grid or shape, which the decode
+    // grid does not use, too: then they are read (again) after the wait.
+    if (p.plan != nullptr && live) {
         first = p.row_info[2 * r];
         n = p.row_info[2 * r + 1];
     }
+    const bool planned = p.plan != nullptr &&
+                         plan_fits(p.plan, p.grid, p.Bv, p.B, p.page_size, p.row_cost);
     grid_dependency_wait();
     // paged_decode_step_advance: the last block advances the metadata for the
     // next step; the decode grid, the only reader of it, has completed

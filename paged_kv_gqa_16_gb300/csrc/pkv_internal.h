@@ -268,6 +268,11 @@ struct FusedParams {
     int32_t *plan_out;
 };
 
+// The same over the 8-bit cache, whose tokens stream in half the time: of {16,
+// 32, 48, 64, 96, 128, 192}, 64 measured best on the serving batch of 128 (59.1,
+// 58.1, 58.4, 57.4, 57.9, 58.7, 59.0 us) and 8 rows of 513 to 1,025 tokens (10.6,
+// 10.0, 9.9, 9.2, 9.2, 9.2, 9.2 us).
+constexpr int kQ8RowCost = 64;
 // Rows x kv-head groups of one launch over the 8-bit cache (pkv_q8_decode.cu),
 // whose ring of stages needs the room of more prefix sums.
 constexpr int kQ8MaxRows = 1024;
@@ -292,7 +297,7 @@ struct PieceCombineParams {
     // a planned call's plan: if it is of this grid and shape, row_info is the
     // plan's and may be read before the decode grid has completed
     const int32_t *plan;
-    int grid, page_size;
+    int grid, page_size, row_cost;
     // paged_decode_step_advance: one extra block runs the metadata advance
     // (adv.seq_lens == nullptr: none)
     AdvanceParams adv;

@@ -126,7 +126,7 @@ __device__ __forceinline__ int first_row(const int *prefix, int Bv, long long st
 }
 
 // The per-step plan (int32 words): [0] T, [1] active blocks G, [2] grid,
-// [3] virtual rows Bv, [4] rows B, [5] page_size, [6..15] unused; then
+// [3] virtual rows Bv, [4] rows B, [5] page_size, [6] row_cost, [7..15] unused; then
 // prefix[0..Bv] (padded to a multiple of 4 words); then one entry of
 // kPlanEntryInts words per block of the grid: [0] its first row r0 (-1: no
 // work), [1] the base wb of that row's page-table window, [2] the row's
@@ -142,11 +142,12 @@ __device__ __forceinline__ const int32_t *plan_entry(const int32_t *plan, int Bv
     return plan + kPlanHeaderInts + ((Bv + 1 + 3) & ~3) + (size_t)c * kPlanEntryInts;
 }
 
-// Whether a plan is of this grid and shape.
+// Whether a plan is of this grid, shape and row cost.
 __device__ __forceinline__ bool plan_fits(const int32_t *plan, int grid, int Bv, int B,
-                                          int page_size)
+                                          int page_size, int row_cost)
 {
-    return plan[2] == grid && plan[3] == Bv && plan[4] == B && plan[5] == page_size;
+    return plan[2] == grid && plan[3] == Bv && plan[4] == B && plan[5] == page_size &&
+           plan[6] == row_cost;
 }
 
 } // namespace pkv

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     // the partition, from the step's plan or computed here (as in pkv_fused.cu)
     bool planned = false;
     if (p.plan != nullptr) {
-        planned = plan_fits(p.plan, (int)gridDim.x, Bv, p.B, p.page_size);
+        planned = plan_fits(p.plan, (int)gridDim.x, Bv, p.B, p.page_size, p.row_cost);
         for (int i = threadIdx.x; i <= Bv; i += C::kThreads)
             prefix[i] = p.plan[kPlanHeaderInts + i];
         __syncthreads();
@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
             p.plan_out[3] = Bv;
             p.plan_out[4] = p.B;
             p.plan_out[5] = p.page_size;
+            p.plan_out[6] = p.row_cost;
         }
     }
     const unsigned t_q = T / Gu, t_r = T % Gu;

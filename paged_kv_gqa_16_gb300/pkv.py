@@ -42,7 +42,7 @@ EXPORTS = (
     "paged_decode_step_planned", "decode_attn_contig_planned", "paged_prefill_attn_ws",
     "pkv_prefill_workspace_bytes", "pkv_prefill_plan", "paged_kv_append_norm",
     "paged_kv_extend_norm", "paged_kv_append_q8", "paged_kv_extend_q8", "paged_kv_read_q8",
-    "paged_decode_attn_q8", "paged_decode_attn_q8_planned",
+    "paged_decode_attn_q8", "paged_decode_attn_q8_planned", "paged_decode_plan_q8",
 )
 
 
@@ -106,6 +106,7 @@ def lib():
             "paged_decode_attn": (I, [DP, P, P, P, P, P, P, I, P, Z, P, P]),
             "paged_decode_step": (I, [DP, P, P, P, P, P, P, P, P, P, I, I, P, Z, P, P]),
             "paged_decode_plan": (I, [DP, P, P, P, I, P, Z, P]),
+            "paged_decode_plan_q8": (I, [DP, P, P, P, I, P, Z, P]),
             "paged_decode_attn_planned": (I, [DP, P, P, P, P, P, P, I, P, Z, P, P]),
             "paged_decode_step_planned": (I, [DP, P, P, P, P, P, P, P, P, P, I, I, P, Z, P, P]),
             "paged_decode_partials": (I, [DP, P, P, P, P, P, P, I, P, Z, P]),
@@ -150,13 +151,11 @@ def _check(fn: str, code: int) -> None:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    if not x.is_contiguous():
-        raise ValueError("tensors passed to libpkv must be contiguous")
-    return x.data_ptr()
+    if x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError("tensors passed to libpkv must be contiguous")
 
 
 _current_stream = None
@@ -482,6 +481,15 @@ def paged_decode_attn_q8(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indi
         ctypes.byref(d), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
         ws_bytes, _ptr(out), _stream(stream)))
+
+
+def paged_decode_plan_q8(d: Dims, kv_indices, kv_indptr, seq_lens, num_splits: int, workspace,
+                         stream=None) -> None:
+    """paged_decode_plan for paged_decode_attn_q8_planned."""
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check("paged_decode_plan_q8", lib().paged_decode_plan_q8(
+        ctypes.byref(d), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits,
+        _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def paged_decode_attn_q8_planned(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices,

@@ -108,6 +108,31 @@ def test_decode_refusals():
     assert call(d=_d(B=0)) == pkv.PKV_OK
 
 
+def test_plan_refusals():
+    d = _d()
+    need = pkv.workspace_bytes(d, 8)
+    call = lambda d=d, ind=FAKE, ptr=FAKE, sl=FAKE, S=8, ws=FAKE, n=need: pkv.lib().paged_decode_plan_q8(  # noqa: E731
+        ctypes.byref(d), ind, ptr, sl, S, ws, n, None)
+    assert call(ind=None) == BAD and call(ptr=None) == BAD and call(sl=FAKE + 2) == BAD
+    assert call(S=0) == BAD and call(ws=None) == BAD and call(ws=FAKE + 16) == BAD
+    assert call(n=need - 1) == pkv.PKV_ERR_WORKSPACE_TOO_SMALL
+    assert call(d=_d(B=0)) == pkv.PKV_OK
+    # a batch of several launches has no plan: nothing is launched
+    d = _d(B=1025)
+    assert call(d=d, n=pkv.workspace_bytes(d, 8)) == pkv.PKV_OK
+
+
+def test_decode_limits():
+    """Shapes that the kernel cannot count are refused, the largest that it can are not."""
+    def call(**kw):
+        d = _d(**kw)
+        return pkv.lib().paged_decode_attn_q8(ctypes.byref(d), *[FAKE] * 8, 1, FAKE, 1 << 40, FAKE, None)
+
+    assert call(B=1, Hq=1031, Hkv=1031) == UNSUP                       # 1031 groups of one head
+    assert call(B=1, num_pages=1 << 27, page_size=16) == UNSUP         # 2^31 token slots
+    assert call(B=1, Hq=24, Hkv=24, max_seq_len=1 << 30) == UNSUP      # 3 groups of 2^30 tokens
+
+
 def test_tokens_of_torch_rows():
     q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     both = torch.zeros(3, 8, 64, dtype=torch.bfloat16)

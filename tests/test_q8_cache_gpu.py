@@ -316,8 +316,8 @@ def _ws(c, S):
 
 @pytest.mark.parametrize("Hq,Hkv,D,ps", [(32, 8, 128, 16), (8, 2, 64, 16), (5, 1, 64, 7), (48, 16, 128, 16)])
 def test_planned_calls_give_the_same_bits(Hq, Hkv, D, ps):
-    """On a plan made by paged_decode_plan, by this decode, and by the bf16
-    decode; and the bf16 decode on this decode's plan."""
+    """On a plan of its own making, and on one that the bf16 decode made (which it
+    does not use); the bf16 decode on either."""
     c = Cache([700, 0, 33, 64, 1, 2000], Hq, Hkv, D, ps, seed=D + Hkv).fill()
     c.k16.normal_()
     c.v16.normal_()
@@ -327,13 +327,15 @@ def test_planned_calls_give_the_same_bits(Hq, Hkv, D, ps):
         want16 = torch.empty_like(want)
         ws = _ws(c, S)
         pkv.paged_decode_attn(c.d, q, c.k16, c.v16, *c.rows, S, ws, want16)
-        for make in ("bf16", "plan", "q8"):
+        for make in ("bf16", "plan", "plan_q8", "q8"):
             ws = _ws(c, S)
             out = torch.full_like(want, float("nan"))
             if make == "bf16":
                 pkv.paged_decode_attn(c.d, q, c.k16, c.v16, *c.rows, S, ws, out)
             elif make == "plan":
                 pkv.paged_decode_plan(c.d, *c.rows, S, ws)
+            elif make == "plan_q8":
+                pkv.paged_decode_plan_q8(c.d, *c.rows, S, ws)
             else:
                 pkv.paged_decode_attn_q8(c.d, q, *c.q8, *c.rows, S, ws, out)
             out.fill_(float("nan"))
@@ -358,7 +360,7 @@ def test_planned_call_on_another_shapes_plan():
     pkv.paged_decode_attn(c.d, q, c.k16, c.v16, *c.rows, S, ws, want16)
     for splits in (S, 64):
         ws, out = pkv.alloc_workspace(other.d, 64, DEV), torch.empty_like(want)
-        pkv.paged_decode_plan(other.d, *other.rows, splits, ws)
+        pkv.paged_decode_plan_q8(other.d, *other.rows, splits, ws)
         pkv.paged_decode_attn_q8_planned(c.d, q, *c.q8, *c.rows, S, ws, out)
         assert torch.equal(out, want)
         ws = pkv.alloc_workspace(other.d, 64, DEV)
