@@ -146,8 +146,8 @@ __device__ __forceinline__ const int32_t *plan_entry(const int32_t *plan, int Bv
 __device__ __forceinline__ bool plan_fits(const int32_t *plan, int grid, int Bv, int B,
                                           int page_size, int row_cost)
 {
-    return plan[2] == grid && plan[3] == Bv && plan[4] == B && plan[5] == page_size &&
-           plan[6] == row_cost;
+    const int g = plan[2], bv = plan[3], b = plan[4], ps = plan[5], rc = plan[6];   // at once
+    return (g == grid) & (bv == Bv) & (b == B) & (ps == page_size) & (rc == row_cost);
 }
 
 } // namespace pkv
