@@ -477,7 +477,8 @@ pkv_status paged_decode_step_advance(const pkv_dims *dims, const void *q, const 
  *   q_out [T, Hq, D] packed receives the processed queries; it may be q
  *   itself where q is packed, and must not overlap it otherwise.
  *   q_norm, k_norm: nullable [D] bf16 weights of a per-head RMS norm, applied
- *   before the rotation: x * rsqrt(mean(x^2) + norm_eps) * weight.
+ *   before the rotation: x * rsqrt(mean(x^2) + norm_eps) * weight (the squares
+ *   are summed in fp32: heads of values past 1e18 overflow it).
  *   rope_cos_sin, rope_max_pos: the table of pkv_rope_table, or NULL for no
  *   rotation.
  * Every step is done in fp32 and the result rounded once. */
@@ -509,8 +510,9 @@ pkv_status paged_kv_append_norm(const pkv_dims *dims, const pkv_tokens *tokens, 
 
 /* The same for ragged chunks (qo_indptr, total_q and positions as in
  * paged_kv_extend).  A token before qo_indptr[0] or behind qo_indptr[B], and
- * every token of a row whose chunk is longer than its length or whose length
- * is above max_seq_len, sets PKV_FLAG_BAD_LEN and writes nothing. */
+ * every token of a row whose chunk leaves [0, total_q) or is longer than its
+ * length, or whose length is above max_seq_len, sets PKV_FLAG_BAD_LEN and
+ * writes nothing. */
 pkv_status paged_kv_extend_norm(const pkv_dims *dims, const pkv_tokens *tokens,
                                 const int32_t *qo_indptr, int total_q, void *k_pool,
                                 void *v_pool, const int32_t *kv_indices,
@@ -566,13 +568,15 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
  * softmax, num_splits, workspace and flags as for that call.  Scales as the
  * writes above choose them, or any in [127 - 40, 127 + 40]; the output of a row
  * holding others is undefined.  A NaN code reaches the outputs that read it, an
- * infinite query element its head's.  One persistent kernel plus, when
- * num_splits > 1, the piece combine; a batch of more than 1024 rows x kv-head
+ * infinite query element its head's.  Rows short by max_seq_len (at most 256 KB
+ * of K and V in a group of kv heads, 512 KB with rows x groups for half the
+ * SMs) are not split whatever num_splits is: one kernel.  Otherwise one
+ * persistent kernel plus, when num_splits > 1, the piece combine; a batch of more than 1024 rows x kv-head
  * groups (a group: 8, 4, 2 or 1 kv heads, the most that divide Hkv) takes
  * several such pairs, one after the other.  PKV_ERR_UNSUPPORTED: Hkv of more
  * than 1024 groups, or max_seq_len x groups or num_pages x page_size past 2^31.
- * A call of one pair leaves its partition in the workspace as the step's plan
- * for paged_decode_attn_q8_planned. */
+ * A call of one such pair leaves its partition in the workspace as the step's
+ * plan for paged_decode_attn_q8_planned (the others need none). */
 pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,
                                 const void *v_codes, const void *k_scale, const void *v_scale,
                                 const int32_t *kv_indices, const int32_t *kv_indptr,

@@ -603,6 +603,7 @@ pkv_status paged_decode_attn_planned(const pkv_dims *dims, const void *q, const 
 }
 
 static int q8_rows(const pkv_dims *dims, int hpc);
+static bool q8_whole(const pkv_dims *dims, int hpc, int *sms);
 
 static pkv_status plan_impl(const pkv_dims *dims, const int32_t *kv_indices,
                             const int32_t *kv_indptr, const int32_t *seq_lens, int num_splits,
@@ -626,7 +627,8 @@ static pkv_status plan_impl(const pkv_dims *dims, const int32_t *kv_indices,
     if (ws_bytes < need)
         return PKV_ERR_WORKSPACE_TOO_SMALL;
     const Layout L = layout_for(dims, num_splits);
-    if (q8 ? dims->B > q8_rows(dims, L.hpc) : !fused_path_ok(dims))
+    int sms;
+    if (q8 ? dims->B > q8_rows(dims, L.hpc) || q8_whole(dims, L.hpc, &sms) : !fused_path_ok(dims))
         return PKV_OK;                     // other shapes compute their split per call
     char *ws = static_cast<char *>(workspace);
     const pkv::FusedParams p =
@@ -1145,6 +1147,22 @@ static int q8_rows(const pkv_dims *dims, int hpc)
     return (int)(by_weight < by_rows ? by_weight : by_rows);
 }
 
+// Whether the decode over the 8-bit cache takes whole rows (kQ8WholeBytes), and
+// the device's SMs.
+static bool q8_whole(const pkv_dims *dims, int hpc, int *sms)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        *sms < 1) {
+        (void)cudaGetLastError();
+        *sms = 1;
+    }
+    const long long rows = (long long)dims->B * (dims->Hkv / hpc);
+    const long long bytes = (long long)dims->max_seq_len * hpc * dims->D * 2;
+    return bytes <= (2 * rows >= *sms ? 2 : 1) * pkv::kQ8WholeBytes;
+}
+
 static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void *k_codes,
                                  const void *v_codes, const void *k_scale, const void *v_scale,
                                  const int32_t *kv_indices, const int32_t *kv_indptr,
@@ -1160,9 +1178,16 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
         return PKV_ERR_INVALID_ARG;
     const Layout L = layout_for(dims, num_splits);
     const int groups = dims->Hkv / L.hpc;
-    const int most = q8_rows(dims, L.hpc);
+    int most = q8_rows(dims, L.hpc);
     if (most < 1)
         return PKV_ERR_UNSUPPORTED;
+    // short rows are not split: a block takes whole ones, up to kQ8MaxRows
+    int sms = 1;
+    const bool whole = q8_whole(dims, L.hpc, &sms);
+    if (whole) {
+        const long long rows = (long long)pkv::kQ8MaxRows * sms / groups;
+        most = rows < dims->B ? (int)rows : dims->B;
+    }
     // the kernel counts a pool's token slots in 31 bits
     if ((long long)dims->num_pages * dims->page_size >= (1ll << 31))
         return PKV_ERR_UNSUPPORTED;
@@ -1185,14 +1210,17 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
         p.ml_part = reinterpret_cast<float *>(ws + L.piece_ml_off);
         p.o_part = reinterpret_cast<float *>(ws + L.piece_ml_off +
                                              round_up(pieces * 2 * sizeof(float), 256));
-        // the plan is of all rows: a call of several launches has none
-        p.plan = one && planned ? plan : nullptr;
-        p.plan_out = one && !planned ? plan : nullptr;
+        // the plan is of all rows: a call of several launches has none, and one
+        // of whole rows needs none
+        p.whole_rows = whole ? 1 : 0;
+        p.plan = one && planned && !whole ? plan : nullptr;
+        p.plan_out = one && !planned && !whole ? plan : nullptr;
         p.scale_log2 = (float)((double)dims->scale * 1.4426950408889634);
-        st = launch_status(pkv::launch_decode_q8(p, d.D, num_splits, (cudaStream_t)stream));
+        const int grid = !whole ? num_splits : p.Bv < sms ? p.Bv : sms;
+        st = launch_status(pkv::launch_decode_q8(p, d.D, grid, (cudaStream_t)stream));
         if (st != PKV_OK)
             return st;
-        if (num_splits == 1)
+        if (whole || num_splits == 1)
             continue;
         pkv::PieceCombineParams c{};
         c.o_part = p.o_part;

@@ -260,6 +260,7 @@ struct FusedParams {
     const uint8_t *v_codes;
     const uint8_t *k_scale;
     const uint8_t *v_scale;
+    int whole_rows;        // each block takes whole rows: cta, cta + grid, ...
     // the step's plan (paged_decode_plan) or nullptr: the partition computed
     // at the kernel's start instead
     const int32_t *plan;
@@ -273,6 +274,16 @@ struct FusedParams {
 // 58.1, 58.4, 57.4, 57.9, 58.7, 59.0 us) and 8 rows of 513 to 1,025 tokens (10.6,
 // 10.0, 9.9, 9.2, 9.2, 9.2, 9.2 us).
 constexpr int kQ8RowCost = 64;
+// Over the 8-bit cache a row of at most this many bytes of K and V of a block's
+// kv heads (by max_seq_len) is not split, and twice as many where there are rows
+// x kv-head groups for half the SMs: no combine, and no block with dozens of
+// rows because the split count counts tokens alone.  Unsplit against split, us:
+//   8 heads of 128, 128 tokens (256 KB): 1 row 8.9, 9.7; 76 rows 9.2, 11.9; 512
+//   rows 28.5, 33.0.  192 (384 KB): 11.0, 9.9; 11.6, 13.8; 36.9, 39.3.  256
+//   (512 KB): 13.4, 9.9; 14.0, 14.7; 46.0, 46.1.  512: 22.2, 10.1; 23.4, 19.0;
+//   82.4, 74.9.  2 heads of 64, 32 rows of 512 (128 KB): 8.0, 10.3.  1 head of
+//   64, 76 rows of 512 (64 KB): 7.4, 12.0.
+constexpr long long kQ8WholeBytes = 256 << 10;
 // Rows x kv-head groups of one launch over the 8-bit cache (pkv_q8_decode.cu),
 // whose ring of stages needs the room of more prefix sums.
 constexpr int kQ8MaxRows = 1024;

@@ -65,16 +65,19 @@ __device__ __forceinline__ int checked_row_len(const FusedParams &p, int r, unsi
     return L;
 }
 
-// prefix[0..Bv] of the rows' partition weights (a non-empty row weighs its
-// tokens plus row_cost), computed by every thread of the block; report: OR
-// the flags of the first B rows into the status word.
-__device__ __forceinline__ void row_prefix(const FusedParams &p, int *prefix, bool report)
+// prefix[0..n] of n rows' partition weights (a non-empty row weighs its tokens
+// plus row_cost), computed by every thread of the block; row i of them is
+// virtual row row_of(i); report: OR the flags of the first B virtual rows into
+// the status word.
+template <typename RowOf>
+__device__ __forceinline__ void row_prefix(const FusedParams &p, int *prefix, int n, RowOf row_of,
+                                           bool report)
 {
-    const int Bv = p.Bv, lane = threadIdx.x & 31;
+    const int Bv = n, lane = threadIdx.x & 31;
     for (int r = threadIdx.x; r < Bv; r += blockDim.x) {
         unsigned bad = 0;
-        const int L = checked_row_len(p, r, bad);
-        if (bad && report && r < p.B)
+        const int L = checked_row_len(p, row_of(r), bad);
+        if (bad && report && row_of(r) < p.B)
             atomicOr(p.status, bad);
         prefix[r + 1] = L > 0 ? L + p.row_cost : 0;
     }
@@ -99,6 +102,12 @@ __device__ __forceinline__ void row_prefix(const FusedParams &p, int *prefix, bo
             prefix[0] = 0;
     }
     __syncthreads();
+}
+
+// The same of all virtual rows.
+__device__ __forceinline__ void row_prefix(const FusedParams &p, int *prefix, bool report)
+{
+    row_prefix(p, prefix, p.Bv, [](int r) { return r; }, report);
 }
 
 // Blocks that get work: at least kFusedMinTokens positions each, at most the

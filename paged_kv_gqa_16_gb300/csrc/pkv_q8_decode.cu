@@ -31,6 +31,8 @@
 //  - base is raised only when some y_t exceeds it by more than 8: a weight is
 //    then at most 2^8 and the usual tile needs no maximum over its lanes and
 //    no rescaling.
+//  - Short rows (kQ8WholeBytes) are not split: a block takes whole rows and
+//    writes their outputs, and there is no combine.
 //  - A kv head has WPH = 8 / HPC warps, which take 16 tokens each of every
 //    stage and have sums of their own, joined in pairs through shared memory at
 //    the end of a piece.  A warp takes two stages at a time: the products and
@@ -45,6 +47,12 @@
 //    times this kernel's time); boxes of 16 tokens x 128 bytes x heads took
 //    59.4 us for that batch against 58.3, 20.4 against 20.0 for a row of 32,768
 //    tokens, 54.5 against 44.4 for one kv head of 128, and no odd pages.
+//
+// Measured (CUDA-graph replay, K and V larger than L2 or rotating): 128 rows,
+// lognormal, 154,103 tokens, 64 over 8 heads of 128, 322 MB: 57.5 us, 5,600 GB/s,
+// 83% of the copy bandwidth (56.7 us with the products left out: the copies set
+// the pace); one row of 32,768: 20.0 us, 10 of them the stream, 5 the combine;
+// 8 rows of 513 to 1,025, heads of 64: 9.2 us, latency.
 #include <cmath>
 
 #include "pkv_partition.cuh"
@@ -184,30 +192,36 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     }
     grid_dependency_wait();
 
-    // the partition, from the step's plan or computed here (as in pkv_fused.cu)
+    // the partition, from the step's plan or computed here (as in pkv_fused.cu);
+    // or whole rows, of which this block takes every gridDim.x-th: its row r
+    // (of n_rows) is virtual row row_of(r)
+    const int n_rows = p.whole_rows ? (Bv - cta + (int)gridDim.x - 1) / (int)gridDim.x : Bv;
+    auto row_of = [&](int r) { return p.whole_rows ? cta + r * (int)gridDim.x : r; };
     bool planned = false;
-    if (p.plan != nullptr) {
+    if (p.whole_rows) {
+        row_prefix(p, prefix, n_rows, row_of, true);
+    } else if (p.plan != nullptr) {
         planned = plan_fits(p.plan, (int)gridDim.x, Bv, p.B, p.page_size, p.row_cost);
         for (int i = threadIdx.x; i <= Bv; i += C::kThreads)
             prefix[i] = p.plan[kPlanHeaderInts + i];
         __syncthreads();
     }
-    if (!planned)
+    if (!planned && !p.whole_rows)
         row_prefix(p, prefix, cta == 0);
 
-    const unsigned T = (unsigned)prefix[Bv];
+    const unsigned T = (unsigned)prefix[n_rows];
     const unsigned Gu = active_blocks(T, gridDim.x);
     const int G = (int)Gu;
 
     // rows with no tokens: zero output, no pieces (owner: block r mod grid)
-    for (int r = cta; r < Bv; r += gridDim.x) {
+    for (int r = p.whole_rows ? 0 : cta; r < n_rows; r += p.whole_rows ? 1 : gridDim.x) {
         if (prefix[r + 1] == prefix[r]) {
-            const int b = r % p.B, hg = r / p.B;
+            const int b = row_of(r) % p.B, hg = row_of(r) / p.B;
             uint4 *o = reinterpret_cast<uint4 *>(
                 p.out + ((size_t)b * p.Hq + (size_t)hg * HPC * p.n_rep) * D);
             for (int i = threadIdx.x; i < HPC * p.n_rep * D / 8; i += blockDim.x)
                 o[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (threadIdx.x == 0 && !planned) {
+            if (threadIdx.x == 0 && !planned && !p.whole_rows) {
                 p.row_info[2 * r] = 0;
                 p.row_info[2 * r + 1] = 0;
             }
@@ -231,14 +245,16 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     }
     const unsigned t_q = T / Gu, t_r = T % Gu;
     // (T < 2^31)
-    const int start = (int)(t_q * cta + t_r * (unsigned)cta / Gu);
-    const int end = (int)(t_q * (cta + 1) + t_r * (unsigned)(cta + 1) / Gu);
-    if (cta >= G || start >= end) {
+    const int start = p.whole_rows ? 0 : (int)(t_q * cta + t_r * (unsigned)cta / Gu);
+    const int end = p.whole_rows
+                        ? (int)T
+                        : (int)(t_q * (cta + 1) + t_r * (unsigned)(cta + 1) / Gu);
+    if ((cta >= G && !p.whole_rows) || start >= end) {
         if (plan_e != nullptr && threadIdx.x == 0)
             plan_e[0] = -1;
         return;
     }
-    const int r0 = first_row(prefix, Bv, start);
+    const int r0 = first_row(prefix, n_rows, start);
 
     if (warp >= kWarps) {
         // ======================= producer warps ===========================
@@ -254,7 +270,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
         auto page_of_tok = [&](int t) {
             return p.ps_shift >= 0 ? (t >> p.ps_shift) : (t / p.page_size);
         };
-        for (int r = r0; r < Bv && !aborted; ++r) {
+        for (int r = r0; r < n_rows && !aborted; ++r) {
             // [lo, hi): the positions of the row's tokens
             const int lo = prefix[r] + p.row_cost, hi = prefix[r + 1];
             if (lo >= end)
@@ -262,7 +278,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
             if (hi == prefix[r])
                 continue;
             const int t0 = max(start, lo) - lo, t1 = min(end, hi) - lo;
-            const int b = r % p.B, hg = r / p.B;
+            const int b = row_of(r) % p.B, hg = row_of(r) / p.B;
             const int pg0 = p.kv_indptr[b];
             int npg = p.kv_indptr[b + 1] - pg0;
             if (pg0 < 0 || npg < 0 || pg0 > p.num_indices - npg)
@@ -412,11 +428,10 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     const uint32_t k_off =
         smem_s + line_addr(tg * 16 + (lane & 15), hw * D + (lane >> 4) * 16);
     const uint32_t v_off = k_off + C::kTok * C::kRowBytes;
-    // lane (g, c)'s elements of head 8 nt + g of row r
-    auto load_q = [&](uint2 (&raw)[D / 16], int r, int nt) {
+    // lane (g, c)'s elements of head 8 nt + g of the heads from qrow0 on
+    auto load_q = [&](uint2 (&raw)[D / 16], size_t qrow0, int nt) {
         const int h = nt * 8 + g;
-        const __nv_bfloat16 *src =
-            p.q + ((size_t)(r % p.B) * p.Hq + (size_t)(r / p.B * HPC + hw) * p.n_rep + h) * D;
+        const __nv_bfloat16 *src = p.q + (qrow0 + h) * D;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
             raw[j] = h < p.n_rep ? __ldg(reinterpret_cast<const uint2 *>(src) + j * 4 + c)
@@ -425,14 +440,14 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     int it = 0;
     bool aborted = false;
 
-    for (int r = r0; r < Bv; ++r) {
+    for (int r = r0; r < n_rows; ++r) {
         const int lo = prefix[r] + p.row_cost, hi = prefix[r + 1];
         if (lo >= end)
             break;
         if (hi == prefix[r])
             continue;
         const int t0 = max(start, lo) - lo, t1 = min(end, hi) - lo;
-        const int b = r % p.B, hg = r / p.B;
+        const int b = row_of(r) % p.B, hg = row_of(r) / p.B;
         const size_t qrow0 = (size_t)b * p.Hq + (size_t)(hg * HPC + hw) * p.n_rep;
 
         // q as the products' B operand: lane (g, c) holds elements 4c .. 4c + 3
@@ -442,7 +457,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             uint2 raw[D / 16];
-            load_q(raw, r, nt);
+            load_q(raw, qrow0, nt);
             float amax = 0.f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
@@ -699,7 +714,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
             continue;
         // oacc[nt][j][e]: head 8 nt + 2c + (e & 1), column 16 j + 2g + (e >> 1)
         const bool whole = t0 == 0 && t1 == hi - lo;
-        if (t0 == 0 && warp == 0 && lane == 0 && !planned) {
+        if (t0 == 0 && warp == 0 && lane == 0 && !planned && !p.whole_rows) {
             p.row_info[2 * r] = cta;
             p.row_info[2 * r + 1] = whole ? 1 : block_of(hi - 1, T, G) - cta + 1;
         }

@@ -384,8 +384,8 @@ def _rows(x, name: str):
     """(pointer, row stride) of new-token rows [T, H, D] whose heads are packed."""
     T, H, D = x.shape
     row, head, one = x.stride()
-    if one != 1 or (head != D and H > 1):
-        raise ValueError(f"{name} must be [tokens, heads, D] with packed heads")
+    if one != 1 or (head != D and H > 1) or x.element_size() != 2:
+        raise ValueError(f"{name} must be bf16 [tokens, heads, D] with packed heads")
     return x.data_ptr(), row if T > 1 else 0
 
 

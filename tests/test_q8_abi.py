@@ -149,6 +149,8 @@ def test_tokens_of_torch_rows():
     with pytest.raises(ValueError):
         pkv.tokens(q[..., ::2], k, k)
     with pytest.raises(ValueError):
+        pkv.tokens(q.float(), k, k)
+    with pytest.raises(ValueError):
         pkv._token_count(_d(B=3), pkv.tokens(q, k, k))                         # other heads
     with pytest.raises(ValueError):
         pkv._token_count(_d(B=4, Hq=4, Hkv=2, D=64), pkv.tokens(q, k, k), per_row=True)

@@ -455,3 +455,35 @@ def test_shared_pages_and_the_same_page_twice():
     out, status = c.decode(q)
     assert status == 0
     c.check_decode(q, out)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(4, 2, 64, 16), (32, 8, 128, 16), (5, 1, 64, 1), (48, 3, 128, 7),
+                                         (64, 16, 64, 32)])
+@pytest.mark.parametrize("most", [1, 16, 128, 257])
+def test_decode_short_rows(Hq, Hkv, D, ps, most):
+    """Short rows are not split (the limit is in bytes of a group of heads: 256
+    tokens and more here); more rows than blocks, empty ones among them, planned
+    and not, whatever the split count."""
+    lens = [(i * 37) % (most + 1) for i in range(331)]
+    c = Cache(lens, Hq, Hkv, D, ps, seed=most, max_seq_len=most).fill()
+    q = _q(c)
+    for S in (pkv.plan(c.d)[0], 1):
+        ws, out = _ws(c, S), torch.full((331, Hq, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+        pkv.paged_decode_attn_q8(c.d, q, *c.q8, *c.rows, S, ws, out)
+        assert pkv.status_word(ws) == 0
+        c.check_decode(q, out)
+        again = torch.full_like(out, float("nan"))
+        pkv.paged_decode_attn_q8_planned(c.d, q, *c.q8, *c.rows, S, ws, again)
+        assert torch.equal(out, again)
+
+
+def test_decode_short_rows_flags():
+    c = Cache([40, 90, 64], 8, 2, 64, 16, seed=5, max_seq_len=80).fill()
+    c.seq_lens[0] = -3
+    c.kv_indices[c.starts[2]] = -1
+    q = _q(c)
+    out, status = c.decode(q)
+    assert status == pkv.FLAG_BAD_LEN | pkv.FLAG_BAD_PAGE
+    assert float(out[0].float().abs().max()) == 0
+    want, bound = attention(q[1].cpu(), *c.held(1, 80), c.scale)        # cut to 80 tokens
+    assert bool(((out[1].cpu().double() - want).abs() <= bound).all())

@@ -229,6 +229,9 @@ def test_extend_flags():
     assert write([0, 6, 10, 12]) == (pkv.FLAG_BAD_LEN, [False] * 6 + [True] * 6)
     # tokens before the first row and behind the last
     assert write([1, 4, 9, 11]) == (pkv.FLAG_BAD_LEN, [False] + [True] * 10 + [False])
+    # chunks that leave the tokens given
+    assert write([-1, 4, 10, 12]) == (pkv.FLAG_BAD_LEN, [False] * 4 + [True] * 8)
+    assert write([0, 4, 10, 13]) == (pkv.FLAG_BAD_LEN, [True] * 10 + [False] * 2)
 
 
 def test_rows_of_one_projection_and_64_bit_offsets():
