@@ -44,9 +44,10 @@ constexpr int kMaxTokens = 32;       // tokens a block takes at most
 // 2 and 1: 73.8; 27.1.  4 and 2: 71.2; 29.9.  2 and 1, four blocks: 72.6; 26.3.
 constexpr int kQ = 4;
 constexpr int kKv = 1;
-// Blocks that fill the GPU several times over (the D = 64 case above, 2 and 1 with
-// four blocks: 23.9 us; with 2048: 26.3, with 4096: 33.5).
-constexpr int kManyBlocks = 1024;
+// From this many blocks on, a token gets fewer groups (1,456 tokens of D = 64: 13.4
+// us with 1024 or 2048 here, 8.4 with 512, 5.5 with 256, 6.3 with 128; 364 tokens:
+// 4.9 with 256, 4.4 with 128; 1,024 of 8 + 1 heads of 64: 5.1, 4.2).
+constexpr int kManyBlocks = 128;
 
 struct TokenPlace {
     int pos;                         // -1: the token writes nothing
@@ -363,8 +364,8 @@ cudaError_t launch(const TokenWriteParams &params, cudaStream_t stream)
     constexpr int kGroupsShift = D == 64 ? 5 : 4;       // groups of a block
     TokenWriteParams p = params;
     // As many groups a token as it has vectors of a kind, for few tokens; with
-    // more tokens than fill the GPU a dozen times over, fewer, which then share
-    // the coefficients among more vectors.
+    // more, fewer (of 8 vectors at least: with 16, 16,384 tokens gain 1%, 4,096 lose
+    // 9%), which then share the coefficients among more vectors.
     const int heads = p.Hq > p.Hkv ? p.Hq : p.Hkv;
     p.width_shift = 0;
     while (p.width_shift < kGroupsShift && (1 << p.width_shift) < heads)
