@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                 // the bf16 decode's entry holds a 64-entry window of the table
                 const int wb = (page_of_tok(t0) >> 5) << 5;
                 for (int k = lane; k < 64; k += 32)
-                    plan_e[8 + k] = wb + k < npg ? __ldg(p.kv_indices + pg0 + wb + k) : 0;
+                    plan_e[8 + k] = wb + k < npg ? p.kv_indices[pg0 + wb + k] : 0;
                 if (lane < 8) {
                     plan_e[lane] = lane == 0 ? r0 : lane == 1 ? wb : lane == 2 ? pg0
                                  : lane == 3 ? npg : lane == 4 ? lo : lane == 5 ? hi
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                 const int at = k * 32 + lane;
                 const bool there = at < C::kTok && tok + at < t1;
                 const int pi = page_of_tok(there ? tok + at : 0);
-                return there && pi < npg ? __ldg(p.kv_indices + pg0 + pi) : 0;
+                return there && pi < npg ? p.kv_indices[pg0 + pi] : 0;
             };
             // the ids of this warp's next stage are loaded a stage ahead
             int ids[IDS];
@@ -428,13 +428,15 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     const uint32_t k_off =
         smem_s + line_addr(tg * 16 + (lane & 15), hw * D + (lane >> 4) * 16);
     const uint32_t v_off = k_off + C::kTok * C::kRowBytes;
-    // lane (g, c)'s elements of head 8 nt + g of the heads from qrow0 on
+    // lane (g, c)'s elements of head 8 nt + g of the heads from qrow0 on (plain
+    // loads, here and for the tables: the grid before may have written them
+    // while this one was already on the GPU)
     auto load_q = [&](uint2 (&raw)[D / 16], size_t qrow0, int nt) {
         const int h = nt * 8 + g;
         const __nv_bfloat16 *src = p.q + (qrow0 + h) * D;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
-            raw[j] = h < p.n_rep ? __ldg(reinterpret_cast<const uint2 *>(src) + j * 4 + c)
+            raw[j] = h < p.n_rep ? reinterpret_cast<const uint2 *>(src)[j * 4 + c]
                                  : make_uint2(0u, 0u);
     };
     int it = 0;
