@@ -151,7 +151,7 @@ def _check(fn: str, code: int) -> None:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
     if x.is_contiguous():
         return x.data_ptr()
@@ -380,15 +380,6 @@ def paged_kv_extend(d: Dims, q, k_new, v_new, qo_indptr, k_pool, v_pool, kv_indi
 
 
 # ---- new tokens: normalised, rotated, written --------------------------------
-def _rows(x, name: str):
-    """(pointer, row stride) of new-token rows [T, H, D] whose heads are packed."""
-    T, H, D = x.shape
-    row, head, one = x.stride()
-    if one != 1 or (head != D and H > 1) or x.element_size() != 2:
-        raise ValueError(f"{name} must be bf16 [tokens, heads, D] with packed heads")
-    return x.data_ptr(), row if T > 1 else 0
-
-
 def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6,
            rope_cos_sin=None, rope_max_pos: int = 0) -> Tokens:
     """The new tokens of a paged_kv_append_norm / _extend_norm / _append_q8 /
@@ -399,19 +390,28 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
     T, Hkv, D = shape = k.shape
     if shape != v.shape:
         raise ValueError("k and v must have the same shape")
-    kp, k_row = _rows(k, "k")
-    vp, v_row = _rows(v, "v")
-    if q is None:
-        Hq = qp = out = q_norm = None
-        q_row = 0
-    else:
+    k_row, k_head, k_one = k.stride()
+    v_row, v_head, v_one = v.stride()
+    # a head's elements next to each other, a row's heads too; two bytes each
+    ok = k_one == v_one == 1 and (k_head == v_head == D or Hkv == 1) and (
+        k.element_size() == v.element_size() == 2)
+    Hq = qp = out = qn = None
+    q_row = 0
+    if q is not None:
         qT, Hq, qD = q.shape
         if qT != T or qD != D:
             raise ValueError("q and k must have the same tokens and head size")
-        qp, q_row = _rows(q, "q")
+        q_row, q_head, q_one = q.stride()
+        ok = ok and q_one == 1 and (q_head == D or Hq == 1) and q.element_size() == 2
+        qp = q.data_ptr()
         out = qp if q_out is None else _ptr(q_out)
-    t = Tokens(qp, kp, vp, q_row, k_row, v_row, out, _ptr(q_norm), _ptr(k_norm), norm_eps,
-               _ptr(rope_cos_sin), rope_max_pos)
+        qn = _ptr(q_norm)
+    if not ok:
+        raise ValueError("q, k and v must be bf16 [tokens, heads, D] with packed heads")
+    if T <= 1:
+        q_row = k_row = v_row = 0                 # a single row is packed
+    t = Tokens(qp, k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, out,
+               qn, _ptr(k_norm), norm_eps, _ptr(rope_cos_sin), rope_max_pos)
     t.shape = (T, Hq, Hkv, D)
     t.tensors = (q, k, v, q_out, q_norm, k_norm, rope_cos_sin)
     return t
