@@ -475,10 +475,11 @@ pkv_status paged_decode_step_advance(const pkv_dims *dims, const void *q, const 
  *   heads of a row are packed.
  *   q == NULL: no query work (q_out, q_norm and q_stride are then ignored).
  *   q_out [T, Hq, D] packed receives the processed queries; it may be q
- *   itself where q is packed, and must not overlap it otherwise.
+ *   itself where q is packed, and must not overlap q, k or v otherwise.
  *   q_norm, k_norm: nullable [D] bf16 weights of a per-head RMS norm, applied
  *   before the rotation: x * rsqrt(mean(x^2) + norm_eps) * weight (the squares
- *   are summed in fp32: heads of values past 1e18 overflow it).
+ *   are summed in fp32: heads of values past 1e18 overflow it, and squares of
+ *   values below 1e-22 are lost beside norm_eps = 0).
  *   rope_cos_sin, rope_max_pos: the table of pkv_rope_table, or NULL for no
  *   rotation.
  * Every step is done in fp32 and the result rounded once. */

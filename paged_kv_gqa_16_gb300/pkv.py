@@ -383,8 +383,8 @@ def paged_kv_extend(d: Dims, q, k_new, v_new, qo_indptr, k_pool, v_pool, kv_indi
 def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6,
            rope_cos_sin=None, rope_max_pos: int = 0) -> Tokens:
     """The new tokens of a paged_kv_append_norm / _extend_norm / _append_q8 /
-    _extend_q8 call: q [T, Hq, D] (or None), k and v [T, Hkv, D] bf16 with any
-    row stride (slices of one projection's output), q_out [T, Hq, D] for the
+    _extend_q8 call: q [T, Hq, D] (or None), k and v [T, Hkv, D] bf16 whose rows
+    do not overlap (slices of one projection's output; no expanded rows), q_out [T, Hq, D] for the
     processed queries (None: in place, which needs a packed q), optional [D]
     norm weights, and the RoPE table."""
     T, Hkv, D = shape = k.shape
@@ -406,10 +406,20 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
         qp = q.data_ptr()
         out = qp if q_out is None else _ptr(q_out)
         qn = _ptr(q_norm)
-    if not ok:
-        raise ValueError("q, k and v must be bf16 [tokens, heads, D] with packed heads")
+        ok = ok and (q_row > 0 or T <= 1)
+        if q_out is not None and q_out.numel() * q_out.element_size() < T * Hq * D * 2:
+            raise ValueError("q_out must hold bf16 [tokens, heads, D]")
+        if q_norm is not None and (q_norm.numel() != D or q_norm.element_size() != 2):
+            raise ValueError("q_norm must be bf16 [D]")
+    if k_norm is not None and (k_norm.numel() != D or k_norm.element_size() != 2):
+        raise ValueError("k_norm must be bf16 [D]")
     if T <= 1:
         q_row = k_row = v_row = 0                 # a single row is packed
+    elif not (k_row > 0 and v_row > 0):
+        ok = False                                # (0 would be taken for packed)
+    if not ok:
+        raise ValueError("q, k and v must be bf16 [tokens, heads, D] with packed heads and "
+                         "rows of their own")
     t = Tokens(qp, k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, out,
                qn, _ptr(k_norm), norm_eps, _ptr(rope_cos_sin), rope_max_pos)
     t.shape = (T, Hq, Hkv, D)

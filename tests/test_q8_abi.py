@@ -154,3 +154,21 @@ def test_tokens_of_torch_rows():
         pkv._token_count(_d(B=3), pkv.tokens(q, k, k))                         # other heads
     with pytest.raises(ValueError):
         pkv._token_count(_d(B=4, Hq=4, Hkv=2, D=64), pkv.tokens(q, k, k), per_row=True)
+
+
+def test_tokens_refuse_expanded_rows_and_short_tensors():
+    """A row stride of 0 stands for packed rows in the C call: rows that share memory would
+    be read past their end."""
+    q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    w = torch.zeros(64, dtype=torch.bfloat16)
+    for bad in ((q[:1].expand(3, 4, 64), k, k), (q, k[:1].expand(3, 2, 64), k),
+                (q, k, k[:1].expand(3, 2, 64))):
+        with pytest.raises(ValueError):
+            pkv.tokens(*bad, torch.empty_like(q))
+    assert pkv.tokens(q[:1], k[:1].expand(1, 2, 64), k[:1], torch.empty_like(q)).k_stride == 0
+    with pytest.raises(ValueError):
+        pkv.tokens(q, k, k, torch.empty_like(q[:2]))
+    for kw in (dict(q_norm=w[:32]), dict(q_norm=w.float()), dict(k_norm=w[:32]), dict(k_norm=w.float())):
+        with pytest.raises(ValueError):
+            pkv.tokens(q, k, k, torch.empty_like(q), **kw)
+    assert pkv.tokens(q, k, k, torch.empty_like(q), w, w).k_norm == w.data_ptr()
