@@ -18,17 +18,17 @@
 // all the token's query heads (and once for its K heads):
 //   y[2i]   = r (x[2i] (w c) - x[2i+1] (w' s)),
 //   y[2i+1] = r (x[2i] (w s) + x[2i+1] (w' c)),   r = rsqrt(mean + eps),
-// in two-wide fp32 operations.  `width` groups share a token; a block's tokens
-// are looked up once into shared memory while their first vectors are already
-// on their way.
+// in two-wide fp32 operations.  `width` groups share a token.  Every warp looks up
+// its own tokens' rows, pages and rotations while their first vectors are already
+// on their way: a block that looks up its tokens together and waits at a barrier
+// takes 5% (4 x 4,096 tokens) to 14% longer, as each dependent load of the look-up
+// queues behind the stream.
 //
 // Measured (CUDA-graph replay): 4 prompts of 4,096 tokens, 32 + 8 heads of 128,
-// norms, 405 MB: 70.7 us, 5,730 GB/s, 84% of the copy bandwidth (98 us with a
-// vector a group at a time and the rotation's products made for each); the 8-bit
-// form on 18,425 tokens, 416 MB: 72.1 us, 85%; 9,537 tokens of 32 + 8 heads of 64,
-// 108 MB: 24.6 us, 65%, the arithmetic of a 16-byte load being the same for
-// half the head; one token of 8 to 128 rows: 3.1 to 3.9 us, the launch and three
-// dependent loads.
+// norms, 405 MB: 66.5 us, 6,090 GB/s, 90% of the copy bandwidth; the 8-bit form on
+// 18,425 tokens, 416 MB: 67.7 us, 91%; 9,537 tokens of 32 + 8 heads of 64, 108 MB:
+// 21.3 us, 75% (an elementwise kernel of as many bytes takes 18 us); one token of 8
+// to 128 rows: 2.4 to 3.6 us, the launch and three dependent loads.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_q8.cuh"
@@ -37,73 +37,111 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 32;       // tokens a block takes at most
-// Query vectors, and K and V vectors, that a group has in flight, with three
-// blocks an SM (4 x 4,096 tokens; 9,537 of D = 64): 4 and 1: 70.6; 26.5 us.
-// 2 and 1: 73.8; 27.1.  4 and 2: 71.2; 29.9.  2 and 1, four blocks: 72.6; 26.3.
-constexpr int kQ = 4;
+// Threads of a block: those of one token, at least kMinThreads.  Few threads keep
+// the SMs' shares even at the end: 64 against 128 and 256 gain up to 2% and 5%.
+constexpr int kMinThreads = 64;
+constexpr int kMaxThreads = 256;
+// Query vectors, and K and V vectors, that a group has in flight, at 80 registers
+// (768 threads an SM).  Extends of 16,384 tokens, 9,537 of D = 64 and 512 tokens: 4
+// and 1 take 67.1, 21.6 and 4.8 us; 2 and 1 71.9, 23.3 and 4.8; 3 and 1 69.3, 22.5
+// and 5.0; 4 and 2 66.3, 22.5 and 5.1; 2 and 1 at 64 registers 67.5, 21.1 and 5.1.
+// One token of 8 and of 32 rows: 4 and 1 2.8 and 2.9 us, 2 and 1 2.4 and 2.6.
+constexpr int kQExtend = 4;
+constexpr int kQAppend = 2;
 constexpr int kKv = 1;
-// From this many blocks on, a token gets fewer groups (1,456 tokens of D = 64: 13.4
-// us with 1024 or 2048 here, 8.4 with 512, 5.5 with 256, 6.3 with 128; 364 tokens:
-// 4.9 with 256, 4.4 with 128; 1,024 of 8 + 1 heads of 64: 5.1, 4.2).
-constexpr int kManyBlocks = 128;
+// From this many threads on, a token gets fewer groups (1,456 tokens of D = 64: 5.6
+// us with 16384 or 32768 here, 5.2 with 65536; 364: 3.5, 3.7, 4.6; 1,024 of 8 + 1
+// heads of 64: 3.3, 3.5, 4.6; one token of 128 rows of 64 + 8 heads of 128: 4.5, 3.4,
+// 3.5).
+constexpr long long kManyThreads = 32768;
 
-struct TokenPlace {
-    int pos;                         // -1: the token writes nothing
-    unsigned slot_hi, slot_lo;       // flat pool slot (page * page_size + slot)
+// What a token's row says of it.
+struct TokenRow {
+    int pos;                             // position, -1: the token writes nothing
+    int at;                              // its entry of kv_indices, -1: none
+    int in_page;                         // its place in that page
+    unsigned bad;                        // kFlag*
 };
 
-// Row, position and slot of token t; flags in `bad` (kFlag*), pos -1 if it
-// writes nothing.
 template <bool EXTEND>
-__device__ __forceinline__ TokenPlace place_token(const TokenWriteParams &p, int t, unsigned &bad)
+__device__ __forceinline__ TokenRow token_row(const TokenWriteParams &p, int t, int a, int e, int L,
+                                              int pg0, int pg1)
 {
-    TokenPlace r{-1, 0, 0};
-    int b = t, pos;
+    TokenRow r{-1, -1, 0, 0};
+    int pos = L - 1;
     if constexpr (EXTEND) {
-        int lo = 0, hi = p.B - 1;    // the last row that starts at or before t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.qo_indptr[mid] <= t)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        b = lo;
-        const int a = p.qo_indptr[b], e = p.qo_indptr[b + 1];
-        const int L = p.seq_lens[b];
         if (a < 0 || e > p.T || t < a || t >= e || e - a > L || L > p.max_seq_len) {
-            bad |= kFlagBadLen;
+            r.bad = kFlagBadLen;
             return r;
         }
         pos = L - (e - a) + (t - a);
-    } else {
-        const int L = p.seq_lens[b];
-        if (L <= 0 || L > p.max_seq_len) {
-            if (L != 0)
-                bad |= kFlagBadLen;
-            return r;
-        }
-        pos = L - 1;
-    }
-    const int pg0 = p.kv_indptr[b], pg1 = p.kv_indptr[b + 1];
-    const int pi = pos / p.page_size;
-    int page = -1;
-    if (pg0 >= 0 && pg1 >= pg0 && pg1 <= p.num_indices && pi < pg1 - pg0)
-        page = p.kv_indices[pg0 + pi];
-    if (page < 0 || page >= p.num_pages)
-        bad |= kFlagBadPage;
-    if (p.rope != nullptr && pos >= p.rope_max_pos)
-        bad |= kFlagBadPos;
-    if (bad)
+    } else if (L <= 0 || L > p.max_seq_len) {
+        r.bad = L != 0 ? kFlagBadLen : 0;
         return r;
-    const unsigned long long slot =
-        (unsigned long long)page * p.page_size + (unsigned)(pos - pi * p.page_size);
+    }
+    const int pi = pos / p.page_size;
+    if (pg0 >= 0 && pg1 >= pg0 && pg1 <= p.num_indices && pi < pg1 - pg0)
+        r.at = pg0 + pi;
+    if (p.rope != nullptr && pos >= p.rope_max_pos)
+        r.bad = kFlagBadPos;
     r.pos = pos;
-    r.slot_hi = (unsigned)(slot >> 32);
-    r.slot_lo = (unsigned)slot;
+    r.in_page = pos - pi * p.page_size;
     return r;
+}
+
+// The row of each lane's token t, whose least in the warp is t0 (lane 0's); every
+// lane calls it.  Dependent loads are the time of a small call, and of a warp that
+// waits for them: a row's words are loaded at once, and for an extend those of 32
+// rows from the first token's on, of which a lane takes its own by shuffles.
+template <bool EXTEND>
+__device__ __forceinline__ TokenRow row_of_token(const TokenWriteParams &p, int t)
+{
+    constexpr unsigned kAll = 0xffffffffu;
+    if constexpr (!EXTEND) {
+        return token_row<false>(p, t, 0, 0, p.seq_lens[t], p.kv_indptr[t], p.kv_indptr[t + 1]);
+    } else {
+        const int lane = threadIdx.x & 31, t0 = __shfl_sync(kAll, t, 0);
+        int lo = 0, n = p.B;             // the first token's row is in [lo, lo + n)
+        while (n > 32) {
+            const int step = (n + 31) / 32, i = lane * step;
+            const int hits = __popc(__ballot_sync(kAll, i < n && p.qo_indptr[lo + i] <= t0));
+            const int to = hits > 0 ? (hits - 1) * step : 0;
+            lo += to;
+            n = min(step, n - to);
+        }
+        const int row = min(lo + lane, p.B - 1);
+        int a = p.qo_indptr[row], e = p.qo_indptr[row + 1], L = p.seq_lens[row];
+        int pg0 = p.kv_indptr[row], pg1 = p.kv_indptr[row + 1];
+        int k = 0;                       // the last of the rows that starts at or before t
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) {
+            const int start = __shfl_sync(kAll, a, k + s);
+            if (lo + k + s < p.B && start <= t)
+                k += s;
+        }
+        const int next = __shfl_sync(kAll, e, 31);
+        a = __shfl_sync(kAll, a, k);
+        e = __shfl_sync(kAll, e, k);
+        L = __shfl_sync(kAll, L, k);
+        pg0 = __shfl_sync(kAll, pg0, k);
+        pg1 = __shfl_sync(kAll, pg1, k);
+        int b = lo + k;
+        if (k == 31 && b + 1 < p.B && next <= t) {
+            // past the 32 rows: steps that double while rows start at or before the
+            // token, and halve behind the last of them
+            int by = 1;
+            while (b + by < p.B && p.qo_indptr[b + by] <= t) {
+                b += by;
+                by <<= 1;
+            }
+            while (by >>= 1)
+                if (b + by < p.B && p.qo_indptr[b + by] <= t)
+                    b += by;
+            a = p.qo_indptr[b], e = p.qo_indptr[b + 1], L = p.seq_lens[b];
+            pg0 = p.kv_indptr[b], pg1 = p.kv_indptr[b + 1];
+        }
+        return token_row<true>(p, t, a, e, L, pg0, pg1);
+    }
 }
 
 template <int LANES>
@@ -245,13 +283,13 @@ __device__ __forceinline__ uint2 quantise(const Eight &x, float f, int &sb)
 
 // A block takes GROUPS / p.width tokens, p.width groups (a power of two) each.
 template <int D, bool Q8, bool EXTEND>
-__global__ void __launch_bounds__(kThreads, 3) token_write_kernel(const TokenWriteParams p)
+__global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const TokenWriteParams p)
 {
     constexpr int LANES = D / 8;             // lanes of a head vector
-    __shared__ TokenPlace s_place[kMaxTokens];
+    constexpr int kQ = EXTEND ? kQExtend : kQAppend;
     grid_dependency_wait();
     const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    const int at_once = kThreads / LANES >> p.width_shift;
+    const int at_once = (int)blockDim.x / LANES >> p.width_shift;
     const int t0 = blockIdx.x * at_once, tok = group >> p.width_shift;
     const int nt = min(at_once, p.T - t0);
     const int width = 1 << p.width_shift, v0 = group & (width - 1);
@@ -261,47 +299,46 @@ __global__ void __launch_bounds__(kThreads, 3) token_write_kernel(const TokenWri
     const __nv_bfloat16 *k = p.k + t * p.k_stride + lane * 8;
     const __nv_bfloat16 *v = p.v + t * p.v_stride + lane * 8;
 
-    auto load = [&](const __nv_bfloat16 *src, int h, int H) {
-        return h < H ? __ldcs(reinterpret_cast<const uint4 *>(src + h * D))
-                     : make_uint4(0u, 0u, 0u, 0u);
+    // (a vector past the last keeps what it held and is not stored)
+    auto load = [&](uint4 &to, const __nv_bfloat16 *src, int h, int H) {
+        if (h < H)
+            to = __ldcs(reinterpret_cast<const uint4 *>(src + h * D));
     };
     // the first vectors do not wait for the look-up
-    uint4 rq[kQ], rk[kKv], rv[kKv];
+    uint4 rq[kQ] = {}, rk[kKv] = {}, rv[kKv] = {};
 #pragma unroll
     for (int u = 0; u < kQ; ++u)
-        rq[u] = load(q, v0 + u * width, p.Hq);
+        load(rq[u], q, v0 + u * width, p.Hq);
 #pragma unroll
     for (int u = 0; u < kKv; ++u) {
-        rk[u] = load(k, v0 + u * width, p.Hkv);
-        rv[u] = load(v, v0 + u * width, p.Hkv);
+        load(rk[u], k, v0 + u * width, p.Hkv);
+        load(rv[u], v, v0 + u * width, p.Hkv);
     }
     const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     uint4 wq = ones, wk = ones;
     if (p.q_norm != nullptr)
         wq = *(reinterpret_cast<const uint4 *>(p.q_norm) + lane);
-    if (p.k_norm != nullptr)
-        wk = *(reinterpret_cast<const uint4 *>(p.k_norm) + lane);
 
-    if (threadIdx.x < nt) {
-        unsigned bad = 0;
-        s_place[threadIdx.x] = place_token<EXTEND>(p, t0 + threadIdx.x, bad);
-        if (bad && p.status != nullptr)
-            atomicOr(p.status, bad);
-    }
-    __syncthreads();
+    // (an extend reads the keys' weight when it needs it: its registers would spill,
+    // 69.2 us in place of 67.1)
+    if (!EXTEND && p.k_norm != nullptr)
+        wk = *(reinterpret_cast<const uint4 *>(p.k_norm) + lane);
+    TokenRow row = row_of_token<EXTEND>(p, (int)t);
+    const int page = row.at >= 0 ? p.kv_indices[row.at] : -1;
     grid_launch_dependents();
-    TokenPlace place{-1, 0, 0};
-    if (tok < nt)
-        place = s_place[tok];
-    const bool live = place.pos >= 0;
-    const size_t slot = ((size_t)place.slot_hi << 32) | place.slot_lo;
     float4 c01 = make_float4(1.f, 0.f, 1.f, 0.f), c23 = c01;
-    if (p.rope != nullptr && live) {
+    if (p.rope != nullptr && row.pos >= 0 && row.bad == 0) {
         const float4 *cs =
-            reinterpret_cast<const float4 *>(p.rope + (size_t)place.pos * D) + lane * 2;
+            reinterpret_cast<const float4 *>(p.rope + (size_t)row.pos * D) + lane * 2;
         c01 = cs[0];
         c23 = cs[1];
     }
+    if (row.pos >= 0 && (page < 0 || page >= p.num_pages))
+        row.bad |= kFlagBadPage;
+    if (row.bad != 0 && lane == 0 && v0 == 0 && p.status != nullptr)
+        atomicOr(p.status, row.bad);
+    const bool live = tok < nt && row.pos >= 0 && row.bad == 0;
+    const long long slot = (long long)page * p.page_size + row.in_page;
 
     // query heads; every lane runs the same rounds, as the shuffles need whole warps
     {
@@ -312,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_write_kernel(const TokenWri
             for (int u = 0; u < kQ; ++u) {
                 const int h = h0 + u * width + v0;
                 Eight x = unpack(rq[u]);
-                rq[u] = load(q, h + kQ * width, p.Hq);
+                load(rq[u], q, h + kQ * width, p.Hq);
                 const float f = p.q_norm != nullptr ? norm_factor<D>(x, p.norm_eps) : 1.f;
                 apply(x, turn, p.rope != nullptr);
                 if (live && h < p.Hq)
@@ -321,6 +358,8 @@ __global__ void __launch_bounds__(kThreads, 3) token_write_kernel(const TokenWri
         }
     }
     // K and V heads
+    if (EXTEND && p.k_norm != nullptr)
+        wk = *(reinterpret_cast<const uint4 *>(p.k_norm) + lane);
     const Turn turn = turn_of(c01, c23, unpack(wk));
     for (int h0 = 0; h0 < p.Hkv; h0 += kKv * width) {
 #pragma unroll
@@ -328,12 +367,12 @@ __global__ void __launch_bounds__(kThreads, 3) token_write_kernel(const TokenWri
             const int h = h0 + u * width + v0;
             const uint4 vraw = rv[u];
             Eight x = unpack(rk[u]);
-            rk[u] = load(k, h + kKv * width, p.Hkv);
-            rv[u] = load(v, h + kKv * width, p.Hkv);
+            load(rk[u], k, h + kKv * width, p.Hkv);
+            load(rv[u], v, h + kKv * width, p.Hkv);
             const float f = p.k_norm != nullptr ? norm_factor<D>(x, p.norm_eps) : 1.f;
             apply(x, turn, p.rope != nullptr);
             const bool store = live && h < p.Hkv;
-            const size_t head = slot * p.Hkv + h;
+            const size_t head = (size_t)slot * p.Hkv + h;
             if constexpr (Q8) {
                 int sk, sv;
                 const uint2 kc = quantise<D>(x, f, sk);
@@ -361,22 +400,24 @@ __global__ void __launch_bounds__(kThreads, 3) token_write_kernel(const TokenWri
 template <int D, bool Q8, bool EXTEND>
 cudaError_t launch(const TokenWriteParams &params, cudaStream_t stream)
 {
-    constexpr int kGroupsShift = D == 64 ? 5 : 4;       // groups of a block
+    constexpr int kLanes = D / 8;
     TokenWriteParams p = params;
     // As many groups a token as it has vectors of a kind, for few tokens; with
-    // more, fewer (of 8 vectors at least: with 16, 16,384 tokens gain 1%, 4,096 lose
-    // 9%), which then share the coefficients among more vectors.
+    // more, fewer (of 8 vectors at least: with 4, 16,384 tokens of 32 heads of 128
+    // take 74.7 us in place of 67.1; with 16, they take 66.6, 9,537 of D = 64 23.9 in
+    // place of 21.6), which then share the coefficients among more vectors.
     const int heads = p.Hq > p.Hkv ? p.Hq : p.Hkv;
     p.width_shift = 0;
-    while (p.width_shift < kGroupsShift && (1 << p.width_shift) < heads)
+    while (kLanes << p.width_shift < kMaxThreads && (1 << p.width_shift) < heads)
         ++p.width_shift;
     while (p.width_shift > 0 && (heads >> p.width_shift) < 8 &&
-           (p.T >> (kGroupsShift - p.width_shift + 1)) >= kManyBlocks)
+           (long long)p.T * (kLanes << p.width_shift >> 1) >= kManyThreads)
         --p.width_shift;
-    const int at_once = 1 << (kGroupsShift - p.width_shift);
+    const int wide = kLanes << p.width_shift;            // threads of a token
+    const int threads = wide > kMinThreads ? wide : kMinThreads;
+    const unsigned at_once = threads / wide;
     const unsigned blocks = ((unsigned)p.T + at_once - 1) / at_once;
-    return launch_pdl(token_write_kernel<D, Q8, EXTEND>, dim3(blocks), dim3(kThreads), 0, stream,
-                      p);
+    return launch_pdl(token_write_kernel<D, Q8, EXTEND>, dim3(blocks), dim3(threads), 0, stream, p);
 }
 
 template <int D>

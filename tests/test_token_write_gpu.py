@@ -105,6 +105,42 @@ def test_extend(q8, Hq, Hkv, D, ps, packed):
     _untouched(c, [(b, L - n, L) for b, (L, n) in enumerate(zip(lens, chunks)) if n])
 
 
+def _sparse(B, every, n=1):
+    return [n if b % every == every - 1 else 0 for b in range(B)]
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (2, 1)])
+@pytest.mark.parametrize("chunks", [[1] * 40, [2, 1] * 33, _sparse(1500, 50), _sparse(1100, 1099, 5),
+                                    [0] * 33 + [3] + [0] * 31 + [1], [1] + [0] * 70 + [1] + [0] * 900 + [2],
+                                    [3] + [0] * 1024, _sparse(64, 33, 2)],
+                         ids=["ones", "pairs", "sparse", "far", "late", "gaps", "first", "two"])
+def test_extend_finds_rows_between_empty_ones(chunks, Hq, Hkv):
+    """One-token chunks, and rows without new tokens before, between and behind the
+    others: a warp's tokens belong to rows that lie far apart."""
+    lens = [n + (3 * b) % 7 if n else b % 3 for b, n in enumerate(chunks)]
+    c = Cache(lens, Hq, Hkv, 64, 4, seed=len(chunks))
+    ends = torch.tensor([0] + list(chunks)).cumsum(0)
+    T = int(ends[-1])
+    q, k, v, qw, kw = _inputs(c, T, False, (True, True))
+    table = rope_table(32, 64)
+    q_out = torch.full((T, Hq, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    qo = ends.to(torch.int32).to(DEV)
+    t = pkv.tokens(q, k, v, q_out, qw, kw, rope_cos_sin=table, rope_max_pos=32)
+    pkv.paged_kv_extend_q8(c.d, t, qo, *c.q8, *c.rows, status=c.status)
+    assert int(c.status.item()) == 0
+    live = [(b, L - n, L) for b, (L, n) in enumerate(zip(lens, chunks)) if n]
+    for b, first, last in live:
+        _check(c, True, q, k, v, qw, kw, table, q_out, b, int(ends[b]), first, last)
+    _untouched(c, live)
+    # with two tokens more than the rows take: those are refused and write nothing
+    more = [torch.cat([x, x[:1], x[:1]]) for x in (q, k, v)]
+    out2 = torch.full((T + 2, Hq, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    pkv.paged_kv_extend_q8(c.d, pkv.tokens(*more, out2, qw, kw, rope_cos_sin=table, rope_max_pos=32), qo,
+                           *c.q8, *c.rows, status=c.status)
+    assert int(c.status.item()) == pkv.FLAG_BAD_LEN
+    assert torch.equal(out2[:T], q_out) and bool(torch.isnan(out2[T:].float()).all())
+
+
 def test_plain_matches_append_bit_for_bit():
     """Without norms the bf16 write is paged_kv_append's, bit for bit."""
     c = Cache([9, 100, 1], 8, 2, 128, 16, seed=3)
