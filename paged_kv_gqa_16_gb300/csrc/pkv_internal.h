@@ -128,7 +128,7 @@ struct ReadQ8Params {
     uint32_t *status;              // nullable
     int B, Hkv, page_size, num_pages, num_indices, max_seq_len;
     int ps_shift;                  // log2 of page_size, or -1
-    int per_block;                 // token slots a block takes (set by the launcher)
+    int per_warp;                  // token slots a warp takes at a time (set by the launcher)
 };
 
 struct DecodeParams {

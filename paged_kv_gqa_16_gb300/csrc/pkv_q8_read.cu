@@ -3,14 +3,16 @@
 // bf16(code * 2^e) is exact: a code has four significant bits, a bf16 eight.
 // Token t of row b moves from pool page kv_indices[kv_indptr[b] + t / ps] to
 // output page kv_indptr[b] + t / ps, so the output, taken as one list of token
-// slots (entry * ps + slot), has the table's order.  A block takes a few
-// consecutive slots of that list: a thread a slot finds the entry's row, its
-// length and the page, then all threads stream the slots' heads, 16 codes of K
-// and the 16 of V beside them at a time.  3 bytes of traffic a value and
-// nothing else to do: bound by memory.  32 ragged rows, 73,728 tokens of 8 heads
-// of 128, 454 MB: 75.0 us, 6,060 GB/s, 89% of the copy bandwidth (86.4 us with
-// two 16-byte stores in place of each 32-byte one, 92 with four vectors of one
-// pool a thread, 105 with 8-byte loads).
+// slots (entry * ps + slot), has the table's order.  A warp takes a few consecutive
+// slots of that list: a lane a slot finds the entry's row, its length and the page,
+// then all lanes stream the slots' heads, 16 codes of K and the 16 of V beside them
+// at a time.  3 bytes of traffic a value and nothing else to do: bound by memory.
+// 32 ragged rows, 73,728 tokens of 8 heads of 128, 454 MB: 73.4 us, 6,190 GB/s, 91% of
+// the copy bandwidth (86.4 us with two 16-byte stores in place of each 32-byte one, 92
+// with four vectors of one pool a thread, 105 with 8-byte loads).  Blocks of 256
+// threads that look up their slots together take 74.6; 9.9 in place of 8.4 for 6,152
+// tokens, 7.0 in place of 4.9 for those of D = 64, 3.0 in place of 2.2 for 137, 4.8 in
+// place of 5.5 for 48,000 of one head of 64 at page size 1.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_q8.cuh"
@@ -19,9 +21,14 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxSlots = 64;            // token slots a block takes at most
-constexpr int kBlockValues = 16384;      // values of K (and of V) a block aims at
+// 12 blocks an SM, at most 42 registers: 76.6 us with the 48 that the compiler takes
+// by itself, 80.0 with 36; 64 threads: 75.7.
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+// Values of K (and of V) a warp takes at most (1024: 77.8 us, 4096: 78.7), and the
+// warps that a small call is spread over (half and twice as many: within 1%).
+constexpr int kWarpValues = 2048;
+constexpr int kShare = 4864;
 
 // Eight codes times f as eight bf16.
 __device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi, float f)
@@ -83,10 +90,9 @@ __device__ __forceinline__ long long source_of(const ReadQ8Params &p, long long 
 }
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads) read_q8_kernel(const ReadQ8Params p)
+__global__ void __launch_bounds__(kThreads, 12) read_q8_kernel(const ReadQ8Params p)
 {
     constexpr int VPH = D / 16;          // 16-code vectors of a head
-    __shared__ long long s_src[kMaxSlots];
     grid_dependency_wait();
     // the rows' own checks, each reported once
     for (long long b = blockIdx.x * (long long)kThreads + threadIdx.x; b < p.B;
@@ -103,17 +109,17 @@ __global__ void __launch_bounds__(kThreads) read_q8_kernel(const ReadQ8Params p)
     }
     const long long slots = (long long)p.num_indices * p.page_size;
     const int per_tok = p.Hkv * VPH;     // vectors of a token, of K or of V
-    for (long long s0 = (long long)blockIdx.x * p.per_block; s0 < slots;
-         s0 += (long long)gridDim.x * p.per_block) {
-        const int n = (int)(slots - s0 < p.per_block ? slots - s0 : p.per_block);
-        if (threadIdx.x < n)
-            s_src[threadIdx.x] = source_of(p, s0 + threadIdx.x);
-        __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const long long warp = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    for (long long s0 = warp * p.per_warp; s0 < slots;
+         s0 += (long long)gridDim.x * kWarps * p.per_warp) {
+        const int n = (int)(slots - s0 < p.per_warp ? slots - s0 : p.per_warp);
+        const long long mine = lane < n ? source_of(p, s0 + lane) : -1;
         const int vecs = n * per_tok;
-        for (int i = threadIdx.x; i < vecs; i += kThreads) {
-            const int tok = i / per_tok, k = i - tok * per_tok;
-            const long long src = s_src[tok];
-            if (src < 0)
+        for (int i0 = 0; i0 < vecs; i0 += 32) {
+            const int i = i0 + lane, tok = min(i / per_tok, n - 1), k = i - tok * per_tok;
+            const long long src = __shfl_sync(0xffffffffu, mine, tok);
+            if (src < 0 || i >= vecs)
                 continue;
             const size_t head = (size_t)src * p.Hkv + k / VPH;
             const size_t from = head * D + (k % VPH) * 16;
@@ -124,7 +130,6 @@ __global__ void __launch_bounds__(kThreads) read_q8_kernel(const ReadQ8Params p)
             store16<WIDE>(p.k_out + to, kc, fk);
             store16<WIDE>(p.v_out + to, vc, fv);
         }
-        __syncthreads();
     }
     grid_launch_dependents();
 }
@@ -137,9 +142,13 @@ cudaError_t launch_read_q8(const ReadQ8Params &params, int D, cudaStream_t strea
     const long long slots = (long long)p.num_indices * p.page_size;
     if (slots <= 0)
         return cudaSuccess;
-    const int per = kBlockValues / (p.Hkv * D > kBlockValues ? kBlockValues : p.Hkv * D);
-    p.per_block = per < kMaxSlots ? per : kMaxSlots;
-    const long long blocks = (slots + p.per_block - 1) / p.per_block;
+    const int most = p.Hkv * D > kWarpValues ? 1 : kWarpValues / (p.Hkv * D);   // up to 32
+    // a slot's share, in whole rounds of 32 lanes (one head of 64: 6.0 us without)
+    const int per_tok = p.Hkv * (D / 16), round = per_tok < 32 ? 32 / per_tok : 1;
+    const long long share = slots / kShare / round * round;
+    p.per_warp = share >= most ? most : share > round ? (int)share : round;
+    const long long per_block = (long long)p.per_warp * kWarps;
+    const long long blocks = (slots + per_block - 1) / per_block;
     const dim3 grid((unsigned)(blocks < (1ll << 30) ? blocks : (1ll << 30)));
     const bool wide = ((reinterpret_cast<uintptr_t>(p.k_out) |
                         reinterpret_cast<uintptr_t>(p.v_out)) & 31) == 0;
