@@ -36,6 +36,12 @@ def test_read(Hkv, D, ps, lens):
     assert bool(torch.isnan(k[left]).all()) and bool(torch.isnan(v[left]).all())
 
 
+@pytest.mark.parametrize("Hkv,D,ps", [(1, 64, 1), (3, 64, 7), (1, 128, 16), (2, 64, 5)])
+def test_read_of_many_slots(Hkv, D, ps):
+    """Enough slots that a warp takes several, with odd shares and rows that end inside one."""
+    test_read(Hkv, D, ps, [9001, 0, 1, 13, 40007, 3, 0, 5 * 4864 + 2])
+
+
 def test_read_flags():
     c = Cache([9, 30, 5], 2, 2, 64, 4, seed=1, max_seq_len=20).fill()
     k, v = (torch.zeros(c.n_ref, 4, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
