@@ -168,7 +168,8 @@ def _current_raw_stream():
         # torch's own shortcut past the Stream object (3 us a call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
-        device = torch.cuda.current_device
+        torch.cuda.current_device()               # initialises CUDA, which the shortcut does not
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _current_stream = lambda: raw(device())  # noqa: E731
     return _current_stream()
 
@@ -384,9 +385,9 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
            rope_cos_sin=None, rope_max_pos: int = 0) -> Tokens:
     """The new tokens of a paged_kv_append_norm / _extend_norm / _append_q8 /
     _extend_q8 call: q [T, Hq, D] (or None), k and v [T, Hkv, D] bf16 whose rows
-    do not overlap (slices of one projection's output; no expanded rows), q_out [T, Hq, D] for the
-    processed queries (None: in place, which needs a packed q), optional [D]
-    norm weights, and the RoPE table."""
+    do not overlap (slices of one projection's output; no expanded rows), q_out
+    [T, Hq, D] for the processed queries (None: in place, which needs a packed q),
+    optional [D] norm weights, and the RoPE table."""
     T, Hkv, D = shape = k.shape
     if shape != v.shape:
         raise ValueError("k and v must have the same shape")
@@ -395,33 +396,40 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
     # a head's elements next to each other, a row's heads too; two bytes each
     ok = k_one == v_one == 1 and (k_head == v_head == D or Hkv == 1) and (
         k.element_size() == v.element_size() == 2)
-    Hq = qp = out = qn = None
-    q_row = 0
+    Hq = qp = out = qn = kn = cs = None
+    q_row = 1
     if q is not None:
         qT, Hq, qD = q.shape
         if qT != T or qD != D:
             raise ValueError("q and k must have the same tokens and head size")
         q_row, q_head, q_one = q.stride()
         ok = ok and q_one == 1 and (q_head == D or Hq == 1) and q.element_size() == 2
-        qp = q.data_ptr()
-        out = qp if q_out is None else _ptr(q_out)
-        qn = _ptr(q_norm)
-        ok = ok and (q_row > 0 or T <= 1)
-        if q_out is not None and q_out.numel() * q_out.element_size() < T * Hq * D * 2:
-            raise ValueError("q_out must hold bf16 [tokens, heads, D]")
-        if q_norm is not None and (q_norm.numel() != D or q_norm.element_size() != 2):
-            raise ValueError("q_norm must be bf16 [D]")
-    if k_norm is not None and (k_norm.numel() != D or k_norm.element_size() != 2):
-        raise ValueError("k_norm must be bf16 [D]")
+        qp = out = q.data_ptr()
+        if q_out is not None:
+            if q_out.numel() < T * Hq * D or q_out.element_size() != 2 or not q_out.is_contiguous():
+                raise ValueError("q_out must be contiguous bf16 [tokens, heads, D]")
+            out = q_out.data_ptr()
+        if q_norm is not None:
+            if q_norm.numel() != D or q_norm.element_size() != 2 or not q_norm.is_contiguous():
+                raise ValueError("q_norm must be contiguous bf16 [D]")
+            qn = q_norm.data_ptr()
+    if k_norm is not None:
+        if k_norm.numel() != D or k_norm.element_size() != 2 or not k_norm.is_contiguous():
+            raise ValueError("k_norm must be contiguous bf16 [D]")
+        kn = k_norm.data_ptr()
+    if rope_cos_sin is not None:
+        if rope_cos_sin.numel() < rope_max_pos * D or not rope_cos_sin.is_contiguous():
+            raise ValueError("rope_cos_sin must be contiguous fp32 [rope_max_pos, D / 2, 2]")
+        cs = rope_cos_sin.data_ptr()
     if T <= 1:
         q_row = k_row = v_row = 0                 # a single row is packed
-    elif not (k_row > 0 and v_row > 0):
+    elif not (q_row and k_row and v_row):
         ok = False                                # (0 would be taken for packed)
     if not ok:
         raise ValueError("q, k and v must be bf16 [tokens, heads, D] with packed heads and "
                          "rows of their own")
-    t = Tokens(qp, k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, out,
-               qn, _ptr(k_norm), norm_eps, _ptr(rope_cos_sin), rope_max_pos)
+    t = Tokens(qp, k.data_ptr(), v.data_ptr(), q_row, k_row, v_row, out, qn, kn, norm_eps, cs,
+               rope_max_pos)
     t.shape = (T, Hq, Hkv, D)
     t.tensors = (q, k, v, q_out, q_norm, k_norm, rope_cos_sin)
     return t

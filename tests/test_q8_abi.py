@@ -172,3 +172,10 @@ def test_tokens_refuse_expanded_rows_and_short_tensors():
         with pytest.raises(ValueError):
             pkv.tokens(q, k, k, torch.empty_like(q), **kw)
     assert pkv.tokens(q, k, k, torch.empty_like(q), w, w).k_norm == w.data_ptr()
+    rope = torch.zeros(5, 32, 2)
+    assert pkv.tokens(q, k, k, rope_cos_sin=rope, rope_max_pos=5).rope_cos_sin == rope.data_ptr()
+    for bad in (dict(rope_cos_sin=rope, rope_max_pos=6), dict(rope_cos_sin=rope[..., :1], rope_max_pos=1),
+                dict(k_norm=torch.zeros(128, dtype=torch.bfloat16)[::2]),
+                dict(q_out=torch.zeros(3, 4, 128, dtype=torch.bfloat16)[..., ::2])):
+        with pytest.raises(ValueError):
+            pkv.tokens(q, k, k, **bad)
