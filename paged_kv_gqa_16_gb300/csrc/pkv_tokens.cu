@@ -360,7 +360,11 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
     // K and V heads
     if (EXTEND && p.k_norm != nullptr)
         wk = *(reinterpret_cast<const uint4 *>(p.k_norm) + lane);
-    const Turn turn = turn_of(c01, c23, unpack(wk));
+    // (codes: a key's products with the weight are formed by themselves, exactly, 16
+    // bits of 24: of 4.9 M codes 4.6 lie across a tie from the 64-bit ones, 5.3 with
+    // the weight in the coefficients, 7.7 in plain 32-bit operations, at the same time)
+    const Eight wk8 = unpack(wk);
+    const Turn turn = turn_of(c01, c23, Q8 ? unpack(ones) : wk8);
     for (int h0 = 0; h0 < p.Hkv; h0 += kKv * width) {
 #pragma unroll
         for (int u = 0; u < kKv; ++u) {
@@ -370,6 +374,13 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
             load(rk[u], k, h + kKv * width, p.Hkv);
             load(rv[u], v, h + kKv * width, p.Hkv);
             const float f = p.k_norm != nullptr ? norm_factor<D>(x, p.norm_eps) : 1.f;
+            if constexpr (Q8) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    x.a[i] = mul2(x.a[i], wk8.a[i]);
+                    x.b[i] = mul2(x.b[i], wk8.b[i]);
+                }
+            }
             apply(x, turn, p.rope != nullptr);
             const bool store = live && h < p.Hkv;
             const size_t head = (size_t)slot * p.Hkv + h;
