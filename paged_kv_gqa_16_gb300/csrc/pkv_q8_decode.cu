@@ -24,13 +24,17 @@
 //    the tensor pipe's time -- this GPU makes them out of f16 products.)
 //  - Both scales act on the scores: x_t = 2^ek_t (s_t c) and y_t = x_t + ev_t
 //    in the log2 domain.  The weights used for O are 2^(y_t - base), base
-//    following the largest y_t, so they are in f16's range however the
-//    values' scales differ; the sum of softmax weights takes each of them, in
-//    fp32, times 2^-ev_t (a power of two, exact).  Both sums carry 2^-base.
-//    A weight is rounded to f16 (11 significant bits) for the product.
-//  - base is raised only when some y_t exceeds it by more than 8: a weight is
-//    then at most 2^8 and the usual tile needs no maximum over its lanes and
-//    no rescaling.
+//    following the largest y_t; the sum of softmax weights takes each of them,
+//    in fp32, times 2^-ev_t (a power of two, exact).  Both sums carry 2^-base.
+//    A weight is rounded to f16 for the product: to 11 significant bits, or,
+//    under f16's normal range, to steps of 2^-24.  base is therefore kept 7
+//    under the largest y_t, which leaves those steps at 2^-31 of the largest
+//    weight: a long tail of small weights still adds up.  A token 2^32 below
+//    the largest is lost from O, which shows where all larger ones have zero
+//    codes in a channel.
+//  - base is raised only when some y_t exceeds it by more than 15: a weight is
+//    then at most 2^15 (f16 ends at 2^16) and the usual tile needs no maximum
+//    over its lanes and no rescaling.
 //  - Short rows (kQ8WholeBytes) are not split: a block takes whole rows and
 //    writes their outputs, and there is no combine.
 //  - A kv head has WPH = 8 / HPC warps, which take 16 tokens each of every
@@ -63,7 +67,8 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 8;                 // consumer warps
-constexpr float kRaise = 8.f;             // how far a score may exceed its base
+constexpr float kRaise = 15.f;            // how far a score may exceed its base
+constexpr float kUnder = 7.f;             // a raised base's distance to the largest score
 
 template <int D, int HPC, int NT>
 struct Q8Cfg {
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                            const float mn = fmaxf(m_run[nt][e], mx);
+                            const float mn = fmaxf(m_run[nt][e], mx - kUnder);
                             const float a = mn == -INFINITY ? 1.f : exp2_ftz(m_run[nt][e] - mn);
                             m_run[nt][e] = mn;
                             l_run[nt][e] *= a;
