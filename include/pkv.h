@@ -571,7 +571,8 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
  * holding others is undefined.  A token's weight, with its value's scale, is
  * rounded to 11 significant bits or to 2^-32 of the row's largest, whichever is
  * more: values 2^32 under the row's largest count in the softmax's sum, but no
- * longer in a channel where all larger ones have zero codes.  A NaN code reaches the outputs that read it, an
+ * longer in a channel where all larger ones have zero codes.  A query element
+ * under 2^-32 of its head's largest is off by up to 2^-40 of that.  A NaN code reaches the outputs that read it, an
  * infinite query element its head's.  Rows short by max_seq_len (at most 256 KB
  * of K and V in a group of kv heads, 512 KB with rows x groups for half the
  * SMs) are not split whatever num_splits is: one kernel.  Otherwise one

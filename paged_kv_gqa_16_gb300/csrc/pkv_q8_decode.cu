@@ -17,11 +17,12 @@
 //    half -- half the products and half the accumulators of heads as rows.
 //    NT = 2 column tiles serve groups of 9 to 16 heads.
 //  - Codes become f16 exactly (one cvt for two codes).  q is scaled by a
-//    power of two to at most 2 in size, which keeps its eight significant
-//    bits in f16; that power and the softmax scale go into the score's
-//    factor in fp32.  (e4m3 x e4m3 products, with q and the weights as two
-//    codes each, were slower: 62.8 us for the serving batch below, at twice
-//    the tensor pipe's time -- this GPU makes them out of f16 products.)
+//    power of two to the top of f16's range, which keeps the eight significant
+//    bits of every element down to 2^-32 of its head's largest (smaller ones
+//    are off by 2^-40 of the largest); that power and the softmax scale go into
+//    the score's factor in fp32.  (e4m3 x e4m3 products, with q and the weights
+//    as two codes each, were slower: 62.8 us for the serving batch below, at
+//    twice the tensor pipe's time -- this GPU makes them out of f16 products.)
 //  - Both scales act on the scores: x_t = 2^ek_t (s_t c) and y_t = x_t + ev_t
 //    in the log2 domain.  The weights used for O are 2^(y_t - base), base
 //    following the largest y_t; the sum of softmax weights takes each of them,
@@ -472,15 +473,16 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
                                          fmaxf(fabsf(bf16_lo(raw[j].y)), fabsf(bf16_hi(raw[j].y)))));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-            // 2^-n, n the exponent of amax, both powers kept in the normal range
-            const int n = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
-            const float down = __uint_as_float((unsigned)(127 - n) << 23);
+            // 2^(15 - n), n the exponent of amax, both powers kept in the normal range
+            // (the largest, 2^16 less a bf16 step, is within f16; infinity stays)
+            const int n = min(max((int)(__float_as_uint(amax) >> 23) - 127, -111), 127);
+            const float down = __uint_as_float((unsigned)(127 + 15 - n) << 23);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 qf[nt][j][0] = pack_f16x2(bf16_lo(raw[j].x) * down, bf16_hi(raw[j].x) * down);
                 qf[nt][j][1] = pack_f16x2(bf16_lo(raw[j].y) * down, bf16_hi(raw[j].y) * down);
             }
-            const float up = __uint_as_float((unsigned)(127 + n) << 23) * p.scale_log2;
+            const float up = __uint_as_float((unsigned)(127 - 15 + n) << 23) * p.scale_log2;
             cq[nt][0] = __shfl_sync(kFull, up, (2 * c) * 4);
             cq[nt][1] = __shfl_sync(kFull, up, (2 * c + 1) * 4);
         }

@@ -87,3 +87,32 @@ def test_loud_tokens_with_zeros_beside_quiet_ones(Hq, Hkv, D, loud):
     q = (c.randn(3, Hq, D) * 0.5).to(torch.bfloat16).to(DEV)
     _check(c, q, 1)
     _check(c, q)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+@pytest.mark.parametrize("loud", [10, 18, 22, 31])
+def test_one_large_query_element_over_zero_keys(Hq, Hkv, D, loud):
+    """A query element 2^loud times the others meets zero codes: the scores are what
+    the others make of them, exactly (an element keeps its bits down to 2^-32 of its
+    head's largest)."""
+    c = Cache([300, 17, 2000], Hq, Hkv, D, 16, seed=3).fill()
+    c.kc[..., 5] = 0
+    q = c.randn(3, Hq, D) * 2
+    q[..., 5] = 3.0 * 2.0 ** loud
+    q = q.to(torch.bfloat16)
+    # an element nearer zero than 2^-32 of the largest is off by 2^-40 of it at most: none here
+    q[q.abs() < 3.0 * 2.0 ** (loud - 32)] = 0
+    _check(c, q.to(DEV), 1)
+    _check(c, q.to(DEV))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [-133, -126, -112, -111, -110, 14, 15, 16, 126, 127])
+def test_queries_at_both_ends_of_the_type(D, power):
+    """Heads whose largest element is the type's smallest or lies near its largest,
+    over keys that are zero or as small as keys get."""
+    c = Cache([77, 5], 8, 2, D, 16, seed=4).fill()
+    if power > 15:
+        c.kc[c.kc != 0x7F] = 0
+    q = torch.randint(-1, 2, (2, 8, D), generator=c.g).double() * 2.0 ** power
+    _check(c, q.to(torch.bfloat16).to(DEV))
