@@ -140,8 +140,6 @@ cudaError_t launch_read_q8(const ReadQ8Params &params, int D, cudaStream_t strea
 {
     ReadQ8Params p = params;
     const long long slots = (long long)p.num_indices * p.page_size;
-    if (slots <= 0)
-        return cudaSuccess;
     const int most = p.Hkv * D > kWarpValues ? 1 : kWarpValues / (p.Hkv * D);   // up to 32
     // a slot's share, in whole rounds of 32 lanes (one head of 64: 6.0 us without)
     const int per_tok = p.Hkv * (D / 16), round = per_tok < 32 ? 32 / per_tok : 1;
@@ -149,7 +147,8 @@ cudaError_t launch_read_q8(const ReadQ8Params &params, int D, cudaStream_t strea
     p.per_warp = share >= most ? most : share > round ? (int)share : round;
     const long long per_block = (long long)p.per_warp * kWarps;
     const long long blocks = (slots + per_block - 1) / per_block;
-    const dim3 grid((unsigned)(blocks < (1ll << 30) ? blocks : (1ll << 30)));
+    // (an empty table: one block, for the rows' checks)
+    const dim3 grid((unsigned)(blocks < 1 ? 1 : blocks < (1ll << 30) ? blocks : (1ll << 30)));
     const bool wide = ((reinterpret_cast<uintptr_t>(p.k_out) |
                         reinterpret_cast<uintptr_t>(p.v_out)) & 31) == 0;
     auto run = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, p); };
