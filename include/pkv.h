@@ -557,8 +557,10 @@ pkv_status paged_kv_extend_q8(const pkv_dims *dims, const pkv_tokens *tokens,
  * row, and those past a row's length, keep what they held.  A row with a
  * negative length or one above max_seq_len (PKV_FLAG_BAD_LEN) is not read; a
  * malformed or short table and a page id outside the pool
- * (PKV_FLAG_BAD_PAGE) leave the tokens without a page as they were.  One
- * launch; graph-capturable. */
+ * (PKV_FLAG_BAD_PAGE) leave the tokens without a page as they were.  kv_indptr
+ * must not decrease, at idle rows neither: where it does (PKV_FLAG_BAD_PAGE),
+ * other rows' tokens may be left as they were too.  One launch;
+ * graph-capturable. */
 pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const void *v_codes,
                             const void *k_scale, const void *v_scale,
                             const int32_t *kv_indices, const int32_t *kv_indptr,

@@ -101,8 +101,9 @@ __global__ void __launch_bounds__(kThreads, 12) read_q8_kernel(const ReadQ8Param
         unsigned bad = 0;
         if (L < 0 || L > p.max_seq_len)
             bad |= kFlagBadLen;
-        else if (L > 0 && (pg0 < 0 || pg1 < pg0 || pg1 > p.num_indices ||
-                           (long long)(pg1 - pg0) * p.page_size < L))
+        // (an idle row's offsets too: the search for a slot's row goes by them)
+        if (pg0 < 0 || pg1 < pg0 || pg1 > p.num_indices ||
+            ((bad & kFlagBadLen) == 0 && (long long)(pg1 - pg0) * p.page_size < L))
             bad |= kFlagBadPage;
         if (bad && p.status != nullptr)
             atomicOr(p.status, bad);

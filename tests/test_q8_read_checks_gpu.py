@@ -23,3 +23,25 @@ def test_rows_are_checked_where_the_table_is_empty(lens, want):
                          status=status)
     assert int(status.item()) == want
     assert bool((k == -1).all()) and bool((v == -1).all())
+
+
+def test_a_table_that_decreases_is_flagged_by_idle_rows_too():
+    """Offsets that decrease hide other rows' entries from the search for a slot's row,
+    so the row that makes them decrease is reported even if it has no tokens."""
+    c = Cache([12, 0, 0, 9], 2, 2, 64, 4, seed=1).fill()
+    k, v = (torch.zeros(c.n_ref, 4, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    indptr = c.kv_indptr.clone()
+
+    def read():
+        c.status.zero_()
+        pkv.paged_kv_read_q8(c.d, *c.q8, c.kv_indices, indptr, c.seq_lens, k, v, status=c.status)
+        return int(c.status.item())
+
+    assert read() == 0
+    for bad in (1000, -3):
+        indptr[2] = bad                                            # ends row 1, starts row 2: both idle
+        assert read() == pkv.FLAG_BAD_PAGE, bad
+    indptr[2] = c.kv_indptr[2]
+    indptr[4] = c.n_ref + 1                                        # the last row's end is past the table
+    c.seq_lens[3] = 0
+    assert read() == pkv.FLAG_BAD_PAGE
