@@ -553,8 +553,9 @@ pkv_status paged_kv_extend_q8(const pkv_dims *dims, const pkv_tokens *tokens,
  * page kv_indptr[b] + t / page_size, slot t % page_size of them -- the page
  * that entry of kv_indices names, moved to the entry's own place.  With
  * kv_indices = 0, 1, 2, ... they are pools for paged_prefill_attn and the
- * other bf16 calls.  Codes times their scale are exact in bf16.  Slots of no
- * row, and those past a row's length, keep what they held.  A row with a
+ * other bf16 calls.  Codes times their scale are exact in bf16 for scales from
+ * 2^-124 to 2^119, elsewhere the nearest bf16; scale byte 255 gives NaN.  Slots
+ * of no row, and those past a row's length, keep what they held.  A row with a
  * negative length or one above max_seq_len (PKV_FLAG_BAD_LEN) is not read; a
  * malformed or short table and a page id outside the pool
  * (PKV_FLAG_BAD_PAGE) leave the tokens without a page as they were.  kv_indptr

@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2_hi(uint32_t w)
     return r;
 }
 
-// 2^(byte - 127) as fp32.
+// 2^(byte - 127) as fp32, for bytes 1 to 254.
 __device__ __forceinline__ float q8_scale(unsigned byte)
 {
     return __uint_as_float(byte << 23);

@@ -1,6 +1,8 @@
 // pkv_q8_read.cu -- the rows of an 8-bit cache read back as bf16.
 //
 // bf16(code * 2^e) is exact: a code has four significant bits, a bf16 eight.
+// (Scales under 2^-124 and over 2^119, which the writes do not choose, leave bf16's
+// range: the result is then the nearest bf16, past its largest value infinity.)
 // Token t of row b moves from pool page kv_indices[kv_indptr[b] + t / ps] to
 // output page kv_indptr[b] + t / ps, so the output, taken as one list of token
 // slots (entry * ps + slot), has the table's order.  A warp takes a few consecutive
@@ -59,6 +61,12 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *dst, uint4 c, float f)
         reinterpret_cast<uint4 *>(dst)[0] = a;
         reinterpret_cast<uint4 *>(dst)[1] = b;
     }
+}
+
+// The scale of any e8m0 byte: 0 stands for 2^-127, 255 for NaN.
+__device__ __forceinline__ float any_scale(unsigned byte)
+{
+    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
 }
 
 // Pool slot of output slot `at`, or -1 if no token of a row is there.
@@ -127,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 12) read_q8_kernel(const ReadQ8Param
             const size_t to = ((size_t)(s0 + tok) * per_tok + k) * 16;
             const uint4 kc = __ldcs(reinterpret_cast<const uint4 *>(p.k_codes + from));
             const uint4 vc = __ldcs(reinterpret_cast<const uint4 *>(p.v_codes + from));
-            const float fk = q8_scale(p.k_scale[head]), fv = q8_scale(p.v_scale[head]);
+            const float fk = any_scale(p.k_scale[head]), fv = any_scale(p.v_scale[head]);
             store16<WIDE>(p.k_out + to, kc, fk);
             store16<WIDE>(p.v_out + to, vc, fv);
         }
