@@ -73,20 +73,22 @@ int log2_exact(int x)
     return s;
 }
 
-// Workspace: [header 256 B | row info, persistent path: Bv x 2 int32 | the same
-//             of the 8-bit cache's decode (whose partition differs, and which
-//             must leave the row info of a bf16 plan as it is, and the other way
-//             round) |
+// Workspace: [header 256 B | row info, persistent path: Bv x 2 int32 |
 //             the per-step plan, persistent path | rotated-q scratch
 //             [B, Hq, D] bf16 | one-page-per-row table of
 //             the contiguous-cache call, (2B + 1) int32 | partials].
+// The 8-bit cache's decode has row info of its own: its partition differs, and
+// it must leave the row info of a bf16 plan as it is, and the other way round.
+// It is in the rotated-q scratch, which is at least as large (8 bytes a virtual
+// row against 128 and more a query head) and which only shapes off the
+// persistent path use, whose 8-bit calls have no plan.
 // The partial region holds either layout: the per-split one [B,Hq,S,(2|D)]
 // of paged_decode_partials, or the piece one [(S+Bv)*HQV, (2|D)] of the
 // persistent path.  Every region starts on a 256-byte boundary.
 struct Layout {
     int hpc, Bv, HQV;
-    size_t rowinfo_off, rowinfo_q8_off, plan_off, qscratch_off, table_off, split_ml_off, split_o_off,
-        piece_ml_off, piece_o_off, total;
+    size_t rowinfo_off, plan_off, qscratch_off, rowinfo_q8_off, table_off, split_ml_off,
+        split_o_off, piece_ml_off, piece_o_off, total;
 };
 
 Layout layout_for(const pkv_dims *d, int num_splits)
@@ -96,12 +98,12 @@ Layout layout_for(const pkv_dims *d, int num_splits)
     L.Bv = d->B * (d->Hkv / L.hpc);
     L.HQV = L.hpc * (d->Hq / d->Hkv);
     L.rowinfo_off = kHeaderBytes;
-    L.rowinfo_q8_off = L.rowinfo_off + round_up((size_t)L.Bv * 2 * sizeof(int32_t), 256);
-    L.plan_off = L.rowinfo_q8_off + round_up((size_t)L.Bv * 2 * sizeof(int32_t), 256);
+    L.plan_off = L.rowinfo_off + round_up((size_t)L.Bv * 2 * sizeof(int32_t), 256);
     // the per-step plan, for shapes the persistent path serves
     const size_t plan = L.Bv <= pkv::kFusedMaxRows
                             ? pkv::plan_words(L.Bv, num_splits) * sizeof(int32_t) : 0;
     L.qscratch_off = L.plan_off + round_up(plan, 256);
+    L.rowinfo_q8_off = L.qscratch_off;
     L.table_off = L.qscratch_off + round_up((size_t)d->B * d->Hq * d->D * 2, 256);
     const size_t part = L.table_off + round_up(((size_t)2 * d->B + 1) * sizeof(int32_t), 256);
     const size_t rows = (size_t)d->B * d->Hq * num_splits;
