@@ -158,6 +158,18 @@ def _ptr(x) -> Optional[int]:
     raise ValueError("tensors passed to libpkv must be contiguous")
 
 
+_types = None
+
+
+def _torch_types():
+    """(bf16, fp32)"""
+    global _types
+    if _types is None:
+        import torch
+        _types = torch.bfloat16, torch.float32
+    return _types
+
+
 _current_stream = None
 
 
@@ -388,14 +400,15 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
     do not overlap (slices of one projection's output; no expanded rows), q_out
     [T, Hq, D] for the processed queries (None: in place, which needs a packed q),
     optional [D] norm weights, and the RoPE table."""
+    bf16, fp32 = _types or _torch_types()
     T, Hkv, D = shape = k.shape
     if shape != v.shape:
         raise ValueError("k and v must have the same shape")
     k_row, k_head, k_one = k.stride()
     v_row, v_head, v_one = v.stride()
-    # a head's elements next to each other, a row's heads too; two bytes each
+    # a head's elements next to each other, a row's heads too
     ok = k_one == v_one == 1 and (k_head == v_head == D or Hkv == 1) and (
-        k.element_size() == v.element_size() == 2)
+        k.dtype is bf16 and v.dtype is bf16)
     Hq = qp = out = qn = kn = cs = None
     q_row = 1
     if q is not None:
@@ -403,22 +416,23 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
         if qT != T or qD != D:
             raise ValueError("q and k must have the same tokens and head size")
         q_row, q_head, q_one = q.stride()
-        ok = ok and q_one == 1 and (q_head == D or Hq == 1) and q.element_size() == 2
+        ok = ok and q_one == 1 and (q_head == D or Hq == 1) and q.dtype is bf16
         qp = out = q.data_ptr()
         if q_out is not None:
-            if q_out.numel() < T * Hq * D or q_out.element_size() != 2 or not q_out.is_contiguous():
+            if q_out.numel() < T * Hq * D or q_out.dtype is not bf16 or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous bf16 [tokens, heads, D]")
             out = q_out.data_ptr()
         if q_norm is not None:
-            if q_norm.numel() != D or q_norm.element_size() != 2 or not q_norm.is_contiguous():
+            if q_norm.numel() != D or q_norm.dtype is not bf16 or not q_norm.is_contiguous():
                 raise ValueError("q_norm must be contiguous bf16 [D]")
             qn = q_norm.data_ptr()
     if k_norm is not None:
-        if k_norm.numel() != D or k_norm.element_size() != 2 or not k_norm.is_contiguous():
+        if k_norm.numel() != D or k_norm.dtype is not bf16 or not k_norm.is_contiguous():
             raise ValueError("k_norm must be contiguous bf16 [D]")
         kn = k_norm.data_ptr()
     if rope_cos_sin is not None:
-        if rope_cos_sin.numel() < rope_max_pos * D or not rope_cos_sin.is_contiguous():
+        if (rope_cos_sin.numel() < rope_max_pos * D or rope_cos_sin.dtype is not fp32 or
+                not rope_cos_sin.is_contiguous()):
             raise ValueError("rope_cos_sin must be contiguous fp32 [rope_max_pos, D / 2, 2]")
         cs = rope_cos_sin.data_ptr()
     if T <= 1:
