@@ -162,12 +162,37 @@ _types = None
 
 
 def _torch_types():
-    """(bf16, fp32)"""
+    """(bf16, fp32, those of e4m3 codes, those of e8m0 scales)"""
     global _types
     if _types is None:
         import torch
-        _types = torch.bfloat16, torch.float32
+        _types = (torch.bfloat16, torch.float32, (torch.float8_e4m3fn, torch.uint8, torch.int8),
+                  (torch.float8_e8m0fnu, torch.uint8, torch.int8))
     return _types
+
+
+def _bf16_ptr(x) -> Optional[int]:
+    if x is None or x.__class__ is int:
+        return x
+    if x.dtype is (_types or _torch_types())[0] and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError(f"expected a contiguous bf16 tensor, got {x.dtype}")
+
+
+def _q8_ptr(x, types) -> Optional[int]:
+    if x is None or x.__class__ is int:
+        return x
+    if x.dtype in types and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError("an 8-bit cache has contiguous e4m3 codes (torch.float8_e4m3fn or uint8) and "
+                     f"e8m0 scales (torch.float8_e8m0fnu or uint8), got {x.dtype}")
+
+
+def _q8_ptrs(k_codes, v_codes, k_scale, v_scale):
+    """The pointers of an 8-bit cache."""
+    _, _, codes, scales = _types or _torch_types()
+    return (_q8_ptr(k_codes, codes), _q8_ptr(v_codes, codes), _q8_ptr(k_scale, scales),
+            _q8_ptr(v_scale, scales))
 
 
 _current_stream = None
@@ -400,7 +425,7 @@ def tokens(q, k, v, q_out=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6
     do not overlap (slices of one projection's output; no expanded rows), q_out
     [T, Hq, D] for the processed queries (None: in place, which needs a packed q),
     optional [D] norm weights, and the RoPE table."""
-    bf16, fp32 = _types or _torch_types()
+    bf16, fp32, _, _ = _types or _torch_types()
     T, Hkv, D = shape = k.shape
     if shape != v.shape:
         raise ValueError("k and v must have the same shape")
@@ -461,7 +486,7 @@ def paged_kv_append_norm(d: Dims, t: Tokens, k_pool, v_pool, kv_indices, kv_indp
     """One new token a row: q and K normalised and rotated, K/V to their slots."""
     _token_count(d, t, per_row=True)
     _check("paged_kv_append_norm", lib().paged_kv_append_norm(
-        ctypes.byref(d), ctypes.byref(t), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices),
+        ctypes.byref(d), ctypes.byref(t), _bf16_ptr(k_pool), _bf16_ptr(v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -469,8 +494,9 @@ def paged_kv_extend_norm(d: Dims, t: Tokens, qo_indptr, k_pool, v_pool, kv_indic
                          seq_lens, status=None, stream=None) -> None:
     """paged_kv_append_norm for ragged chunks of new tokens."""
     _check("paged_kv_extend_norm", lib().paged_kv_extend_norm(
-        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t), _ptr(k_pool), _ptr(v_pool),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
+        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t), _bf16_ptr(k_pool),
+        _bf16_ptr(v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status),
+        _stream(stream)))
 
 
 # ---- the 8-bit cache ----------------------------------------------------------
@@ -481,17 +507,16 @@ def paged_kv_append_q8(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, k
     (torch.float8_e8m0fnu or uint8)."""
     _token_count(d, t, per_row=True)
     _check("paged_kv_append_q8", lib().paged_kv_append_q8(
-        ctypes.byref(d), ctypes.byref(t), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
-        _ptr(v_scale), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status),
-        _stream(stream)))
+        ctypes.byref(d), ctypes.byref(t), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
 def paged_kv_extend_q8(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale, v_scale,
                        kv_indices, kv_indptr, seq_lens, status=None, stream=None) -> None:
     """paged_kv_append_q8 for ragged chunks of new tokens."""
     _check("paged_kv_extend_q8", lib().paged_kv_extend_q8(
-        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t), _ptr(k_codes),
-        _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), _ptr(kv_indices), _ptr(kv_indptr),
+        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
+        *_q8_ptrs(k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
         _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -500,8 +525,8 @@ def paged_kv_read_q8(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv
     """Every row's tokens as bf16 into pages [num_indices, page_size, Hkv, D]
     in the table's order (pools for paged_prefill_attn with kv_indices 0, 1, ...)."""
     _check("paged_kv_read_q8", lib().paged_kv_read_q8(
-        ctypes.byref(d), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(k_out), _ptr(v_out),
+        ctypes.byref(d), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out), _bf16_ptr(v_out),
         _ptr(status), _stream(stream)))
 
 
@@ -510,9 +535,9 @@ def paged_decode_attn_q8(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indi
     """paged_decode_attn over an 8-bit cache."""
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_attn_q8", lib().paged_decode_attn_q8(
-        ctypes.byref(d), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
+        ctypes.byref(d), _bf16_ptr(q), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
-        ws_bytes, _ptr(out), _stream(stream)))
+        ws_bytes, _bf16_ptr(out), _stream(stream)))
 
 
 def paged_decode_plan_q8(d: Dims, kv_indices, kv_indptr, seq_lens, num_splits: int, workspace,
@@ -530,9 +555,9 @@ def paged_decode_attn_q8_planned(d: Dims, q, k_codes, v_codes, k_scale, v_scale,
     """paged_decode_attn_q8 on the workspace's plan (a step's later layers)."""
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_attn_q8_planned", lib().paged_decode_attn_q8_planned(
-        ctypes.byref(d), _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale),
+        ctypes.byref(d), _bf16_ptr(q), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
-        ws_bytes, _ptr(out), _stream(stream)))
+        ws_bytes, _bf16_ptr(out), _stream(stream)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -35,3 +35,54 @@ def test_the_rotation_table_is_fp32(other):
     assert pkv.tokens(q, k, k, rope_cos_sin=rope, rope_max_pos=5).rope_cos_sin == rope.data_ptr()
     with pytest.raises(ValueError):
         pkv.tokens(q, k, k, rope_cos_sin=rope.to(other), rope_max_pos=5)
+
+
+E4M3, E5M2, E8M0, U8 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu, torch.uint8
+
+
+def _calls():
+    """name -> (call of an empty batch, which launches nothing, and its cache tensors' types)"""
+    d = pkv.dims(0, 4, 2, 64, 16, 3, 0, 40)
+    zeros = lambda t, *s: torch.zeros(*s, dtype=t)  # noqa: E731
+    k, q = zeros(BF16, 0, 2, 64), zeros(BF16, 0, 4, 64)
+    t = pkv.tokens(None, k, k)
+    none = (None, None, None)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    pool = lambda kind: zeros(kind, 3, 16, 2, 64)  # noqa: E731
+    bf16 = dict(k_pool=pool(BF16), v_pool=pool(BF16))
+    q8 = dict(k_codes=pool(E4M3), v_codes=pool(E4M3), k_scale=zeros(U8, 3, 16, 2).view(E8M0),
+              v_scale=zeros(U8, 3, 16, 2).view(E8M0))
+    read = dict(q8, k_out=pool(BF16), v_out=pool(BF16))
+    dec = dict(q8, q=q, out=q)
+    four = lambda a: [a[n] for n in ("k_codes", "v_codes", "k_scale", "v_scale")]  # noqa: E731
+    return {
+        "append_norm": (lambda a: pkv.paged_kv_append_norm(d, t, a["k_pool"], a["v_pool"], *none, stream=0), bf16),
+        "extend_norm": (lambda a: pkv.paged_kv_extend_norm(d, t, None, a["k_pool"], a["v_pool"], *none, stream=0), bf16),
+        "append_q8": (lambda a: pkv.paged_kv_append_q8(d, t, *four(a), *none, stream=0), q8),
+        "extend_q8": (lambda a: pkv.paged_kv_extend_q8(d, t, None, *four(a), *none, stream=0), q8),
+        "read_q8": (lambda a: pkv.paged_kv_read_q8(d, *four(a), *none, a["k_out"], a["v_out"], stream=0), read),
+        "decode_q8": (lambda a: pkv.paged_decode_attn_q8(d, a["q"], *four(a), *none, 1, ws, a["out"], stream=0), dec),
+        "decode_q8_planned": (lambda a: pkv.paged_decode_attn_q8_planned(d, a["q"], *four(a), *none, 1, ws, a["out"],
+                                                                         stream=0), dec),
+    }
+
+
+@pytest.mark.parametrize("name", ["append_norm", "extend_norm", "append_q8", "extend_q8", "read_q8", "decode_q8",
+                                  "decode_q8_planned"])
+def test_a_cache_of_another_type_is_refused(name):
+    """An 8-bit pool taken for bf16 would be written at twice its size."""
+    call, args = _calls()[name]
+    call(args)
+    for at, right in args.items():
+        for other in (F16, torch.float32, E5M2, U8, E4M3, E8M0, BF16):
+            fits = (other is right.dtype or
+                    (other is U8 and right.element_size() == 1))
+            a = dict(args, **{at: torch.zeros(right.shape, dtype=other)})
+            if fits:
+                call(a)
+            else:
+                with pytest.raises(ValueError):
+                    call(a)
+        if right.dim() > 2 and right.numel():
+            with pytest.raises(ValueError):
+                call(dict(args, **{at: right.transpose(1, 2)}))
