@@ -171,6 +171,16 @@ def _torch_types():
     return _types
 
 
+def _pool_ptr(d: Dims, x) -> Optional[int]:
+    """A bf16 call's pool; one of single bytes must have room for bf16 (an 8-bit
+    cache's codes do not: they would be passed at twice their size)."""
+    if x is None or x.__class__ is int:
+        return x
+    if x.element_size() == 1 and x.numel() < d.num_pages * d.page_size * d.Hkv * d.D * 2:
+        raise ValueError(f"a pool of {x.dtype} is too small for bf16")
+    return _ptr(x)
+
+
 def _bf16_ptr(x) -> Optional[int]:
     if x is None or x.__class__ is int:
         return x
@@ -269,8 +279,8 @@ def paged_kv_append(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indices, kv_ind
                     seq_lens, rope_cos_sin=None, rope_max_pos: int = 0, rope_q: bool = False,
                     status=None, stream=None) -> None:
     _check("paged_kv_append", lib().paged_kv_append(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(rope_cos_sin),
+        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(rope_cos_sin),
         rope_max_pos, int(bool(rope_q)), _ptr(status), _stream(stream)))
 
 
@@ -278,7 +288,7 @@ def paged_decode_attn(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, seq_len
                       num_splits: int, workspace, out, stream=None) -> None:
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_attn", lib().paged_decode_attn(
-        ctypes.byref(d), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices),
+        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace), ws_bytes, _ptr(out),
         _stream(stream)))
 
@@ -288,9 +298,10 @@ def paged_decode_step(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indices, kv_i
                       out, stream=None) -> None:
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_step", lib().paged_decode_step(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(rope_cos_sin), rope_max_pos,
-        num_splits, _ptr(workspace), ws_bytes, _ptr(out), _stream(stream)))
+        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
+        _ptr(rope_cos_sin), rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out),
+        _stream(stream)))
 
 
 def paged_decode_plan(d: Dims, kv_indices, kv_indptr, seq_lens, num_splits: int, workspace,
@@ -307,7 +318,7 @@ def paged_decode_attn_planned(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr,
                               num_splits: int, workspace, out, stream=None) -> None:
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_attn_planned", lib().paged_decode_attn_planned(
-        ctypes.byref(d), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices),
+        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace), ws_bytes, _ptr(out),
         _stream(stream)))
 
@@ -317,9 +328,10 @@ def paged_decode_step_planned(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indic
                               workspace, out, stream=None) -> None:
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_step_planned", lib().paged_decode_step_planned(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(rope_cos_sin), rope_max_pos,
-        num_splits, _ptr(workspace), ws_bytes, _ptr(out), _stream(stream)))
+        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
+        _ptr(rope_cos_sin), rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out),
+        _stream(stream)))
 
 
 def paged_kv_advance(d: Dims, seq_lens, kv_indptr, kv_indices, free_pages, free_head,
@@ -343,10 +355,10 @@ def paged_decode_step_advance(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indic
     ws_bytes = workspace.numel() * workspace.element_size()
     num_free = 0 if free_pages is None else int(free_pages.numel())
     _check("paged_decode_step_advance", lib().paged_decode_step_advance(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(rope_cos_sin), rope_max_pos,
-        num_splits, _ptr(workspace), ws_bytes, _ptr(out), _ptr(free_pages), num_free,
-        _ptr(free_head), _stream(stream)))
+        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
+        _ptr(rope_cos_sin), rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out),
+        _ptr(free_pages), num_free, _ptr(free_head), _stream(stream)))
 
 
 def decode_attn_contig(d: Dims, q, k_cache, v_cache, seq_lens, num_splits: int, workspace,
@@ -360,9 +372,9 @@ def decode_attn_contig(d: Dims, q, k_cache, v_cache, seq_lens, num_splits: int, 
     ws_bytes = workspace.numel() * workspace.element_size()
     name = "decode_attn_contig_planned" if planned else "decode_attn_contig"
     _check(name, getattr(lib(), name)(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-        _ptr(cache_batch_idx), _ptr(seq_lens), _ptr(rope_cos_sin), rope_max_pos, num_splits,
-        _ptr(workspace), ws_bytes, _ptr(out), _stream(stream)))
+        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_cache),
+        _pool_ptr(d, v_cache), _ptr(cache_batch_idx), _ptr(seq_lens), _ptr(rope_cos_sin),
+        rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out), _stream(stream)))
 
 
 def paged_prefill_attn(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices, kv_indptr, seq_lens,
@@ -379,15 +391,15 @@ def paged_prefill_attn(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices, kv_ind
     mq = total_q if max_q_len is None else int(max_q_len)
     if workspace is None:
         _check("paged_prefill_attn", lib().paged_prefill_attn(
-            ctypes.byref(d), _ptr(q), _ptr(qo_indptr), total_q, mq, _ptr(k_pool), _ptr(v_pool),
-            _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(out), _ptr(status),
-            _stream(stream)))
+            ctypes.byref(d), _ptr(q), _ptr(qo_indptr), total_q, mq, _pool_ptr(d, k_pool),
+            _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(out),
+            _ptr(status), _stream(stream)))
         return
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_prefill_attn_ws", lib().paged_prefill_attn_ws(
-        ctypes.byref(d), _ptr(q), _ptr(qo_indptr), total_q, mq, _ptr(k_pool), _ptr(v_pool),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(workspace), ws_bytes,
-        _ptr(out), _ptr(status), _stream(stream)))
+        ctypes.byref(d), _ptr(q), _ptr(qo_indptr), total_q, mq, _pool_ptr(d, k_pool),
+        _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
+        _ptr(workspace), ws_bytes, _ptr(out), _ptr(status), _stream(stream)))
 
 
 def prefill_plan(d: Dims, max_q_len: int, num_sms: int, ws_bytes: int = 0) -> dict:
@@ -413,8 +425,9 @@ def paged_kv_extend(d: Dims, q, k_new, v_new, qo_indptr, k_pool, v_pool, kv_indi
     total_q = int(k_new.shape[0])
     _check("paged_kv_extend", lib().paged_kv_extend(
         ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(qo_indptr), total_q,
-        _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
-        _ptr(rope_cos_sin), rope_max_pos, int(bool(rope_q)), _ptr(status), _stream(stream)))
+        _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr),
+        _ptr(seq_lens), _ptr(rope_cos_sin), rope_max_pos, int(bool(rope_q)), _ptr(status),
+        _stream(stream)))
 
 
 # ---- new tokens: normalised, rotated, written --------------------------------
@@ -569,7 +582,7 @@ def paged_decode_attn_noalloc(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr,
     the library's own 16 MiB device array, shared by every call (calls that
     overlap on the GPU race)."""
     _check("paged_decode_attn_noalloc", lib().paged_decode_attn_noalloc(
-        ctypes.byref(d), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices),
+        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(out), _ptr(status),
         _stream(stream)))
 
@@ -578,7 +591,7 @@ def paged_decode_partials(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, seq
                           num_splits: int, workspace, stream=None) -> None:
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_partials", lib().paged_decode_partials(
-        ctypes.byref(d), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(kv_indices),
+        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace), ws_bytes,
         _stream(stream)))
 

@@ -86,3 +86,40 @@ def test_a_cache_of_another_type_is_refused(name):
         if right.dim() > 2 and right.numel():
             with pytest.raises(ValueError):
                 call(dict(args, **{at: right.transpose(1, 2)}))
+
+
+BF16_CALLS = {
+    "append": lambda d, k, v, x, ws: pkv.paged_kv_append(d, x, x, x, k, v, *[None] * 3, stream=0),
+    "extend": lambda d, k, v, x, ws: pkv.paged_kv_extend(d, x, x, x, None, k, v, *[None] * 3, stream=0),
+    "decode": lambda d, k, v, x, ws: pkv.paged_decode_attn(d, x, k, v, *[None] * 3, 1, ws, x, stream=0),
+    "planned": lambda d, k, v, x, ws: pkv.paged_decode_attn_planned(d, x, k, v, *[None] * 3, 1, ws, x, stream=0),
+    "step": lambda d, k, v, x, ws: pkv.paged_decode_step(d, x, x, x, k, v, *[None] * 4, 0, 1, ws, x, stream=0),
+    "step_planned": lambda d, k, v, x, ws: pkv.paged_decode_step_planned(d, x, x, x, k, v, *[None] * 4, 0, 1, ws, x,
+                                                                         stream=0),
+    "advance": lambda d, k, v, x, ws: pkv.paged_decode_step_advance(d, x, x, x, k, v, *[None] * 4, 0, 1, ws, x, None,
+                                                                    None, stream=0),
+    "contig": lambda d, k, v, x, ws: pkv.decode_attn_contig(d, x, k, v, None, 1, ws, x, stream=0),
+    "partials": lambda d, k, v, x, ws: pkv.paged_decode_partials(d, x, k, v, *[None] * 3, 1, ws, stream=0),
+    "noalloc": lambda d, k, v, x, ws: pkv.paged_decode_attn_noalloc(d, x, k, v, *[None] * 3, 1, x, stream=0),
+    "prefill": lambda d, k, v, x, ws: pkv.paged_prefill_attn(d, x, None, k, v, *[None] * 3, x, stream=0),
+    "prefill_ws": lambda d, k, v, x, ws: pkv.paged_prefill_attn(d, x, None, k, v, *[None] * 3, x, stream=0,
+                                                                workspace=ws),
+}
+
+
+@pytest.mark.parametrize("name", BF16_CALLS)
+def test_bf16_calls_refuse_the_codes_of_an_8_bit_cache(name):
+    """They would be read at twice their size.  (An empty batch: nothing is launched.)"""
+    d = pkv.dims(0, 4, 2, 64, 16, 3, 0, 40)
+    x, ws = torch.zeros(0, 4, 64, dtype=BF16), torch.zeros(1 << 20, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+    right = torch.zeros(3, 16, 2, 64, dtype=BF16)
+    call = BF16_CALLS[name]
+    call(d, right, right, x, ws)
+    raw = right.view(U8)                              # bytes with room for bf16 pass as before
+    call(d, raw, raw, x, ws)
+    for kind in (U8, E4M3):
+        codes = torch.zeros(3, 16, 2, 64, dtype=kind)
+        for k, v in ((codes, right), (right, codes)):
+            with pytest.raises(ValueError, match="too small"):
+                call(d, k, v, x, ws)
