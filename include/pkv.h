@@ -593,7 +593,8 @@ pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void 
 
 /* paged_decode_plan for the decode over an 8-bit cache, which weighs rows
  * otherwise: neither decode uses the other's plan (a planned call then computes
- * its partition itself, with the same results). */
+ * its partition itself, with the same results).  It holds the rows' prefix sums
+ * and their pieces, and no page-table windows: one launch of one block. */
 pkv_status paged_decode_plan_q8(const pkv_dims *dims, const int32_t *kv_indices,
                                 const int32_t *kv_indptr, const int32_t *seq_lens,
                                 int num_splits, void *workspace, size_t ws_bytes,

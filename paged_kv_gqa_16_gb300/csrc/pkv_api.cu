@@ -636,7 +636,7 @@ static pkv_status plan_impl(const pkv_dims *dims, const int32_t *kv_indices,
     const pkv::FusedParams p =
         persistent_params(dims, L, ws, kv_indices, kv_indptr, seq_lens, q8);
     return launch_status(pkv::launch_decode_plan(
-        p, num_splits, reinterpret_cast<int32_t *>(ws + L.plan_off), (cudaStream_t)stream));
+        p, num_splits, reinterpret_cast<int32_t *>(ws + L.plan_off), !q8, (cudaStream_t)stream));
 }
 
 pkv_status paged_decode_plan(const pkv_dims *dims, const int32_t *kv_indices,

@@ -733,16 +733,19 @@ __global__ void __launch_bounds__(FusedCfg<D, HPC>::kThreads, 1)
 // first block and piece count (row_info, read by the piece combine), and for
 // every block its first row and that row's page-table window.  A planned
 // decode call then starts its copies after one round trip to memory instead
-// of three.  One block per decode block; dynamic shared memory: Bv + 1 ints.
+// of three.  One block per decode block (`grid` of them); dynamic shared memory:
+// Bv + 1 ints.  The decode of the 8-bit cache reads no block entries: its plan
+// is written by one block.
 __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const FusedParams p,
-                                                                   int32_t *plan)
+                                                                   int32_t *plan, int grid,
+                                                                   bool entries)
 {
     extern __shared__ int pl_prefix[];
     const int Bv = p.Bv, cta = blockIdx.x, tid = threadIdx.x;
     grid_dependency_wait();
     row_prefix(p, pl_prefix, cta == 0);
     const unsigned T = (unsigned)pl_prefix[Bv];
-    const unsigned Gu = active_blocks(T, gridDim.x);
+    const unsigned Gu = active_blocks(T, (unsigned)grid);
     const int G = (int)Gu;
     if (cta == 0) {
         for (int i = tid; i <= Bv; i += blockDim.x)
@@ -760,13 +763,15 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const FusedPa
         if (tid == 0) {
             plan[0] = (int)T;
             plan[1] = G;
-            plan[2] = (int)gridDim.x;
+            plan[2] = grid;
             plan[3] = Bv;
             plan[4] = p.B;
             plan[5] = p.page_size;
             plan[6] = p.row_cost;
         }
     }
+    if (!entries)
+        return;
     int32_t *e = const_cast<int32_t *>(plan_entry(plan, Bv, cta));
     const unsigned t_q = T / Gu, t_r = T % Gu;
     const long long start = (long long)t_q * cta + t_r * (unsigned)cta / Gu;
@@ -1053,12 +1058,12 @@ extern "C" pkv_status pkv_testing_set_handoff_wait_ns(unsigned long long ns)
 
 namespace pkv {
 
-cudaError_t launch_decode_plan(const FusedParams &p, int grid, int32_t *plan,
+cudaError_t launch_decode_plan(const FusedParams &p, int grid, int32_t *plan, bool entries,
                                cudaStream_t stream)
 {
     const size_t smem = ((size_t)p.Bv + 1) * sizeof(int);
-    cudaError_t e = launch_pdl(decode_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, stream,
-                               p, plan);
+    cudaError_t e = launch_pdl(decode_plan_kernel, dim3(entries ? grid : 1), dim3(kPlanThreads),
+                               smem, stream, p, plan, grid, entries);
     if (e != cudaSuccess)
         return e;
     return cudaGetLastError();

@@ -359,8 +359,9 @@ cudaError_t launch_fused_decode(const FusedParams &p, int D, int grid, cudaStrea
 cudaError_t launch_piece_combine(const PieceCombineParams &p, int D, int grid_blocks,
                                  cudaStream_t stream);
 // The per-step plan for the decode kernel's grid of `grid` blocks; p carries
-// the shape, the tables, row_info and the status word.
-cudaError_t launch_decode_plan(const FusedParams &p, int grid, int32_t *plan,
+// the shape, the tables, row_info and the status word.  entries: with the
+// blocks' own entries, which the bf16 decode reads.
+cudaError_t launch_decode_plan(const FusedParams &p, int grid, int32_t *plan, bool entries,
                                cudaStream_t stream);
 int fused_heads_per_block(int Hkv);
 

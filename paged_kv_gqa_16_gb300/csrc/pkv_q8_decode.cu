@@ -233,9 +233,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
             }
         }
     }
-    // an unplanned call leaves its partition behind as the step's plan
-    int32_t *plan_e = p.plan_out != nullptr
-                          ? const_cast<int32_t *>(plan_entry(p.plan_out, Bv, cta)) : nullptr;
+    // an unplanned call leaves its partition behind as the step's plan (the prefix
+    // sums and the rows' pieces: this kernel reads no blocks' entries)
     if (p.plan_out != nullptr && cta == 0) {
         for (int i = threadIdx.x; i <= Bv; i += blockDim.x)
             p.plan_out[kPlanHeaderInts + i] = prefix[i];
@@ -255,11 +254,8 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
     const int end = p.whole_rows
                         ? (int)T
                         : (int)(t_q * (cta + 1) + t_r * (unsigned)(cta + 1) / Gu);
-    if ((cta >= G && !p.whole_rows) || start >= end) {
-        if (plan_e != nullptr && threadIdx.x == 0)
-            plan_e[0] = -1;
+    if ((cta >= G && !p.whole_rows) || start >= end)
         return;
-    }
     const int r0 = first_row(prefix, n_rows, start);
 
     if (warp >= kWarps) {
@@ -289,17 +285,6 @@ __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)
             int npg = p.kv_indptr[b + 1] - pg0;
             if (pg0 < 0 || npg < 0 || pg0 > p.num_indices - npg)
                 npg = 0;                               // a table changed since the plan
-            if (plan_e != nullptr && r == r0 && pw == 0) {
-                // the bf16 decode's entry holds a 64-entry window of the table
-                const int wb = (page_of_tok(t0) >> 5) << 5;
-                for (int k = lane; k < 64; k += 32)
-                    plan_e[8 + k] = wb + k < npg ? p.kv_indices[pg0 + wb + k] : 0;
-                if (lane < 8) {
-                    plan_e[lane] = lane == 0 ? r0 : lane == 1 ? wb : lane == 2 ? pg0
-                                 : lane == 3 ? npg : lane == 4 ? lo : lane == 5 ? hi
-                                 : lane == 6 ? start : end;
-                }
-            }
             // the table's entry for this lane's token k of the stage at tok
             auto load_id = [&](int tok, int k) {
                 const int at = k * 32 + lane;
