@@ -481,7 +481,11 @@ pkv_status paged_decode_step_advance(const pkv_dims *dims, const void *q, const 
  *   are summed in fp32: heads of values past 1e18 overflow it, and squares of
  *   values below 1e-22 are lost beside norm_eps = 0).
  *   rope_cos_sin, rope_max_pos: the table of pkv_rope_table, or NULL for no
- *   rotation.
+ *   rotation.  The rotation is on pairs (x[2i], x[2i+1]), as in every call here.
+ *   A model that rotates (x[i], x[i + D/2]) uses it on heads whose elements are
+ *   reordered to x[0], x[D/2], x[1], x[D/2 + 1], ...: reorder the rows of its q
+ *   and k projections within each head once, and q_norm and k_norm the same way
+ *   (q.k, and the norms, do not change under one order for both; v keeps its own).
  * Every step is done in fp32 and the result rounded once. */
 typedef struct {
     const void *q;

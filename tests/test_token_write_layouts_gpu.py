@@ -65,3 +65,33 @@ def test_row_strides_past_31_bits(extend, q8):
     assert int(c.status.item()) == 0 and bool(torch.isfinite(got[0][0].float()).all())
     for a, b in zip(*got):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_models_that_rotate_the_halves_of_a_head(D):
+    """With the heads' elements and the norm weights in the order x[0], x[D/2], x[1], ...
+    the write gives what norm and rotation of (x[i], x[i + D/2]) give, in that order."""
+    c = Cache([40, 7], 4, 2, D, 16, seed=3)
+    order = torch.arange(D).view(2, D // 2).T.reshape(-1)
+    q, k, v = (c.randn(2, H, D).to(torch.bfloat16) for H in (4, 2, 2))
+    w = (1 + 0.3 * c.randn(D)).to(torch.bfloat16)
+    table = rope_table(64, D)
+    q_out = torch.empty(2, 4, D, dtype=torch.bfloat16, device=DEV)
+    pkv.paged_kv_append_norm(
+        c.d, pkv.tokens(q[..., order].contiguous().to(DEV), k[..., order].contiguous().to(DEV), v.to(DEV), q_out,
+                        w[order].to(DEV), w[order].to(DEV), rope_cos_sin=table, rope_max_pos=64),
+        c.k16, c.v16, *c.rows)
+
+    def want(x, pos):
+        x = x.double()
+        x = x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w.double()
+        cos, sin = table[pos].cpu().double().unbind(-1)
+        a, b = x[..., :D // 2], x[..., D // 2:]
+        return torch.cat([a * cos - b * sin, a * sin + b * cos], -1)[..., order]
+
+    for b, L in enumerate(c.lens):
+        page, slot = c.places(b, L - 1, L)
+        for got, x in ((q_out[b], q[b]), (c.k16[page[0], slot[0]], k[b])):
+            # one rounding to bf16, and fp32's of a norm and a rotation of values up to 8
+            assert bool(((got.cpu().double() - want(x, L - 1)).abs() <=
+                         want(x, L - 1).abs() * 2.0 ** -8 + 2.0 ** -13).all())
