@@ -142,7 +142,8 @@ __device__ __forceinline__ int first_row(const int *prefix, int Bv, long long st
 // first table entry kv_indptr[b], [3] its entry count, [4] and [5] the
 // positions of the row's first and last-plus-one token, [6] and [7] the
 // block's positions [start, end), [8..71] the window (the row's table
-// entries wb .. wb + 63, 0 past the table).
+// entries wb .. wb + 63, 0 past the table).  A plan of the 8-bit cache's decode
+// has no entries.
 constexpr int kPlanHeaderInts = 16;
 constexpr int kPlanEntryInts = 72;
 

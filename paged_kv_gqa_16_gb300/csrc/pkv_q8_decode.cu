@@ -54,10 +54,11 @@
 //    tokens, 54.5 against 44.4 for one kv head of 128, and no odd pages.
 //
 // Measured (CUDA-graph replay, K and V larger than L2 or rotating): 128 rows,
-// lognormal, 154,103 tokens, 64 over 8 heads of 128, 322 MB: 57.5 us, 5,600 GB/s,
-// 83% of the copy bandwidth (56.7 us with the products left out: the copies set
-// the pace); one row of 32,768: 20.0 us, 10 of them the stream, 5 the combine;
-// 8 rows of 513 to 1,025, heads of 64: 9.2 us, latency.
+// lognormal, 154,103 tokens, 64 over 8 heads of 128, 322 MB: 57.3 us, 5,620 GB/s,
+// 83% of the copy bandwidth (0.4 us less with the products left out: the copies
+// set the pace; 53.2 without the combine); one row of 32,768: 19.6 us, 10 of them
+// the stream, 3.5 the combine and its launch; 8 rows of 513 to 1,025, heads of 64:
+// 8.7 us, latency (2.8 the combine).
 #include <cmath>
 
 #include "pkv_partition.cuh"

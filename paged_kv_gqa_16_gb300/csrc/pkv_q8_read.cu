@@ -9,12 +9,13 @@
 // slots of that list: a lane a slot finds the entry's row, its length and the page,
 // then all lanes stream the slots' heads, 16 codes of K and the 16 of V beside them
 // at a time.  3 bytes of traffic a value and nothing else to do: bound by memory.
-// 32 ragged rows, 73,728 tokens of 8 heads of 128, 454 MB: 73.4 us, 6,190 GB/s, 91% of
-// the copy bandwidth (86.4 us with two 16-byte stores in place of each 32-byte one, 92
-// with four vectors of one pool a thread, 105 with 8-byte loads).  Blocks of 256
-// threads that look up their slots together take 74.6; 9.9 in place of 8.4 for 6,152
-// tokens, 7.0 in place of 4.9 for those of D = 64, 3.0 in place of 2.2 for 137, 4.8 in
-// place of 5.5 for 48,000 of one head of 64 at page size 1.
+// 32 ragged rows, 73,728 tokens of 8 heads of 128, 454 MB: 71.7 us, 6,330 GB/s, 93% of
+// the copy bandwidth.  Variants, measured against 73.4 us for this layout at the time:
+// 86.4 us with two 16-byte stores in place of each 32-byte one, 92 with four vectors of
+// one pool a thread, 105 with 8-byte loads.  Blocks of 256 threads that look up their
+// slots together took 74.6; 9.9 in place of 8.4 for 6,152 tokens, 7.0 in place of 4.9
+// for those of D = 64, 3.0 in place of 2.2 for 137, 4.8 in place of 5.5 for 48,000 of
+// one head of 64 at page size 1.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_q8.cuh"
