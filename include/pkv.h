@@ -613,6 +613,46 @@ pkv_status paged_decode_attn_q8_planned(const pkv_dims *dims, const void *q, con
                                         int num_splits, void *workspace, size_t ws_bytes,
                                         void *out, pkv_stream_t stream);
 
+/* ---- the 4-bit cache -------------------------------------------------------- */
+
+/* A cache of e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one
+ * power-of-two scale for each 32 elements of a head vector, in a little over a
+ * quarter of the bytes of the bf16 pools:
+ *   k_codes, v_codes [num_pages, page_size, Hkv, D / 2]  bytes of two codes, elements
+ *                    2i and 2i + 1 of a head in the low and the high half of
+ *                    byte i; 16-byte aligned
+ *   k_scale, v_scale [num_pages, page_size, Hkv, D / 32] e8m0, 16-byte aligned
+ * An element is code * 2^(scale - 127).  The writes below choose, for 32 elements
+ * whose largest magnitude is amax,
+ *   scale = 127 + clamp(ceil(log2(amax / 6)), -40, 40),
+ *   code  = x * 2^(127 - scale) rounded to the nearest e2m1 (ties to the even
+ *           code, saturating at 6),
+ * of the exact value x of the formulas above (its last bits count next to a
+ * border; the norm's sum overflows and underflows as in fp32), V: the bf16 value.
+ * Where one of the 32 is infinite or NaN, all have scale 255, which stands for
+ * NaN; magnitudes above 6 * 2^40 saturate.  The same pages, tables and lengths as
+ * the bf16 calls. */
+
+/* paged_kv_append_norm into a 4-bit cache (norms optional). */
+pkv_status paged_kv_append_q4(const pkv_dims *dims, const pkv_tokens *tokens, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream);
+
+/* paged_kv_extend_norm into a 4-bit cache (norms optional). */
+pkv_status paged_kv_extend_q4(const pkv_dims *dims, const pkv_tokens *tokens,
+                              const int32_t *qo_indptr, int total_q, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream);
+
+/* paged_kv_read_q8 of a 4-bit cache: the same outputs, checks and flags. */
+pkv_status paged_kv_read_q4(const pkv_dims *dims, const void *k_codes, const void *v_codes,
+                            const void *k_scale, const void *v_scale,
+                            const int32_t *kv_indices, const int32_t *kv_indptr,
+                            const int32_t *seq_lens, void *k_out, void *v_out,
+                            uint32_t *status, pkv_stream_t stream);
+
 /* ---- for callers that cannot allocate ------------------------------------ */
 
 /* Size of the library-held scratch used by paged_decode_attn_noalloc. */

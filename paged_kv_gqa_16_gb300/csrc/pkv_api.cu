@@ -980,10 +980,10 @@ pkv_status check_row_stride(long long stride, int H, int D)
                                                                          : PKV_ERR_INVALID_ARG;
 }
 
-// The append and extend of pkv_tokens; k_scale == nullptr: bf16 pools.
+// The append and extend of pkv_tokens; bits 16: bf16 pools, 8 and 4: codes and scales.
 pkv_status token_write(const pkv_dims *dims, const pkv_tokens *t, bool extend,
                        const int32_t *qo_indptr, int total_q, void *k_pool, void *v_pool,
-                       bool q8, void *k_scale, void *v_scale, const int32_t *kv_indices,
+                       int bits, void *k_scale, void *v_scale, const int32_t *kv_indices,
                        const int32_t *kv_indptr, const int32_t *seq_lens, uint32_t *status,
                        pkv_stream_t stream)
 {
@@ -996,7 +996,7 @@ pkv_status token_write(const pkv_dims *dims, const pkv_tokens *t, bool extend,
         return PKV_OK;
     if (t->k == nullptr || t->v == nullptr || k_pool == nullptr || v_pool == nullptr ||
         kv_indptr == nullptr || seq_lens == nullptr || (extend && qo_indptr == nullptr) ||
-        (q8 && (k_scale == nullptr || v_scale == nullptr)) ||
+        (bits < 16 && (k_scale == nullptr || v_scale == nullptr)) ||
         (dims->num_indices > 0 && kv_indices == nullptr) ||
         (t->q != nullptr && t->q_out == nullptr))
         return PKV_ERR_INVALID_ARG;
@@ -1040,8 +1040,9 @@ pkv_status token_write(const pkv_dims *dims, const pkv_tokens *t, bool extend,
     p.rope_max_pos = t->rope_max_pos;
     p.k_pool = k_pool;
     p.v_pool = v_pool;
-    p.k_scale = q8 ? static_cast<uint8_t *>(k_scale) : nullptr;
-    p.v_scale = q8 ? static_cast<uint8_t *>(v_scale) : nullptr;
+    p.bits = bits;
+    p.k_scale = static_cast<uint8_t *>(k_scale);
+    p.v_scale = static_cast<uint8_t *>(v_scale);
     p.kv_indices = kv_indices;
     p.kv_indptr = kv_indptr;
     p.seq_lens = seq_lens;
@@ -1064,7 +1065,7 @@ pkv_status paged_kv_append_norm(const pkv_dims *dims, const pkv_tokens *tokens, 
                                 const int32_t *kv_indptr, const int32_t *seq_lens,
                                 uint32_t *status, pkv_stream_t stream)
 {
-    return token_write(dims, tokens, false, nullptr, 0, k_pool, v_pool, false, nullptr, nullptr,
+    return token_write(dims, tokens, false, nullptr, 0, k_pool, v_pool, 16, nullptr, nullptr,
                        kv_indices, kv_indptr, seq_lens, status, stream);
 }
 
@@ -1074,7 +1075,7 @@ pkv_status paged_kv_extend_norm(const pkv_dims *dims, const pkv_tokens *tokens,
                                 const int32_t *kv_indptr, const int32_t *seq_lens,
                                 uint32_t *status, pkv_stream_t stream)
 {
-    return token_write(dims, tokens, true, qo_indptr, total_q, k_pool, v_pool, false, nullptr,
+    return token_write(dims, tokens, true, qo_indptr, total_q, k_pool, v_pool, 16, nullptr,
                        nullptr, kv_indices, kv_indptr, seq_lens, status, stream);
 }
 
@@ -1083,7 +1084,7 @@ pkv_status paged_kv_append_q8(const pkv_dims *dims, const pkv_tokens *tokens, vo
                               const int32_t *kv_indices, const int32_t *kv_indptr,
                               const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream)
 {
-    return token_write(dims, tokens, false, nullptr, 0, k_codes, v_codes, true, k_scale, v_scale,
+    return token_write(dims, tokens, false, nullptr, 0, k_codes, v_codes, 8, k_scale, v_scale,
                        kv_indices, kv_indptr, seq_lens, status, stream);
 }
 
@@ -1093,15 +1094,34 @@ pkv_status paged_kv_extend_q8(const pkv_dims *dims, const pkv_tokens *tokens,
                               const int32_t *kv_indices, const int32_t *kv_indptr,
                               const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream)
 {
-    return token_write(dims, tokens, true, qo_indptr, total_q, k_codes, v_codes, true, k_scale,
+    return token_write(dims, tokens, true, qo_indptr, total_q, k_codes, v_codes, 8, k_scale,
                        v_scale, kv_indices, kv_indptr, seq_lens, status, stream);
 }
 
-pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const void *v_codes,
-                            const void *k_scale, const void *v_scale,
-                            const int32_t *kv_indices, const int32_t *kv_indptr,
-                            const int32_t *seq_lens, void *k_out, void *v_out,
-                            uint32_t *status, pkv_stream_t stream)
+pkv_status paged_kv_append_q4(const pkv_dims *dims, const pkv_tokens *tokens, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream)
+{
+    return token_write(dims, tokens, false, nullptr, 0, k_codes, v_codes, 4, k_scale, v_scale,
+                       kv_indices, kv_indptr, seq_lens, status, stream);
+}
+
+pkv_status paged_kv_extend_q4(const pkv_dims *dims, const pkv_tokens *tokens,
+                              const int32_t *qo_indptr, int total_q, void *k_codes,
+                              void *v_codes, void *k_scale, void *v_scale,
+                              const int32_t *kv_indices, const int32_t *kv_indptr,
+                              const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream)
+{
+    return token_write(dims, tokens, true, qo_indptr, total_q, k_codes, v_codes, 4, k_scale,
+                       v_scale, kv_indices, kv_indptr, seq_lens, status, stream);
+}
+
+static pkv_status read_codes(const pkv_dims *dims, int bits, const void *k_codes,
+                             const void *v_codes, const void *k_scale, const void *v_scale,
+                             const int32_t *kv_indices, const int32_t *kv_indptr,
+                             const int32_t *seq_lens, void *k_out, void *v_out,
+                             uint32_t *status, pkv_stream_t stream)
 {
     pkv_status st = check_dims(dims);
     if (st != PKV_OK)
@@ -1117,7 +1137,8 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
         !aligned(kv_indptr, 4) || !aligned(seq_lens, 4) || !aligned(kv_indices, 4) ||
         !aligned(status, 4))
         return PKV_ERR_INVALID_ARG;
-    pkv::ReadQ8Params p{};
+    pkv::ReadCodesParams p{};
+    p.bits = bits;
     p.k_codes = static_cast<const uint8_t *>(k_codes);
     p.v_codes = static_cast<const uint8_t *>(v_codes);
     p.k_scale = static_cast<const uint8_t *>(k_scale);
@@ -1135,7 +1156,27 @@ pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const voi
     p.num_pages = dims->num_pages;
     p.num_indices = dims->num_indices;
     p.max_seq_len = dims->max_seq_len;
-    return launch_status(pkv::launch_read_q8(p, dims->D, (cudaStream_t)stream));
+    return launch_status(pkv::launch_read_codes(p, dims->D, (cudaStream_t)stream));
+}
+
+pkv_status paged_kv_read_q8(const pkv_dims *dims, const void *k_codes, const void *v_codes,
+                            const void *k_scale, const void *v_scale,
+                            const int32_t *kv_indices, const int32_t *kv_indptr,
+                            const int32_t *seq_lens, void *k_out, void *v_out,
+                            uint32_t *status, pkv_stream_t stream)
+{
+    return read_codes(dims, 8, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr, seq_lens,
+                      k_out, v_out, status, stream);
+}
+
+pkv_status paged_kv_read_q4(const pkv_dims *dims, const void *k_codes, const void *v_codes,
+                            const void *k_scale, const void *v_scale,
+                            const int32_t *kv_indices, const int32_t *kv_indptr,
+                            const int32_t *seq_lens, void *k_out, void *v_out,
+                            uint32_t *status, pkv_stream_t stream)
+{
+    return read_codes(dims, 4, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr, seq_lens,
+                      k_out, v_out, status, stream);
 }
 
 // Rows that one launch over the 8-bit cache takes: its rows x kv-head groups

@@ -89,8 +89,8 @@ struct AppendParams {
     int total_q;               // extend: tokens in all chunks
 };
 
-// New tokens written to the cache (pkv_tokens.cu); k_scale == nullptr: bf16
-// pools, else e4m3 codes and e8m0 scales.
+// New tokens written to the cache (pkv_tokens.cu); bits 16: bf16 pools, 8 and 4:
+// codes and e8m0 scales.
 struct TokenWriteParams {
     const __nv_bfloat16 *q;        // nullable: no query work
     const __nv_bfloat16 *k;
@@ -100,7 +100,7 @@ struct TokenWriteParams {
     const __nv_bfloat16 *q_norm;   // [D] or nullptr
     const __nv_bfloat16 *k_norm;
     const float *rope;             // [rope_max_pos, D/2, 2] or nullptr
-    void *k_pool;                  // bf16 pools or e4m3 codes
+    void *k_pool;                  // bf16 pools or codes
     void *v_pool;
     uint8_t *k_scale;
     uint8_t *v_scale;
@@ -111,11 +111,12 @@ struct TokenWriteParams {
     uint32_t *status;              // nullable
     float norm_eps;
     int T, B, Hq, Hkv, page_size, num_pages, num_indices, max_seq_len, rope_max_pos;
+    int bits;                      // 16, 8 or 4
     int width_shift;               // log2 of the lane groups a token takes (set by the launcher)
 };
 
-// An 8-bit cache read back as bf16 (pkv_q8_read.cu).
-struct ReadQ8Params {
+// An 8-bit or 4-bit cache read back as bf16 (pkv_q8_read.cu).
+struct ReadCodesParams {
     const uint8_t *k_codes;
     const uint8_t *v_codes;
     const uint8_t *k_scale;
@@ -128,6 +129,7 @@ struct ReadQ8Params {
     uint32_t *status;              // nullable
     int B, Hkv, page_size, num_pages, num_indices, max_seq_len;
     int ps_shift;                  // log2 of page_size, or -1
+    int bits;                      // 8 or 4
     int per_warp;                  // token slots a warp takes at a time (set by the launcher)
 };
 
@@ -324,7 +326,7 @@ struct CombineParams {
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_extend(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_token_write(const TokenWriteParams &p, int D, cudaStream_t stream);
-cudaError_t launch_read_q8(const ReadQ8Params &p, int D, cudaStream_t stream);
+cudaError_t launch_read_codes(const ReadCodesParams &p, int D, cudaStream_t stream);
 // the decode over an 8-bit cache; p.k_codes ... p.v_scale in place of the pools
 cudaError_t launch_decode_q8(const FusedParams &p, int D, int grid, cudaStream_t stream);
 cudaError_t launch_advance(const AdvanceParams &p, cudaStream_t stream);

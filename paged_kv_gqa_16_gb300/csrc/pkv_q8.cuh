@@ -76,4 +76,10 @@ __device__ __forceinline__ float q8_scale(unsigned byte)
     return __uint_as_float(byte << 23);
 }
 
+// The scale of any e8m0 byte: 0 stands for 2^-127, 255 for NaN.
+__device__ __forceinline__ float any_scale(unsigned byte)
+{
+    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
+}
+
 } // namespace pkv

@@ -1,4 +1,4 @@
-// pkv_q8_read.cu -- the rows of an 8-bit cache read back as bf16.
+// pkv_q8_read.cu -- the rows of an 8-bit or a 4-bit cache read back as bf16.
 //
 // bf16(code * 2^e) is exact: a code has four significant bits, a bf16 eight.
 // (Scales under 2^-124 and over 2^119, which the writes do not choose, leave bf16's
@@ -18,6 +18,7 @@
 // one head of 64 at page size 1.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_q4.cuh"
 #include "pkv_q8.cuh"
 
 namespace pkv {
@@ -47,12 +48,11 @@ __device__ __forceinline__ uint4 decode8(uint32_t lo, uint32_t hi, float f)
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 16 codes times f to dst: one 32-byte store where the outputs are so aligned
-// (two of 16 bytes write each 32-byte sector in halves, a warp apart).
+// 16 values to dst: one 32-byte store where the outputs are so aligned (two of 16
+// bytes write each 32-byte sector in halves, a warp apart).
 template <bool WIDE>
-__device__ __forceinline__ void store16(__nv_bfloat16 *dst, uint4 c, float f)
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *dst, uint4 a, uint4 b)
 {
-    const uint4 a = decode8(c.x, c.y, f), b = decode8(c.z, c.w, f);
     if constexpr (WIDE) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
                      "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z),
@@ -64,14 +64,36 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *dst, uint4 c, float f)
     }
 }
 
-// The scale of any e8m0 byte: 0 stands for 2^-127, 255 for NaN.
-__device__ __forceinline__ float any_scale(unsigned byte)
+// 16 codes times f to dst.
+template <bool WIDE>
+__device__ __forceinline__ void store16(__nv_bfloat16 *dst, uint4 c, float f)
 {
-    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
+    store_pair<WIDE>(dst, decode8(c.x, c.y, f), decode8(c.z, c.w, f));
+}
+
+// Eight 4-bit codes times f as eight bf16.
+__device__ __forceinline__ uint4 decode8_q4(uint32_t w, float f)
+{
+    const uint32_t h[4] = {f16x2_of_e2m1x2<0>(w), f16x2_of_e2m1x2<1>(w), f16x2_of_e2m1x2<2>(w),
+                           f16x2_of_e2m1x2<3>(w)};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+        o[j] = pack_bf16x2(x.x * f, x.y * f);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 16 of them (two words of codes).
+template <bool WIDE>
+__device__ __forceinline__ void store16_q4(__nv_bfloat16 *dst, uint2 c, float f)
+{
+    store_pair<WIDE>(dst, decode8_q4(c.x, f), decode8_q4(c.y, f));
 }
 
 // Pool slot of output slot `at`, or -1 if no token of a row is there.
-__device__ __forceinline__ long long source_of(const ReadQ8Params &p, long long at)
+__device__ __forceinline__ long long source_of(const ReadCodesParams &p, long long at)
 {
     const int j = p.ps_shift >= 0     ? (int)(at >> p.ps_shift)
                   : at < (1ll << 31) ? (int)at / p.page_size
@@ -98,8 +120,8 @@ __device__ __forceinline__ long long source_of(const ReadQ8Params &p, long long 
     return (long long)page * p.page_size + sl;
 }
 
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 12) read_q8_kernel(const ReadQ8Params p)
+template <int D, int BITS, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 12) read_codes_kernel(const ReadCodesParams p)
 {
     constexpr int VPH = D / 16;          // 16-code vectors of a head
     grid_dependency_wait();
@@ -134,11 +156,20 @@ __global__ void __launch_bounds__(kThreads, 12) read_q8_kernel(const ReadQ8Param
             const size_t head = (size_t)src * p.Hkv + k / VPH;
             const size_t from = head * D + (k % VPH) * 16;
             const size_t to = ((size_t)(s0 + tok) * per_tok + k) * 16;
-            const uint4 kc = __ldcs(reinterpret_cast<const uint4 *>(p.k_codes + from));
-            const uint4 vc = __ldcs(reinterpret_cast<const uint4 *>(p.v_codes + from));
-            const float fk = any_scale(p.k_scale[head]), fv = any_scale(p.v_scale[head]);
-            store16<WIDE>(p.k_out + to, kc, fk);
-            store16<WIDE>(p.v_out + to, vc, fv);
+            if constexpr (BITS == 8) {
+                const uint4 kc = __ldcs(reinterpret_cast<const uint4 *>(p.k_codes + from));
+                const uint4 vc = __ldcs(reinterpret_cast<const uint4 *>(p.v_codes + from));
+                const float fk = any_scale(p.k_scale[head]), fv = any_scale(p.v_scale[head]);
+                store16<WIDE>(p.k_out + to, kc, fk);
+                store16<WIDE>(p.v_out + to, vc, fv);
+            } else {
+                const uint2 kc = __ldcs(reinterpret_cast<const uint2 *>(p.k_codes + from / 2));
+                const uint2 vc = __ldcs(reinterpret_cast<const uint2 *>(p.v_codes + from / 2));
+                const size_t group = from / kQ4Group;
+                const float fk = any_scale(p.k_scale[group]), fv = any_scale(p.v_scale[group]);
+                store16_q4<WIDE>(p.k_out + to, kc, fk);
+                store16_q4<WIDE>(p.v_out + to, vc, fv);
+            }
         }
     }
     grid_launch_dependents();
@@ -146,9 +177,9 @@ __global__ void __launch_bounds__(kThreads, 12) read_q8_kernel(const ReadQ8Param
 
 } // namespace
 
-cudaError_t launch_read_q8(const ReadQ8Params &params, int D, cudaStream_t stream)
+cudaError_t launch_read_codes(const ReadCodesParams &params, int D, cudaStream_t stream)
 {
-    ReadQ8Params p = params;
+    ReadCodesParams p = params;
     const long long slots = (long long)p.num_indices * p.page_size;
     const int most = p.Hkv * D > kWarpValues ? 1 : kWarpValues / (p.Hkv * D);   // up to 32
     // a slot's share, in whole rounds of 32 lanes (one head of 64: 6.0 us without)
@@ -162,9 +193,14 @@ cudaError_t launch_read_q8(const ReadQ8Params &params, int D, cudaStream_t strea
     const bool wide = ((reinterpret_cast<uintptr_t>(p.k_out) |
                         reinterpret_cast<uintptr_t>(p.v_out)) & 31) == 0;
     auto run = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, p); };
+    if (p.bits == 8) {
+        if (D == 64)
+            return wide ? run(read_codes_kernel<64, 8, true>) : run(read_codes_kernel<64, 8, false>);
+        return wide ? run(read_codes_kernel<128, 8, true>) : run(read_codes_kernel<128, 8, false>);
+    }
     if (D == 64)
-        return wide ? run(read_q8_kernel<64, true>) : run(read_q8_kernel<64, false>);
-    return wide ? run(read_q8_kernel<128, true>) : run(read_q8_kernel<128, false>);
+        return wide ? run(read_codes_kernel<64, 4, true>) : run(read_codes_kernel<64, 4, false>);
+    return wide ? run(read_codes_kernel<128, 4, true>) : run(read_codes_kernel<128, 4, false>);
 }
 
 } // namespace pkv

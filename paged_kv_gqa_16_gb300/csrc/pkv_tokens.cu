@@ -9,6 +9,11 @@
 //             e = clamp(ceil(log2(amax / 448)), -40, 40) of the vector.  Codes
 //             are floating point, so a power of two keeps the precision of an
 //             arbitrary scale, costs one byte, and scales without rounding.
+//             Or e2m1 codes, e = clamp(ceil(log2(amax / 6)), -40, 40) of each
+//             32 elements.  A step of these codes is up to half their value, so
+//             a key next to a border is decided as the exact value is: where 32
+//             bits do not tell (their error against the distance, one warp's
+//             round in some hundreds) the warp forms its vectors in 64.
 //
 // The pass reads and writes every value once and is bound by memory, if the
 // arithmetic is kept small: a head vector belongs to a group of D / 8 lanes with
@@ -31,6 +36,7 @@
 // to 128 rows: 2.4 to 3.6 us, the launch and three dependent loads.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_q4.cuh"
 #include "pkv_q8.cuh"
 
 namespace pkv {
@@ -265,6 +271,26 @@ __device__ __forceinline__ uint4 pack(const Eight &x, float f)
                       pack_bf16x2(a1.x, b1.x), pack_bf16x2(a1.y, b1.y));
 }
 
+// x f, in order.
+__device__ __forceinline__ void values_of(const Eight &x, float f, float (&y)[8])
+{
+    const F2 ff = f2(f, f);
+    const float2 a0 = parts(mul2(x.a[0], ff)), a1 = parts(mul2(x.a[1], ff));
+    const float2 b0 = parts(mul2(x.b[0], ff)), b1 = parts(mul2(x.b[1], ff));
+    y[0] = a0.x, y[1] = b0.x, y[2] = a0.y, y[3] = b0.y;
+    y[4] = a1.x, y[5] = b1.x, y[6] = a1.y, y[7] = b1.y;
+}
+
+// The pairs' sums of magnitudes, times f.
+__device__ __forceinline__ void pair_sizes(const Eight &x, float f, float (&s)[4])
+{
+    const float2 a0 = parts(x.a[0]), a1 = parts(x.a[1]), b0 = parts(x.b[0]), b1 = parts(x.b[1]);
+    s[0] = (fabsf(a0.x) + fabsf(b0.x)) * f;
+    s[1] = (fabsf(a0.y) + fabsf(b0.y)) * f;
+    s[2] = (fabsf(a1.x) + fabsf(b1.x)) * f;
+    s[3] = (fabsf(a1.y) + fabsf(b1.y)) * f;
+}
+
 // x f as codes and the scale byte of the group's vector.
 template <int D>
 __device__ __forceinline__ uint2 quantise(const Eight &x, float f, int &sb)
@@ -281,8 +307,122 @@ __device__ __forceinline__ uint2 quantise(const Eight &x, float f, int &sb)
     return q8_encode8(y, f, sb, amax == INFINITY);
 }
 
+// The nearest float toward zero, its last bit set if x is not that float: rounding
+// it to fewer bits, and comparing it with numbers of fewer bits, give what x gives.
+__device__ __forceinline__ float odd_of(double x)
+{
+    const float f = __double2float_rz(x);
+    return __uint_as_float(__float_as_uint(f) | ((double)f != x ? 1u : 0u));
+}
+
+// A lane's eight key values in 64 bits, as odd_of them: for the codes that lie too
+// near a border for 32 bits.  Rare (under 1% of a warp's rounds), so it reads the
+// weight and the rotation again.  1 / sqrt from the 32-bit one by two Newton steps.
+template <int D>
+__device__ __noinline__ void key_values_in_64(const __nv_bfloat16 *weight, const float *cos_sin,
+                                              float eps, uint4 raw, float (&y)[8])
+{
+    constexpr int LANES = D / 8;
+    const int lane = threadIdx.x % LANES;
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    double x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[2 * i] = bf16_lo(in[i]), x[2 * i + 1] = bf16_hi(in[i]);
+    double r = 1.0;
+    if (weight != nullptr) {
+        double s = 0.0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s = fma(x[j], x[j], s);
+#pragma unroll
+        for (int m = 1; m < LANES; m <<= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, m);
+        s = s * (1.0 / D) + (double)eps;
+        const float r32 = rsqrtf((float)s);
+        r = r32;
+        if (r32 > 0.f && r32 < INFINITY) {          // (else as in 32 bits)
+            r = r * (1.5 - 0.5 * s * r * r);
+            r = r * (1.5 - 0.5 * s * r * r);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] *= (double)__bfloat162float(weight[lane * 8 + j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        double a = x[2 * i], b = x[2 * i + 1];
+        if (cos_sin != nullptr) {
+            const double c = cos_sin[lane * 8 + 2 * i], t = cos_sin[lane * 8 + 2 * i + 1];
+            const double u = a * c - b * t;
+            b = a * t + b * c;
+            a = u;
+        }
+        y[2 * i] = odd_of(a * r);
+        y[2 * i + 1] = odd_of(b * r);
+    }
+}
+
+// The largest magnitude of the 32 elements of a scale, four lanes', as bits (of
+// which those of a NaN and of infinity are the largest).
+__device__ __forceinline__ unsigned scale_group_max(const float (&y)[8])
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// Eight codes of y at scale byte sb (255: zero codes).
+__device__ __forceinline__ uint32_t q4_encode8(const float (&y)[8], int sb)
+{
+    const float by = q4_unscale(sb);
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        z[j] = y[j] * by;
+    return sb == 255 ? 0u : e2m1x8(z);
+}
+
+// Whether some code of y, or its scale, could be another for a value `off` of y's pair
+// away (relative to the sum of the pair's magnitudes).
+__device__ __forceinline__ bool q4_near_border(const float (&y)[8], const float (&pair)[4],
+                                               unsigned amax, int sb, float off)
+{
+    const float by = q4_unscale(sb);
+    float lo[8], hi[8], most = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float z = y[j] * by, t = pair[j / 2] * (by * off);
+        lo[j] = z - t;
+        hi[j] = z + t;
+        most = fmaxf(most, t);
+    }
+    // (the group's largest is one of four lanes'; any of them may find it near)
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    const float z = __uint_as_float(amax) * by;
+    const bool scale = sb < 255 && (z + most > 6.f || (z - most <= 3.f && sb > 127 + kQ4MinExp));
+    return e2m1x8(lo) != e2m1x8(hi) || scale;
+}
+
+// A lane's scale bytes of a head, D / 32 of its four-lane groups, in one word of
+// the head's first lane.
+template <int D>
+__device__ __forceinline__ uint32_t q4_scale_word(int sb, int lane)
+{
+    uint32_t w = (uint32_t)sb << (lane / 4 * 8);
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    if constexpr (D == 128)
+        w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    return w;
+}
+
 // A block takes GROUPS / p.width tokens, p.width groups (a power of two) each.
-template <int D, bool Q8, bool EXTEND>
+// BITS: 16 (bf16 pools), 8 or 4 (codes and scales).
+template <int D, int BITS, bool EXTEND>
 __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const TokenWriteParams p)
 {
     constexpr int LANES = D / 8;             // lanes of a head vector
@@ -364,27 +504,74 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
     // bits of 24: of 4.9 M codes 4.6 lie across a tie from the 64-bit ones, 5.3 with
     // the weight in the coefficients, 7.7 in plain 32-bit operations, at the same time)
     const Eight wk8 = unpack(wk);
-    const Turn turn = turn_of(c01, c23, Q8 ? unpack(ones) : wk8);
+    const Turn turn = turn_of(c01, c23, BITS < 16 ? unpack(ones) : wk8);
+    // (tables may be scaled: the largest of the lane's factors, at least 1)
+    float turn_gain = 1.f;
+    if constexpr (BITS == 4) {
+        turn_gain = fmaxf(fmaxf(fmaxf(fabsf(c01.x), fabsf(c01.y)), fmaxf(fabsf(c01.z), fabsf(c01.w))),
+                          fmaxf(fmaxf(fabsf(c23.x), fabsf(c23.y)), fmaxf(fabsf(c23.z), fabsf(c23.w))));
+        turn_gain = fmaxf(turn_gain, 1.f);
+    }
     for (int h0 = 0; h0 < p.Hkv; h0 += kKv * width) {
 #pragma unroll
         for (int u = 0; u < kKv; ++u) {
             const int h = h0 + u * width + v0;
             const uint4 vraw = rv[u];
+            const uint4 kraw = rk[u];
             Eight x = unpack(rk[u]);
             load(rk[u], k, h + kKv * width, p.Hkv);
             load(rv[u], v, h + kKv * width, p.Hkv);
             const float f = p.k_norm != nullptr ? norm_factor<D>(x, p.norm_eps) : 1.f;
-            if constexpr (Q8) {
+            if constexpr (BITS < 16) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     x.a[i] = mul2(x.a[i], wk8.a[i]);
                     x.b[i] = mul2(x.b[i], wk8.b[i]);
                 }
             }
+            const Eight before = x;
             apply(x, turn, p.rope != nullptr);
             const bool store = live && h < p.Hkv;
             const size_t head = (size_t)slot * p.Hkv + h;
-            if constexpr (Q8) {
+            if constexpr (BITS == 4) {
+                float y[8], pair[4], v8[8];
+                values_of(x, f, y);
+                unsigned amax = scale_group_max(y);
+                int sk = q4_scale_byte(amax);
+                if (p.rope != nullptr || p.k_norm != nullptr) {
+                    // What 32-bit operations may be off by, of the pair's magnitudes: the
+                    // rotation's two roundings 2^-23, the check's one 2^-24; the norm's nine
+                    // of the sum (halved by the root), rsqrtf's two units and the product
+                    // 2^-20.7 more.
+                    const float off = turn_gain * (p.k_norm != nullptr ? 0x1.8p-20f : 0x1p-22f);
+                    pair_sizes(before, f, pair);
+                    if (__any_sync(0xffffffffu, q4_near_border(y, pair, amax, sk, off))) {
+                        key_values_in_64<D>(p.k_norm,
+                                            p.rope != nullptr && row.pos >= 0 && row.bad == 0
+                                                ? p.rope + (size_t)row.pos * D : nullptr,
+                                            p.norm_eps, kraw, y);
+                        amax = scale_group_max(y);
+                        sk = q4_scale_byte(amax);
+                    }
+                }
+                values_of(unpack(vraw), 1.f, v8);
+                const int sv = q4_scale_byte(scale_group_max(v8));
+                const uint32_t kc = q4_encode8(y, sk), vc = q4_encode8(v8, sv);
+                const uint32_t ks = q4_scale_word<D>(sk, lane), vs = q4_scale_word<D>(sv, lane);
+                if (store) {
+                    reinterpret_cast<uint32_t *>(p.k_pool)[head * LANES + lane] = kc;
+                    reinterpret_cast<uint32_t *>(p.v_pool)[head * LANES + lane] = vc;
+                    if (lane == 0) {
+                        if constexpr (D == 128) {
+                            reinterpret_cast<uint32_t *>(p.k_scale)[head] = ks;
+                            reinterpret_cast<uint32_t *>(p.v_scale)[head] = vs;
+                        } else {
+                            reinterpret_cast<uint16_t *>(p.k_scale)[head] = (uint16_t)ks;
+                            reinterpret_cast<uint16_t *>(p.v_scale)[head] = (uint16_t)vs;
+                        }
+                    }
+                }
+            } else if constexpr (BITS == 8) {
                 int sk, sv;
                 const uint2 kc = quantise<D>(x, f, sk);
                 const uint2 vc = quantise<D>(unpack(vraw), 1.f, sv);
@@ -408,7 +595,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
     }
 }
 
-template <int D, bool Q8, bool EXTEND>
+template <int D, int BITS, bool EXTEND>
 cudaError_t launch(const TokenWriteParams &params, cudaStream_t stream)
 {
     constexpr int kLanes = D / 8;
@@ -428,16 +615,22 @@ cudaError_t launch(const TokenWriteParams &params, cudaStream_t stream)
     const int threads = wide > kMinThreads ? wide : kMinThreads;
     const unsigned at_once = threads / wide;
     const unsigned blocks = ((unsigned)p.T + at_once - 1) / at_once;
-    return launch_pdl(token_write_kernel<D, Q8, EXTEND>, dim3(blocks), dim3(threads), 0, stream, p);
+    return launch_pdl(token_write_kernel<D, BITS, EXTEND>, dim3(blocks), dim3(threads), 0, stream, p);
+}
+
+template <int D, int BITS>
+cudaError_t launch_bits(const TokenWriteParams &p, cudaStream_t stream)
+{
+    return p.qo_indptr != nullptr ? launch<D, BITS, true>(p, stream)
+                                  : launch<D, BITS, false>(p, stream);
 }
 
 template <int D>
 cudaError_t launch_d(const TokenWriteParams &p, cudaStream_t stream)
 {
-    const bool q8 = p.k_scale != nullptr, extend = p.qo_indptr != nullptr;
-    if (q8)
-        return extend ? launch<D, true, true>(p, stream) : launch<D, true, false>(p, stream);
-    return extend ? launch<D, false, true>(p, stream) : launch<D, false, false>(p, stream);
+    return p.bits == 16  ? launch_bits<D, 16>(p, stream)
+           : p.bits == 8 ? launch_bits<D, 8>(p, stream)
+                         : launch_bits<D, 4>(p, stream);
 }
 
 } // namespace

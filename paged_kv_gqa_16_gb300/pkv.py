@@ -43,6 +43,7 @@ EXPORTS = (
     "pkv_prefill_workspace_bytes", "pkv_prefill_plan", "paged_kv_append_norm",
     "paged_kv_extend_norm", "paged_kv_append_q8", "paged_kv_extend_q8", "paged_kv_read_q8",
     "paged_decode_attn_q8", "paged_decode_attn_q8_planned", "paged_decode_plan_q8",
+    "paged_kv_append_q4", "paged_kv_extend_q4", "paged_kv_read_q4",
 )
 
 
@@ -129,6 +130,9 @@ def lib():
             "paged_kv_read_q8": (I, [DP, P, P, P, P, P, P, P, P, P, P, P]),
             "paged_decode_attn_q8": (I, [DP, P, P, P, P, P, P, P, P, I, P, Z, P, P]),
             "paged_decode_attn_q8_planned": (I, [DP, P, P, P, P, P, P, P, P, I, P, Z, P, P]),
+            "paged_kv_append_q4": (I, [DP, TP, P, P, P, P, P, P, P, P, P]),
+            "paged_kv_extend_q4": (I, [DP, TP, P, I, P, P, P, P, P, P, P, P, P]),
+            "paged_kv_read_q4": (I, [DP, P, P, P, P, P, P, P, P, P, P, P]),
             "pkv_testing_set_handoff_wait_ns": (I, [ctypes.c_ulonglong]),
             "pkv_status_str": (ctypes.c_char_p, [I]),
             "pkv_version": (I, []),
@@ -214,6 +218,23 @@ def _q8_ptrs(k, v, ks, vs):
     if _bf16 is None:
         _load_types()
     return _q8_ptr(k, _codes), _q8_ptr(v, _codes), _q8_ptr(ks, _scales), _q8_ptr(vs, _scales)
+
+
+def _q4_ptr(x, at_least: int) -> Optional[int]:
+    if x is None or x.__class__ is int:
+        return x
+    if x.element_size() == 1 and x.numel() >= at_least and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError("a 4-bit cache has contiguous byte tensors, codes [num_pages, page_size, Hkv, D / 2] and "
+                     f"scales [num_pages, page_size, Hkv, D / 32]: got {x.dtype} {tuple(x.shape)}")
+
+
+def _q4_ptrs(d: Dims, k, v, ks, vs):
+    """The pointers of a 4-bit cache's codes and scales (their sizes are checked: an
+    8-bit cache has the same types)."""
+    heads = d.num_pages * d.page_size * d.Hkv
+    codes, scales = heads * (d.D // 2), heads * (d.D // 32)
+    return _q4_ptr(k, codes), _q4_ptr(v, codes), _q4_ptr(ks, scales), _q4_ptr(vs, scales)
 
 
 def _find_current_stream():
@@ -584,6 +605,36 @@ def paged_decode_attn_q8_planned(d: Dims, q, k_codes, v_codes, k_scale, v_scale,
         ctypes.byref(d), _bf16_ptr(q), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
         ws_bytes, _bf16_ptr(out), _stream(stream)))
+
+
+# ---- the 4-bit cache ----------------------------------------------------------
+def paged_kv_append_q4(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, kv_indices,
+                       kv_indptr, seq_lens, status=None, stream=None) -> None:
+    """paged_kv_append_norm into a 4-bit cache: codes [num_pages, page_size, Hkv,
+    D / 2] (uint8, two e2m1 to a byte, the first in the low half) and scales
+    [num_pages, page_size, Hkv, D / 32] (uint8 or torch.float8_e8m0fnu)."""
+    _token_count(d, t, per_row=True)
+    _check("paged_kv_append_q4", lib().paged_kv_append_q4(
+        ctypes.byref(d), ctypes.byref(t), *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
+
+
+def paged_kv_extend_q4(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale, v_scale,
+                       kv_indices, kv_indptr, seq_lens, status=None, stream=None) -> None:
+    """paged_kv_append_q4 for ragged chunks of new tokens."""
+    _check("paged_kv_extend_q4", lib().paged_kv_extend_q4(
+        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
+        *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
+        _ptr(seq_lens), _ptr(status), _stream(stream)))
+
+
+def paged_kv_read_q4(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
+                     seq_lens, k_out, v_out, status=None, stream=None) -> None:
+    """paged_kv_read_q8 of a 4-bit cache."""
+    _check("paged_kv_read_q4", lib().paged_kv_read_q4(
+        ctypes.byref(d), *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out), _bf16_ptr(v_out),
+        _ptr(status), _stream(stream)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
