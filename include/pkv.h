@@ -653,6 +653,44 @@ pkv_status paged_kv_read_q4(const pkv_dims *dims, const void *k_codes, const voi
                             const int32_t *seq_lens, void *k_out, void *v_out,
                             uint32_t *status, pkv_stream_t stream);
 
+/* paged_decode_attn over a 4-bit cache: q and out bf16 [B, Hq, D], fp32 softmax,
+ * num_splits, workspace and flags as for that call, window and sinks as for
+ * paged_decode_attn_window (window 0: all tokens).  Scales as the writes choose them,
+ * or any in [127 - 40, 127 + 40]; the output of a row holding others is undefined,
+ * but that scale 255 with zero codes, as written for infinities and NaN, reaches all
+ * outputs of the query heads that read it.  A token's weight, with its value's scale,
+ * is rounded to 11 significant bits or to 2^-31 of the row's largest, whichever is
+ * more; a query element under 2^-32 of its head's largest is off by up to 2^-40 of
+ * that.  Rows short by the tokens that their last one sees (256 KB of K and V in a
+ * group of kv heads, 512 KB with rows x groups for half the SMs) are not split
+ * whatever num_splits is: one kernel.  Otherwise one persistent kernel plus, when
+ * num_splits > 1, the piece combine; a batch of more than 1024 rows x kv-head groups
+ * (a group: 8, 4, 2 or 1 kv heads, the most that divide Hkv) takes several such
+ * pairs, one after the other.  PKV_ERR_UNSUPPORTED: Hkv of more than 1024 groups, or
+ * seen tokens x groups or num_pages x page_size past 2^31.  The workspace's plan of
+ * a bf16 decode stays as it is. */
+pkv_status paged_decode_attn_q4(const pkv_dims *dims, const void *q, const void *k_codes,
+                                const void *v_codes, const void *k_scale, const void *v_scale,
+                                const int32_t *kv_indices, const int32_t *kv_indptr,
+                                const int32_t *seq_lens, int window, int sinks, int num_splits,
+                                void *workspace, size_t ws_bytes, void *out, pkv_stream_t stream);
+
+/* ---- sliding windows --------------------------------------------------------- */
+
+/* paged_decode_attn in which a row's query, its token L - 1 (L = seq_lens[b]), sees
+ * the last `window` of the row's tokens and its first `sinks`: token t if
+ * t >= L - window or t < sinks.  A row of at most window + sinks tokens is seen
+ * whole; window 0 stands for no window.  Pages without a seen token are not read,
+ * and their entries of kv_indices may hold anything (a serving loop frees them).
+ * Other arguments, results, errors and flags are those of paged_decode_attn;
+ * rows and batches are split as by paged_decode_attn_q4, and PKV_ERR_UNSUPPORTED is
+ * for the same sizes. */
+pkv_status paged_decode_attn_window(const pkv_dims *dims, const void *q, const void *k_pool,
+                                    const void *v_pool, const int32_t *kv_indices,
+                                    const int32_t *kv_indptr, const int32_t *seq_lens, int window,
+                                    int sinks, int num_splits, void *workspace, size_t ws_bytes,
+                                    void *out, pkv_stream_t stream);
+
 /* ---- for callers that cannot allocate ------------------------------------ */
 
 /* Size of the library-held scratch used by paged_decode_attn_noalloc. */

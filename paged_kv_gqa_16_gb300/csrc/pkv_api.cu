@@ -1190,17 +1190,24 @@ static int q8_rows(const pkv_dims *dims, int hpc)
     return (int)(by_weight < by_rows ? by_weight : by_rows);
 }
 
+// The current device's SMs (1 where it does not say).
+static int device_sms()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        sms < 1) {
+        (void)cudaGetLastError();
+        sms = 1;
+    }
+    return sms;
+}
+
 // Whether the decode over the 8-bit cache takes whole rows (kQ8WholeBytes), and
 // the device's SMs.
 static bool q8_whole(const pkv_dims *dims, int hpc, int *sms)
 {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        *sms < 1) {
-        (void)cudaGetLastError();
-        *sms = 1;
-    }
+    *sms = device_sms();
     const long long rows = (long long)dims->B * (dims->Hkv / hpc);
     const long long bytes = (long long)dims->max_seq_len * hpc * dims->D * 2;
     return bytes <= (2 * rows >= *sms ? 2 : 1) * pkv::kQ8WholeBytes;
@@ -1284,6 +1291,124 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
             return st;
     }
     return PKV_OK;
+}
+
+// Rows x kv-head groups whose rows the stream decode takes whole, by the bytes of
+// K and V that a row's last token sees (kStreamWholeBytes).
+static bool stream_whole(const pkv_dims *dims, int hpc, int bits, int most_seen, int sms)
+{
+    const long long rows = (long long)dims->B * (dims->Hkv / hpc);
+    const long long head = bits == 4 ? dims->D / 2 + dims->D / 32 : dims->D * 2;
+    return (long long)most_seen * hpc * head * 2 <=
+           (2 * rows >= sms ? 2 : 1) * pkv::kStreamWholeBytes;
+}
+
+// Decode over a 4-bit cache (bits 4) or bf16 pools; window 0: all tokens.
+static pkv_status decode_stream(const pkv_dims *dims, int bits, const void *q, const void *k,
+                                const void *v, const void *k_scale, const void *v_scale,
+                                const int32_t *kv_indices, const int32_t *kv_indptr,
+                                const int32_t *seq_lens, int window, int sinks, int num_splits,
+                                void *workspace, size_t ws_bytes, void *out, pkv_stream_t stream)
+{
+    pkv_status st = check_decode_args(dims, q, k, v, kv_indices, kv_indptr, seq_lens, num_splits,
+                                      workspace, ws_bytes, out, true);
+    if (st != PKV_OK)
+        return st;
+    if (window < 0 || sinks < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (dims->B == 0)
+        return PKV_OK;
+    if (bits == 4 && (k_scale == nullptr || v_scale == nullptr || !aligned(k_scale, 16) ||
+                      !aligned(v_scale, 16)))
+        return PKV_ERR_INVALID_ARG;
+    // the kernel counts a pool's token slots in 31 bits
+    if ((long long)dims->num_pages * dims->page_size >= (1ll << 31))
+        return PKV_ERR_UNSUPPORTED;
+    const Layout L = layout_for(dims, num_splits);
+    const int groups = dims->Hkv / L.hpc;
+    // (a window of at least max_seq_len tokens with its sinks is none)
+    const long long limit = (long long)window + sinks;
+    const bool windowed = window > 0 && limit < dims->max_seq_len;
+    const int most_seen = windowed ? (int)limit : dims->max_seq_len;
+    int sms = device_sms();
+    // Rows of one launch: their prefix sums in shared memory, their weights in 31
+    // bits; short rows are not split, a block takes whole ones.
+    const bool whole = stream_whole(dims, L.hpc, bits, most_seen, sms);
+    const long long cost = bits == 4 ? pkv::kQ4RowCost : pkv::kWindowRowCost;
+    const long long by_weight = ((1ll << 31) - 1) / (most_seen + cost) / groups;
+    const long long by_rows = (long long)pkv::kQ8MaxRows * (whole ? sms : 1) / groups;
+    const long long rows = whole || by_rows < by_weight ? by_rows : by_weight;
+    if (rows < 1)
+        return PKV_ERR_UNSUPPORTED;
+    const int most = rows < dims->B ? (int)rows : dims->B;
+    char *ws = static_cast<char *>(workspace);
+    for (int b0 = 0; b0 < dims->B; b0 += most) {
+        pkv_dims d = *dims;
+        d.B = dims->B - b0 < most ? dims->B - b0 : most;
+        pkv::StreamParams sp{};
+        sp.f = persistent_params(&d, L, ws, kv_indices, kv_indptr + b0, seq_lens + b0, true);
+        sp.bits = bits;
+        sp.most_seen = most_seen;
+        sp.sinks = windowed ? sinks : 0;
+        pkv::FusedParams &p = sp.f;
+        p.Bv = d.B * groups;
+        p.row_cost = (int)cost;
+        p.q = static_cast<const __nv_bfloat16 *>(q) + (size_t)b0 * d.Hq * d.D;
+        p.out = static_cast<__nv_bfloat16 *>(out) + (size_t)b0 * d.Hq * d.D;
+        p.k_codes = static_cast<const uint8_t *>(k);
+        p.v_codes = static_cast<const uint8_t *>(v);
+        p.k_scale = static_cast<const uint8_t *>(k_scale);
+        p.v_scale = static_cast<const uint8_t *>(v_scale);
+        const size_t pieces = ((size_t)num_splits + p.Bv) * L.HQV;
+        p.ml_part = reinterpret_cast<float *>(ws + L.piece_ml_off);
+        p.o_part = reinterpret_cast<float *>(ws + L.piece_ml_off +
+                                             round_up(pieces * 2 * sizeof(float), 256));
+        p.whole_rows = whole ? 1 : 0;
+        p.scale_log2 = (float)((double)dims->scale * 1.4426950408889634);
+        const int grid = !whole ? num_splits : p.Bv < sms ? p.Bv : sms;
+        st = launch_status(pkv::launch_stream_decode(sp, d.D, grid, (cudaStream_t)stream));
+        if (st != PKV_OK)
+            return st;
+        if (whole || num_splits == 1)
+            continue;
+        pkv::PieceCombineParams c{};
+        c.o_part = p.o_part;
+        c.ml_part = p.ml_part;
+        c.row_info = p.row_info;
+        c.out = p.out;
+        c.B = d.B;
+        c.Bv = p.Bv;
+        c.Hq = d.Hq;
+        c.HQV = L.HQV;
+        c.grid = num_splits;
+        c.page_size = d.page_size;
+        c.row_cost = p.row_cost;
+        st = launch_status(
+            pkv::launch_piece_combine(c, d.D, num_splits, (cudaStream_t)stream));
+        if (st != PKV_OK)
+            return st;
+    }
+    return PKV_OK;
+}
+
+pkv_status paged_decode_attn_q4(const pkv_dims *dims, const void *q, const void *k_codes,
+                                const void *v_codes, const void *k_scale, const void *v_scale,
+                                const int32_t *kv_indices, const int32_t *kv_indptr,
+                                const int32_t *seq_lens, int window, int sinks, int num_splits,
+                                void *workspace, size_t ws_bytes, void *out, pkv_stream_t stream)
+{
+    return decode_stream(dims, 4, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
+                         seq_lens, window, sinks, num_splits, workspace, ws_bytes, out, stream);
+}
+
+pkv_status paged_decode_attn_window(const pkv_dims *dims, const void *q, const void *k_pool,
+                                    const void *v_pool, const int32_t *kv_indices,
+                                    const int32_t *kv_indptr, const int32_t *seq_lens, int window,
+                                    int sinks, int num_splits, void *workspace, size_t ws_bytes,
+                                    void *out, pkv_stream_t stream)
+{
+    return decode_stream(dims, 16, q, k_pool, v_pool, nullptr, nullptr, kv_indices, kv_indptr,
+                         seq_lens, window, sinks, num_splits, workspace, ws_bytes, out, stream);
 }
 
 pkv_status paged_decode_attn_q8(const pkv_dims *dims, const void *q, const void *k_codes,

@@ -290,6 +290,20 @@ constexpr long long kQ8WholeBytes = 256 << 10;
 // whose ring of stages needs the room of more prefix sums.
 constexpr int kQ8MaxRows = 1024;
 
+// Decode over the 4-bit cache or through a window (pkv_stream_decode.cu).  A row's
+// last token sees its first `sinks` tokens and the last most_seen - sinks (a row of
+// at most most_seen: all); no window: most_seen is max_seq_len's bound and no row's
+// tokens are skipped.  f.k_codes and f.v_codes are the pools of either kind.
+constexpr int kQ4RowCost = 64;
+constexpr int kWindowRowCost = 32;
+constexpr long long kStreamWholeBytes = 256 << 10;
+struct StreamParams {
+    FusedParams f;
+    int bits;              // 16 (bf16 pools) or 4 (codes and scales)
+    int most_seen;
+    int sinks;
+};
+
 // Threads of a plan block.
 constexpr int kPlanThreads = 256;
 // int32 words of the plan for Bv virtual rows and a grid of `grid` blocks.
@@ -329,6 +343,7 @@ cudaError_t launch_token_write(const TokenWriteParams &p, int D, cudaStream_t st
 cudaError_t launch_read_codes(const ReadCodesParams &p, int D, cudaStream_t stream);
 // the decode over an 8-bit cache; p.k_codes ... p.v_scale in place of the pools
 cudaError_t launch_decode_q8(const FusedParams &p, int D, int grid, cudaStream_t stream);
+cudaError_t launch_stream_decode(const StreamParams &p, int D, int grid, cudaStream_t stream);
 cudaError_t launch_advance(const AdvanceParams &p, cudaStream_t stream);
 // one persistent block per SM over the units (pairs of query tiles x B x Hkv)
 // The prefill's list for a launch (host only): units of tile pairs, their

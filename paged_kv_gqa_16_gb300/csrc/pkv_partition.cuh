@@ -67,16 +67,16 @@ __device__ __forceinline__ int checked_row_len(const FusedParams &p, int r, unsi
 
 // prefix[0..n] of n rows' partition weights (a non-empty row weighs its tokens
 // plus row_cost), computed by every thread of the block; row i of them is
-// virtual row row_of(i); report: OR the flags of the first B virtual rows into
-// the status word.
-template <typename RowOf>
+// virtual row row_of(i), its tokens the seen(L) that a call looks at; report: OR
+// the flags of the first B virtual rows into the status word.
+template <typename RowOf, typename Seen>
 __device__ __forceinline__ void row_prefix(const FusedParams &p, int *prefix, int n, RowOf row_of,
-                                           bool report)
+                                           Seen seen, bool report)
 {
     const int Bv = n, lane = threadIdx.x & 31;
     for (int r = threadIdx.x; r < Bv; r += blockDim.x) {
         unsigned bad = 0;
-        const int L = checked_row_len(p, row_of(r), bad);
+        const int L = seen(checked_row_len(p, row_of(r), bad));
         if (bad && report && row_of(r) < p.B)
             atomicOr(p.status, bad);
         prefix[r + 1] = L > 0 ? L + p.row_cost : 0;
@@ -102,6 +102,14 @@ __device__ __forceinline__ void row_prefix(const FusedParams &p, int *prefix, in
             prefix[0] = 0;
     }
     __syncthreads();
+}
+
+// All tokens of each row.
+template <typename RowOf>
+__device__ __forceinline__ void row_prefix(const FusedParams &p, int *prefix, int n, RowOf row_of,
+                                           bool report)
+{
+    row_prefix(p, prefix, n, row_of, [](int L) { return L; }, report);
 }
 
 // The same of all virtual rows.

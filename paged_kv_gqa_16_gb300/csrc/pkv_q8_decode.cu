@@ -61,6 +61,7 @@
 // 8.7 us, latency (2.8 the combine).
 #include <cmath>
 
+#include "pkv_decode.cuh"
 #include "pkv_partition.cuh"
 #include "pkv_q8.cuh"
 
@@ -109,61 +110,6 @@ struct Q8Cfg {
     static_assert(kStageBytes % 1024 == 0, "swizzled rows");
     static_assert(kJoinBytes % 16 == 0, "alignment");
 };
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two floats to f16x2, the first in the low half.
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ __forceinline__ float exp2_ftz(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
-{
-    uint32_t d;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
-// This thread's earlier cp.async copies arrive on `bar` when they have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
-// 16 bytes global -> shared.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint64_t policy)
-{
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(src), "l"(policy)
-                 : "memory");
-}
-
-// Four or eight bytes global -> shared, of which the first `bytes` are read
-// (the others are zero).
-template <int SIZE>
-__device__ __forceinline__ void cp_async(void *dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src),
-                 "n"(SIZE), "r"(bytes)
-                 : "memory");
-}
 
 template <int D, int HPC, int NT>
 __global__ void __launch_bounds__(Q8Cfg<D, HPC, NT>::kThreads, 1)

@@ -43,7 +43,8 @@ EXPORTS = (
     "pkv_prefill_workspace_bytes", "pkv_prefill_plan", "paged_kv_append_norm",
     "paged_kv_extend_norm", "paged_kv_append_q8", "paged_kv_extend_q8", "paged_kv_read_q8",
     "paged_decode_attn_q8", "paged_decode_attn_q8_planned", "paged_decode_plan_q8",
-    "paged_kv_append_q4", "paged_kv_extend_q4", "paged_kv_read_q4",
+    "paged_kv_append_q4", "paged_kv_extend_q4", "paged_kv_read_q4", "paged_decode_attn_q4",
+    "paged_decode_attn_window",
 )
 
 
@@ -133,6 +134,8 @@ def lib():
             "paged_kv_append_q4": (I, [DP, TP, P, P, P, P, P, P, P, P, P]),
             "paged_kv_extend_q4": (I, [DP, TP, P, I, P, P, P, P, P, P, P, P, P]),
             "paged_kv_read_q4": (I, [DP, P, P, P, P, P, P, P, P, P, P, P]),
+            "paged_decode_attn_q4": (I, [DP, P, P, P, P, P, P, P, P, I, I, I, P, Z, P, P]),
+            "paged_decode_attn_window": (I, [DP, P, P, P, P, P, P, I, I, I, P, Z, P, P]),
             "pkv_testing_set_handoff_wait_ns": (I, [ctypes.c_ulonglong]),
             "pkv_status_str": (ctypes.c_char_p, [I]),
             "pkv_version": (I, []),
@@ -635,6 +638,31 @@ def paged_kv_read_q4(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv
         ctypes.byref(d), *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out), _bf16_ptr(v_out),
         _ptr(status), _stream(stream)))
+
+
+def paged_decode_attn_q4(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
+                         seq_lens, num_splits: int, workspace, out, window: int = 0,
+                         sinks: int = 0, stream=None) -> None:
+    """paged_decode_attn over a 4-bit cache; with a window, over each row's last
+    `window` tokens and its first `sinks`."""
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check("paged_decode_attn_q4", lib().paged_decode_attn_q4(
+        ctypes.byref(d), _bf16_ptr(q), *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits,
+        _ptr(workspace), ws_bytes, _bf16_ptr(out), _stream(stream)))
+
+
+# ---- sliding windows ----------------------------------------------------------
+def paged_decode_attn_window(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, seq_lens,
+                             window: int, sinks: int, num_splits: int, workspace, out,
+                             stream=None) -> None:
+    """paged_decode_attn in which a row's query sees the last `window` of its
+    seq_lens[b] tokens and the first `sinks` (window 0: all)."""
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check("paged_decode_attn_window", lib().paged_decode_attn_window(
+        ctypes.byref(d), _bf16_ptr(q), _bf16_ptr(k_pool), _bf16_ptr(v_pool), _ptr(kv_indices),
+        _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits, _ptr(workspace), ws_bytes,
+        _bf16_ptr(out), _stream(stream)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -81,3 +81,30 @@ def test_tensors_of_another_cache_are_refused():
                 [codes.to(torch.bfloat16), codes, scale, scale], [codes, codes.transpose(1, 2), scale, scale]):
         with pytest.raises(ValueError):
             pkv._q4_ptrs(d, *bad)
+
+
+@pytest.mark.parametrize("name", ["paged_decode_attn_q4", "paged_decode_attn_window"])
+def test_decode_refusals(name):
+    d = _d()
+    need = pkv.workspace_bytes(d, 8)
+    q4 = name.endswith("q4")
+
+    def call(d=d, splits=8, ws_bytes=need, window=64, sinks=4, **kw):
+        a = dict(q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, ind=FAKE, ptr=FAKE, sl=FAKE)
+        if not q4:
+            del a["ks"], a["vs"]
+        a.update({k: v for k, v in kw.items() if k in a})
+        return getattr(pkv.lib(), name)(ctypes.byref(d), *a.values(), window, sinks, splits, kw.get("ws", FAKE),
+                                        ws_bytes, kw.get("out", FAKE), None)
+
+    for field in ("q", "kc", "vc", "ind", "ptr", "sl", "ws", "out") + (("ks", "vs") if q4 else ()):
+        assert call(**{field: None}) == BAD, field
+        assert call(**{field: FAKE + 2}) == BAD, field
+    assert call(ws=FAKE + 16) == BAD and call(q=FAKE + 8) == BAD
+    assert call(splits=0) == BAD and call(splits=70000) == BAD
+    assert call(window=-1) == BAD and call(sinks=-1) == BAD
+    assert call(ws_bytes=need - 1) == pkv.PKV_ERR_WORKSPACE_TOO_SMALL
+    assert call(d=_d(D=96)) == UNSUP and call(d=_d(Hq=8 * 17)) == UNSUP
+    assert call(d=_d(B=0)) == pkv.PKV_OK
+    big = _d(num_pages=1 << 28)
+    assert call(d=big, ws_bytes=pkv.workspace_bytes(big, 8)) == UNSUP
