@@ -691,6 +691,22 @@ pkv_status paged_decode_attn_window(const pkv_dims *dims, const void *q, const v
                                     int sinks, int num_splits, void *workspace, size_t ws_bytes,
                                     void *out, pkv_stream_t stream);
 
+/* paged_prefill_attn_ws (or, with a NULL workspace, paged_prefill_attn) in which the
+ * query at position p sees the last `window` keys up to its own and the row's first
+ * `sinks`: key t <= p if t > p - window or t < sinks; window 0 stands for no window.
+ * Pages without a key that a query of the row's chunk sees are not read, and their
+ * entries of kv_indices may hold anything.  An infinite or NaN value that some
+ * queries of a tile see reaches the tile's others too, as one past a query's
+ * position does in paged_prefill_attn.  Other arguments, results, errors and flags
+ * are those calls'. */
+pkv_status paged_prefill_attn_window(const pkv_dims *dims, const void *q,
+                                     const int32_t *qo_indptr, int total_q, int max_q_len,
+                                     const void *k_pool, const void *v_pool,
+                                     const int32_t *kv_indices, const int32_t *kv_indptr,
+                                     const int32_t *seq_lens, int window, int sinks,
+                                     void *workspace, size_t ws_bytes, void *out,
+                                     uint32_t *status, pkv_stream_t stream);
+
 /* ---- for callers that cannot allocate ------------------------------------ */
 
 /* Size of the library-held scratch used by paged_decode_attn_noalloc. */

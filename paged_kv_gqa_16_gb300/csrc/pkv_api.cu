@@ -858,13 +858,13 @@ namespace {
 pkv_status prefill_impl(const pkv_dims *dims, const void *q, const int32_t *qo_indptr,
                         int total_q, int max_q_len, const void *k_pool, const void *v_pool,
                         const int32_t *kv_indices, const int32_t *kv_indptr,
-                        const int32_t *seq_lens, void *workspace, size_t ws_bytes, void *out,
-                        uint32_t *status, pkv_stream_t stream)
+                        const int32_t *seq_lens, int window, int sinks, void *workspace,
+                        size_t ws_bytes, void *out, uint32_t *status, pkv_stream_t stream)
 {
     pkv_status st = check_dims(dims);
     if (st != PKV_OK)
         return st;
-    if (total_q < 0 || max_q_len < 0 || !(dims->scale > 0.f))
+    if (total_q < 0 || max_q_len < 0 || !(dims->scale > 0.f) || window < 0 || sinks < 0)
         return PKV_ERR_INVALID_ARG;
     if (workspace != nullptr && !aligned(workspace, 256))
         return PKV_ERR_INVALID_ARG;
@@ -905,6 +905,9 @@ pkv_status prefill_impl(const pkv_dims *dims, const void *q, const int32_t *qo_i
     p.max_seq_len = dims->max_seq_len;
     p.total_q = total_q;
     p.tq = 128 / p.n_rep;
+    // (a window that no row reaches past is none)
+    p.window = window > 0 && (long long)window + sinks < dims->max_seq_len ? window : 0;
+    p.sinks = sinks;
     p.scale_log2 = (float)((double)dims->scale * 1.4426950408889634);
     return launch_status(pkv::launch_prefill(p, dims->D, max_q_len, workspace,
                                              workspace != nullptr ? ws_bytes : 0,
@@ -920,7 +923,7 @@ pkv_status paged_prefill_attn(const pkv_dims *dims, const void *q, const int32_t
                               pkv_stream_t stream)
 {
     return prefill_impl(dims, q, qo_indptr, total_q, max_q_len, k_pool, v_pool, kv_indices,
-                        kv_indptr, seq_lens, nullptr, 0, out, status, stream);
+                        kv_indptr, seq_lens, 0, 0, nullptr, 0, out, status, stream);
 }
 
 pkv_status paged_prefill_attn_ws(const pkv_dims *dims, const void *q, const int32_t *qo_indptr,
@@ -931,7 +934,20 @@ pkv_status paged_prefill_attn_ws(const pkv_dims *dims, const void *q, const int3
                                  pkv_stream_t stream)
 {
     return prefill_impl(dims, q, qo_indptr, total_q, max_q_len, k_pool, v_pool, kv_indices,
-                        kv_indptr, seq_lens, workspace, ws_bytes, out, status, stream);
+                        kv_indptr, seq_lens, 0, 0, workspace, ws_bytes, out, status, stream);
+}
+
+pkv_status paged_prefill_attn_window(const pkv_dims *dims, const void *q,
+                                     const int32_t *qo_indptr, int total_q, int max_q_len,
+                                     const void *k_pool, const void *v_pool,
+                                     const int32_t *kv_indices, const int32_t *kv_indptr,
+                                     const int32_t *seq_lens, int window, int sinks,
+                                     void *workspace, size_t ws_bytes, void *out,
+                                     uint32_t *status, pkv_stream_t stream)
+{
+    return prefill_impl(dims, q, qo_indptr, total_q, max_q_len, k_pool, v_pool, kv_indices,
+                        kv_indptr, seq_lens, window, sinks, workspace, ws_bytes, out, status,
+                        stream);
 }
 
 pkv_status paged_decode_partials(const pkv_dims *dims, const void *q, const void *k_pool,

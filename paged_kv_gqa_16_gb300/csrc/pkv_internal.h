@@ -174,6 +174,10 @@ struct PrefillParams {
     int B, Hq, Hkv, n_rep, page_size, ps_shift, num_pages, num_indices, max_seq_len, total_q;
     int tq;                        // query tokens per block: 128 / n_rep
     float scale_log2;
+    // a query sees the last `window` keys up to its own and the first `sinks`
+    // (window 0: all keys up to its own)
+    int window;
+    int sinks;
     // the pools as 3-D tiled tensors {D, Hkv, pages x page_size} with a box of
     // {64, 1, tma_rows} and 128-byte swizzle (use_tma != 0; set by
     // launch_prefill when the page size is a power of two >= 8)

@@ -34,6 +34,11 @@
 //   - tile A's products are issued by one thread and tile B's by another,
 //     taking turns one run at a time, so each makes its waits and commits
 //     while the other's run goes out.
+// With a window (paged_prefill_attn_window) query p sees keys p - window + 1 .. p
+// and the first `sinks`: a unit's list of key blocks is then the blocks of the
+// sinks and those from its first query's window on, the blocks between are never
+// read, keys that no query of the unit sees are zeroed (their page is not read
+// either), and the softmax masks the rest of a row's unseen keys.
 // With a workspace (paged_prefill_attn_ws), a list whose last round would
 // leave at least half the SMs idle cuts that round's units along their key
 // blocks (the split-KV of the decode, applied to prefill): each part stores
@@ -400,6 +405,28 @@ struct PrefillUnit {
     bool table_ok;
 };
 
+// A unit's keys under a window: keys in [sinks, low) are seen by none of its
+// queries; entry i of its list of key blocks is block i, from `first` on i + gap.
+struct UnitWindow {
+    int low, first, gap;
+    __device__ __forceinline__ int block(int i) const { return i < first ? i : i + gap; }
+    // whether each of n keys from key0 on is seen by some query
+    __device__ __forceinline__ bool whole(int key0, int n, int sinks) const
+    {
+        return key0 >= low || key0 + n <= sinks;
+    }
+};
+
+__device__ __forceinline__ UnitWindow unit_window(const PrefillParams &p, int L, int q_len, int tA,
+                                                  int tB)
+{
+    UnitWindow u;
+    u.low = max(0, L - q_len + max(tA, tA < 0 ? tB : 0) * p.tq - p.window + 1);
+    u.first = (min(p.sinks, u.low) + 127) / 128;
+    u.gap = max(0, u.low / 128 - u.first);
+    return u;
+}
+
 // Wait for phase `parity` of `bar`; false if the time limit ran out or
 // another role aborted.  The abort flag is read only once the phase is not
 // already complete: a role that fails stops producing, so every role's next
@@ -485,6 +512,7 @@ __device__ __forceinline__ void store_rows_warp(__nv_bfloat16 *dst, const float 
 // groups one after another and each group pair-major (its rows' largest
 // pairs first); false when the unit has no work: a pair past its row's
 // chunk, or a refused row.  flag: report refusals in the status.
+template <bool kWindow>
 __device__ __forceinline__ bool prefill_whole_unit(const PrefillParams &p, int u, PrefillUnit &w,
                                                    bool flag)
 {
@@ -524,6 +552,8 @@ __device__ __forceinline__ bool prefill_whole_unit(const PrefillParams &p, int u
     w.tA = w.tB - 1;
     w.kv_end = w.L - w.q_len + min(w.q_len, (w.tB + 1) * p.tq);
     w.n_kb = (w.kv_end + 127) / 128;
+    if constexpr (kWindow)
+        w.n_kb -= unit_window(p, w.L, w.q_len, w.tA, w.tB).gap;
     w.kb0 = 0;
     w.part_id = -1;
     w.pg0 = k0;
@@ -540,13 +570,13 @@ __device__ __forceinline__ bool prefill_whole_unit(const PrefillParams &p, int u
 // np = min(p.split, n / kPrefillMinPartBlocks) parts (at least one) takes
 // blocks [k n / np, (k + 1) n / np); false when the entry has no work (also
 // a part past its unit's share).
-template <bool kSplit>
+template <bool kSplit, bool kWindow>
 __device__ __forceinline__ bool prefill_unit(const PrefillParams &p, int u, PrefillUnit &w,
                                              bool flag)
 {
     if (kSplit && u >= p.split_base) {
         const int slot = u - p.split_base, part = slot % p.split;
-        if (!prefill_whole_unit(p, p.split_base + slot / p.split, w, flag && part == 0))
+        if (!prefill_whole_unit<kWindow>(p, p.split_base + slot / p.split, w, flag && part == 0))
             return false;
         const int np = max(1, min(p.split, w.n_kb / kPrefillMinPartBlocks));
         if (part >= np)
@@ -558,7 +588,7 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams &p, int u, Pref
             w.part_id = slot << 9 | np << 4 | part;
         return true;
     }
-    return prefill_whole_unit(p, u, w, flag);
+    return prefill_whole_unit<kWindow>(p, u, w, flag);
 }
 
 // A unit as a ring record: [0] has work, then its fields.
@@ -604,7 +634,8 @@ __device__ __forceinline__ bool rec_to_unit(const int *rec, PrefillUnit &w)
 // loads and first products.
 // kSplit: the list ends in a key split's parts (p.split > 1); without one the
 // kernel has no trace of it (every entry a whole unit from key 0).
-template <int D, bool kSplit>
+// kWindow: queries see a window and the sinks.
+template <int D, bool kSplit, bool kWindow>
 __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillParams p)
 {
@@ -726,7 +757,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                     // the K warp looks the unit up (reporting refusals once)
                     // and publishes it for the other roles
                     const int u = unit_index(r);
-                    have = u < n_units && prefill_unit<kSplit>(p, u, w, lane == 0);
+                    have = u < n_units && prefill_unit<kSplit, kWindow>(p, u, w, lane == 0);
                     if (lane == 0) {
                         const bool free_slot =
                             r < C::kRecs ||
@@ -795,6 +826,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 }
                 if (is_v)
                     ++qit;
+                UnitWindow uw;
+                if constexpr (kWindow)
+                    uw = unit_window(p, w.L, w.q_len, w.tA, w.tB);
                 for (int j = 0; j < w.n_kb; ++j) {
                     const int slot = kb % ns;
                     if (kb >= ns) {
@@ -806,22 +840,35 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                     if (*abort_flag)
                         break;
                     const uint32_t dst = ring + slot * C::kKVBytes;
-                    const int key0 = (w.kb0 + j) * C::kKeys;
+                    const int key0 =
+                        (kWindow ? uw.block(w.kb0 + j) : w.kb0 + j) * C::kKeys;
                     const int nkeys = min(C::kKeys, w.kv_end - key0);
+                    const bool seen_whole = !kWindow || uw.whole(key0, nkeys, p.sinks);
                     // K rows past kv_end are masked out of S whatever they hold,
                     // so a K block loads whole boxes; V rows past it meet P = 0 and
                     // must be finite, so a partial V block is copied with zero fill
-                    if (p.use_tma && (!is_v || nkeys == C::kKeys)) {
+                    // (and so is one with keys that no query of the unit sees; of K,
+                    // boxes of such keys alone are left out)
+                    if (p.use_tma && (!is_v || (nkeys == C::kKeys && seen_whole))) {
                         const int R = p.tma_rows;
-                        const int nbox = (nkeys + R - 1) / R;
+                        const int nbox = (nkeys + R - 1) / R;      // at most 16
+                        int boxes = nbox;
+                        auto box_seen = [&](int tok) {
+                            return seen_whole || tok < p.sinks || tok + R > uw.low;
+                        };
+                        if constexpr (kWindow)
+                            boxes = __popc(__ballot_sync(
+                                kAllTc, lane < nbox && box_seen(key0 + lane * R)));
                         if (lane == 0)
                             mbar_arrive_expect_tx(&full[slot],
-                                                  (uint32_t)(nbox * (D / 64) * R * 128));
+                                                  (uint32_t)(boxes * (D / 64) * R * 128));
                         else
                             mbar_arrive(&full[slot]);
                         __syncwarp();
                         for (int bx = lane; bx < nbox; bx += 32) {
                             const int tok = key0 + bx * R;
+                            if (kWindow && !box_seen(tok))
+                                continue;
                             const int pi = tok >> p.ps_shift;
                             int page = w.table_ok ? __ldg(p.kv_indices + w.pg0 + pi) : 0;
                             if (page < 0 || page >= p.num_pages) {
@@ -841,7 +888,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                         for (int kg = 0; kg < C::kKeys / 8; ++kg) {
                             const int tok = key0 + kg * 8 + kl;
                             offs[kg] = 0;
-                            if (tok < w.kv_end) {
+                            if (tok < w.kv_end &&
+                                (!kWindow || tok < p.sinks || tok >= uw.low)) {
                                 const int pi =
                                     p.ps_shift >= 0 ? (tok >> p.ps_shift) : (tok / p.page_size);
                                 const int sl = tok - pi * p.page_size;
@@ -955,6 +1003,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                     w.kv_end = rec[8];
                     w.kb0 = rec[10];
                     w.n_kb = rec[11];
+                    UnitWindow uw;
+                    if constexpr (kWindow)
+                        uw = unit_window(p, rec[5], rec[4], rec[6], rec[7]);
                     mbar_arrive(&rec_empty[rs]);
                     if (!have)
                         continue;
@@ -981,8 +1032,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                         const bool more = j + 1 < n_kb;
                         // this run's data and P, waited for while the other
                         // tile's run is issued
+                        const int key0 =
+                            (kWindow ? uw.block(w.kb0 + j) : w.kb0 + j) * C::kKeys;
                         const bool v_gen =
-                            !p.use_tma || w.kv_end - (w.kb0 + j) * C::kKeys < C::kKeys;
+                            !p.use_tma || w.kv_end - key0 < C::kKeys ||
+                            (kWindow && !uw.whole(key0, C::kKeys, p.sinks));
                         if (!wait_only(&v_full[kj % VS], (uint32_t)((kj / VS) & 1)))
                             break;
                         if (more &&
@@ -1093,11 +1147,16 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
             const int ntok = t >= 0 ? min(tq, q_len - t * tq) : 0;
             // positions counted from the entry's first key (a part of a split
             // unit starts at block kb0); a row with no query masks every key
-            const int pos_first = rec[5] - q_len + (t >= 0 ? t * tq : 0) - rec[10] * C::kKeys;
+            // (with a window: from the row's first key)
+            const int pos_first = rec[5] - q_len + (t >= 0 ? t * tq : 0) -
+                                  (kWindow ? 0 : rec[10] * C::kKeys);
             const int pos =
                 (t >= 0 && m < rows_used && tok_m < ntok) ? pos_first + tok_m : kNoQuery;
             float m_run = -INFINITY, l_run = 0.f;
             const int n_kb = rec[11];
+            UnitWindow uw;
+            if constexpr (kWindow)
+                uw = unit_window(p, rec[5], q_len, rec[6], rec[7]);
             // the partner half has read the previous unit's l (it loaded O
             // after it) before this unit's first max overwrites it
             if (!C::kOnesL && it > 0) {
@@ -1117,11 +1176,21 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 tc_fence_after();
                 float sv[64];
                 tmem_ld64(t_s + 64 * h, sv);
-                const int key0 = j * C::kKeys + 64 * h;
+                const int key0 = (kWindow ? uw.block(rec[10] + j) : j) * C::kKeys + 64 * h;
                 if (key0 + 63 > pos_first) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
                         sv[i] = key0 + i > pos ? -INFINITY : sv[i];
+                }
+                if constexpr (kWindow) {
+                    // keys under the window, behind the sinks; none of a tile whose last
+                    // query's window starts at or before the half's first key
+                    if (key0 < pos_first + ntok - p.window && key0 + 63 >= p.sinks) {
+                        const int under = pos - p.window;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            sv[i] = key0 + i <= under && key0 + i >= p.sinks ? -INFINITY : sv[i];
+                    }
                 }
                 // this half's max: three-input max over 8 independent chains
                 float mx8[8];
@@ -1277,7 +1346,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
 // base of its own with (base, l): part i weighs l_i 2^(base_i - the largest
 // base), and the parts are summed in part order (the pages' split-KV merge
 // by (max, sum), as decode_combine does per split).
-template <int D>
+template <int D, bool kWindow>
 __global__ void __launch_bounds__(128) prefill_merge_kernel(const __grid_constant__ PrefillParams p)
 {
     using C = PrefillCfg<D>;
@@ -1300,7 +1369,7 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const __grid_constan
     }
     PrefillUnit w;
     // the unit as its first part sees it: np parts, or not cut
-    if (!prefill_unit<true>(p, p.split_base + su * p.split, w, false) || w.part_id < 0)
+    if (!prefill_unit<true, kWindow>(p, p.split_base + su * p.split, w, false) || w.part_id < 0)
         return;                                        // no work, or written whole
     const int np = (w.part_id >> 4) & 31;
     const int t = x == 0 ? w.tA : w.tB;
@@ -1356,16 +1425,17 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const __grid_constan
                    pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv));
 }
 
-template <int D>
+template <int D, bool kWindow>
 cudaError_t launch_prefill_d(const PrefillParams &p, int sms, cudaStream_t stream)
 {
     using C = PrefillCfg<D>;
     static DeviceOnce attrs;
     const cudaError_t attr_err = attrs.run([] {
-        cudaError_t e = cudaFuncSetAttribute(
-            prefill_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, false, kWindow>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::kSmemBytes);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefill_kernel<D, true>,
+            e = cudaFuncSetAttribute(prefill_kernel<D, true, kWindow>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
         return e;
     });
@@ -1383,14 +1453,14 @@ cudaError_t launch_prefill_d(const PrefillParams &p, int sms, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = p.split > 1 ? cudaLaunchKernelEx(&cfg, prefill_kernel<D, true>, p)
-                                : cudaLaunchKernelEx(&cfg, prefill_kernel<D, false>, p);
+    cudaError_t e = p.split > 1 ? cudaLaunchKernelEx(&cfg, prefill_kernel<D, true, kWindow>, p)
+                                : cudaLaunchKernelEx(&cfg, prefill_kernel<D, false, kWindow>, p);
     if (e == cudaSuccess && p.split > 1) {
         // the split units' merge, once the kernel above has finished
         cfg.gridDim = dim3((unsigned)(2 * ((p.n_units - p.split_base) / p.split) * (D / 8)));
         cfg.blockDim = dim3(C::kRows);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, p);
+        e = cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D, kWindow>, p);
     }
     if (e != cudaSuccess)
         return e;
@@ -1544,7 +1614,11 @@ cudaError_t launch_prefill(const PrefillParams &p_in, int D, int max_q_len, void
         p.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) +
                                              entries * prefill_slot_o_bytes(D));
     }
-    return D == 64 ? launch_prefill_d<64>(p, sms, stream) : launch_prefill_d<128>(p, sms, stream);
+    if (p.window > 0)
+        return D == 64 ? launch_prefill_d<64, true>(p, sms, stream)
+                       : launch_prefill_d<128, true>(p, sms, stream);
+    return D == 64 ? launch_prefill_d<64, false>(p, sms, stream)
+                   : launch_prefill_d<128, false>(p, sms, stream);
 }
 
 } // namespace pkv

@@ -44,7 +44,7 @@ EXPORTS = (
     "paged_kv_extend_norm", "paged_kv_append_q8", "paged_kv_extend_q8", "paged_kv_read_q8",
     "paged_decode_attn_q8", "paged_decode_attn_q8_planned", "paged_decode_plan_q8",
     "paged_kv_append_q4", "paged_kv_extend_q4", "paged_kv_read_q4", "paged_decode_attn_q4",
-    "paged_decode_attn_window",
+    "paged_decode_attn_window", "paged_prefill_attn_window",
 )
 
 
@@ -136,6 +136,7 @@ def lib():
             "paged_kv_read_q4": (I, [DP, P, P, P, P, P, P, P, P, P, P, P]),
             "paged_decode_attn_q4": (I, [DP, P, P, P, P, P, P, P, P, I, I, I, P, Z, P, P]),
             "paged_decode_attn_window": (I, [DP, P, P, P, P, P, P, I, I, I, P, Z, P, P]),
+            "paged_prefill_attn_window": (I, [DP, P, P, I, I, P, P, P, P, P, I, I, P, Z, P, P, P]),
             "pkv_testing_set_handoff_wait_ns": (I, [ctypes.c_ulonglong]),
             "pkv_status_str": (ctypes.c_char_p, [I]),
             "pkv_version": (I, []),
@@ -663,6 +664,20 @@ def paged_decode_attn_window(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, 
         ctypes.byref(d), _bf16_ptr(q), _bf16_ptr(k_pool), _bf16_ptr(v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits, _ptr(workspace), ws_bytes,
         _bf16_ptr(out), _stream(stream)))
+
+
+def paged_prefill_attn_window(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices, kv_indptr,
+                              seq_lens, window: int, sinks: int, out, status=None,
+                              max_q_len: Optional[int] = None, stream=None, workspace=None) -> None:
+    """paged_prefill_attn in which a query sees the last `window` keys up to its own
+    and the row's first `sinks` (window 0: all up to its own)."""
+    total_q = int(q.shape[0])
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("paged_prefill_attn_window", lib().paged_prefill_attn_window(
+        ctypes.byref(d), _bf16_ptr(q), _ptr(qo_indptr), total_q,
+        total_q if max_q_len is None else int(max_q_len), _bf16_ptr(k_pool), _bf16_ptr(v_pool),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, _ptr(workspace), ws_bytes,
+        _bf16_ptr(out), _ptr(status), _stream(stream)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -108,3 +108,20 @@ def test_decode_refusals(name):
     assert call(d=_d(B=0)) == pkv.PKV_OK
     big = _d(num_pages=1 << 28)
     assert call(d=big, ws_bytes=pkv.workspace_bytes(big, 8)) == UNSUP
+
+
+def test_window_prefill_refusals():
+    def call(d=None, total_q=8, max_q=8, window=64, sinks=4, **kw):
+        a = dict(q=FAKE, qo=FAKE, k=FAKE, v=FAKE, ind=FAKE, ptr=FAKE, sl=FAKE, ws=FAKE, out=FAKE, st=None)
+        a.update(kw)
+        return pkv.lib().paged_prefill_attn_window(
+            ctypes.byref(d or _d()), a["q"], a["qo"], total_q, max_q, a["k"], a["v"], a["ind"], a["ptr"], a["sl"],
+            window, sinks, a["ws"], 1 << 20, a["out"], a["st"], None)
+
+    for field in ("q", "qo", "k", "v", "ind", "ptr", "sl", "out"):
+        assert call(**{field: None}) == BAD, field
+        assert call(**{field: FAKE + 2}) == BAD, field
+    assert call(ws=FAKE + 16) == BAD and call(st=FAKE + 1) == BAD
+    assert call(window=-1) == BAD and call(sinks=-1) == BAD
+    assert call(total_q=-1) == BAD and call(max_q=-1) == BAD
+    assert call(d=_d(D=96)) == UNSUP and call(d=_d(B=0)) == pkv.PKV_OK and call(total_q=0) == pkv.PKV_OK
