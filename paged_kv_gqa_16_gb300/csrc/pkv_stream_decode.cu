@@ -41,22 +41,31 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;                 // consumer warps
 constexpr float kRaise = 15.f;            // how far a score may exceed its base
 
 template <int BITS, int D, int HPC, int NT>
 struct StreamCfg {
     static constexpr bool kCodes = BITS == 4;
+#ifndef QW
+#define QW 8
+#define QT 2
+#endif
+    static constexpr int kWarps = kCodes && NT == 1 ? QW : 8;   // consumer warps
     static constexpr int kWph = kWarps / HPC;             // warps of a kv head
-    // tiles of 16 tokens that a warp takes at a time: two chains of products and
-    // exponentials to overlap, where the registers allow it
-    static constexpr int kTiles = kCodes && NT == 1 ? 2 : 1;
+    // tiles of 16 tokens that a warp takes at a time
+    static constexpr int kTiles = kCodes && NT == 1 ? QT : 1;
     static constexpr int kTok = 16 * kTiles * kWph;       // tokens of a stage
     static constexpr int kProducers = 3;                  // producer warps, a stage each in turn
     static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kHeadBytes = D * BITS / 8;
     static constexpr int kRowBytes = HPC * kHeadBytes;    // one token, HPC kv heads
-    static constexpr int kStageBytes = 2 * kTok * kRowBytes;
+    // Rows of 2 KB go by one bulk copy each, with a pitch that spreads them over the
+    // banks: a lane's instruction in place of four of a warp.  (Shorter ones would be
+    // slower so: the copy engine takes about 24 copies a microsecond and SM.)
+    static constexpr bool kBulk = BITS == 16 && kRowBytes >= 2048;
+    static_assert(!kBulk || kTok == 16, "a lane copies a row of K or of V");
+    static constexpr int kPitch = kBulk ? kRowBytes + 16 : kRowBytes;
+    static constexpr int kStageBytes = 2 * kTok * kPitch;
     // a token's scale bytes (of K, and of V), and its room for them
     static constexpr int kScaleRow = kCodes ? HPC * D / kQ4Group : 0;
     static constexpr int kScalePitch = kScaleRow == 2 ? 8 : kScaleRow;
@@ -78,7 +87,7 @@ struct StreamCfg {
     static constexpr int kPrefixOffset = kAbortOffset + 16;
     static constexpr int kSmemBytes = kPrefixOffset + (kQ8MaxRows + 1) * 4;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
-    static_assert(kStageBytes % 1024 == 0, "swizzled rows");
+    static_assert(kBulk || kStageBytes % 1024 == 0, "swizzled rows");
     static_assert(kScaleBytes % 16 == 0 && kJoinBytes % 16 == 0, "alignment");
 };
 
@@ -91,15 +100,39 @@ __device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, i
                  : "memory");
 }
 
-// The four codes of two tokens in a transposed word (token 2c in the low half) as
-// f16 pairs of the two, code J of each.
-template <int J>
-__device__ __forceinline__ uint32_t f16x2_of_two_tokens(uint32_t even, uint32_t odd)
+// d = A B, f16 products in fp32 (mma_f16 from zero: no registers to clear).
+__device__ __forceinline__ void mma_f16_from_zero(float (&d)[4], const uint32_t (&a)[4],
+                                                  uint32_t b0, uint32_t b1)
 {
-    return J == 0   ? f16x2_of_e2m1x2<0>(even)
-           : J == 1 ? f16x2_of_e2m1x2<0>(odd)
-           : J == 2 ? f16x2_of_e2m1x2<1>(even)
-                    : f16x2_of_e2m1x2<1>(odd);
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Left shifts as products: the arithmetic-logic pipe, which makes the conversions,
+// sets this kernel's pace, and the multiply-add pipe has time.  (The factors come
+// from a place that the compiler does not see through.)
+struct Shifts {
+    uint32_t by4, by7, by12, by15, by16, by23;
+};
+
+__device__ __forceinline__ Shifts shifts()
+{
+    uint32_t one;
+    asm volatile("mov.u32 %0, 1;" : "=r"(one));
+    return {one << 4, one << 7, one << 12, one << 15, one << 16, one << 23};
+}
+
+// A transposed word holds four codes of two tokens, A0 .. A3 in its low half, B0 ..
+// B3 in its high half.  `even` and `odd` hold (A0, B0), (A2, B2) and (A1, B1), (A3, B3)
+// in bytes 2 and 3.
+__device__ __forceinline__ void two_tokens(uint32_t w, const Shifts &by, uint32_t &even,
+                                           uint32_t &odd)
+{
+    const uint32_t w16 = w * by.by16, w4 = w * by.by4, w12 = w * by.by12;
+    even = (w16 & 0x0f0f0f0fu) | (w4 & 0xf0f0f0f0u);
+    odd = (w12 & 0x0f0f0f0fu) | (w & 0xf0f0f0f0u);
 }
 
 template <int N>
@@ -107,9 +140,10 @@ using Const = std::integral_constant<int, N>;
 
 // Byte B of a scale word as 2^(byte - 127) (infinity for 255).
 template <int B>
-__device__ __forceinline__ float scale_of(uint32_t w)
+__device__ __forceinline__ float scale_of(uint32_t w, const Shifts &by)
 {
-    return __uint_as_float((B == 3 ? w >> 1 : w << (23 - 8 * B)) & 0x7f800000u);
+    const uint32_t at = B == 0 ? w * by.by23 : B == 1 ? w * by.by15 : B == 2 ? w * by.by7 : w >> 1;
+    return __uint_as_float(at & 0x7f800000u);
 }
 
 template <int BITS, int D, int HPC, int NT>
@@ -118,6 +152,7 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
 {
     using C = StreamCfg<BITS, D, HPC, NT>;
     constexpr int kProducers = C::kProducers;
+    constexpr int kWarps = C::kWarps;
     constexpr int NST = C::kStages;
     constexpr int U = C::kTiles;
     constexpr int G32 = D / kQ4Group;             // scales of a head vector
@@ -136,12 +171,15 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
     // that the units of eight tokens at one column are in different banks
     constexpr int kKeyShift = C::kRowBytes >= 128 ? 0 : C::kRowBytes == 64 ? 1 : 2;
     auto line_addr = [](int t, int b) {
-        return (uint32_t)(t * C::kRowBytes + b) ^ (uint32_t)((t >> kKeyShift) & 7) << 4;
+        return C::kBulk ? (uint32_t)(t * C::kPitch + b)
+                        : (uint32_t)(t * C::kRowBytes + b) ^
+                              (uint32_t)((t >> kKeyShift) & 7) << 4;
     };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&full[i], 33);     // a producer warp, and each of its lanes' copies
+            // a producer warp's lanes, or it once and each of its lanes' copies
+            mbar_init(&full[i], C::kBulk ? 32 : 33);
             mbar_init(&empty[i], kWarps);
         }
         fence_mbar_init();
@@ -192,106 +230,148 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
         const int pw = warp - kWarps;
         const uint64_t policy = policy_evict_first();
         constexpr int IDS = (C::kTok + 31) / 32;      // page ids a lane holds
-        int it = 0;
-        bool aborted = false;
         auto page_of_tok = [&](int t) {
             return p.ps_shift >= 0 ? (t >> p.ps_shift) : (t / p.page_size);
         };
-        for (int r = r0; r < n_rows && !aborted; ++r) {
+        // A stage: seen tokens [tok, t1) of a row as far as they fit; hg < 0: none.
+        struct Stage {
+            int r, tok, t1, hg, pg0, npg, skip;
+        };
+        // the first stage of the rows from r on
+        auto row_stage = [&](Stage &s, int r) {
+            while (r < n_rows && prefix[r + 1] == prefix[r])
+                ++r;
             // [lo, hi): the positions of the row's seen tokens
-            const int lo = prefix[r] + p.row_cost, hi = prefix[r + 1];
+            const int lo = r < n_rows ? prefix[r] + p.row_cost : end;
+            s.hg = -1;
             if (lo >= end)
-                break;
-            if (hi == prefix[r])
-                continue;
-            const int t0 = max(start, lo) - lo, t1 = min(end, hi) - lo;
-            const int b = row_of(r) % p.B, hg = row_of(r) / p.B;
-            const int pg0 = p.kv_indptr[b];
-            int npg = p.kv_indptr[b + 1] - pg0;
-            if (pg0 < 0 || npg < 0 || pg0 > p.num_indices - npg)
-                npg = 0;
+                return;
+            const int hi = prefix[r + 1], v = row_of(r), b = v % p.B;
+            s.r = r;
+            s.tok = max(start, lo) - lo;
+            s.t1 = min(end, hi) - lo;
+            s.hg = v / p.B;
+            s.pg0 = p.kv_indptr[b];
+            s.npg = p.kv_indptr[b + 1] - s.pg0;
+            if (s.pg0 < 0 || s.npg < 0 || s.pg0 > p.num_indices - s.npg)
+                s.npg = 0;
             // tokens that a row of the window's length skips behind its sinks
-            int skip = 0;
+            s.skip = 0;
             if (hi - lo == sp.most_seen) {
                 unsigned bad = 0;
-                skip = checked_row_len(p, b, bad) - sp.most_seen;
+                s.skip = checked_row_len(p, b, bad) - sp.most_seen;
             }
-            auto token = [&](int i) { return i < sp.sinks ? i : i + skip; };
-            // the table's entry for this lane's k-th token of the stage at tok
-            auto load_id = [&](int tok, int k) {
-                const int at = k * 32 + lane;
-                const bool there = at < C::kTok && tok + at < t1;
-                const int pi = page_of_tok(there ? token(tok + at) : 0);
-                return there && pi < npg ? p.kv_indices[pg0 + pi] : 0;
-            };
-            // the ids of this warp's next stage are loaded a stage ahead
-            int ids[IDS];
-            const int first = (pw - it % kProducers + kProducers) % kProducers;
+        };
+        auto step = [&](Stage &s, int n) {
+            for (int k = 0; k < n && s.hg >= 0; ++k) {
+                s.tok += C::kTok;
+                if (s.tok >= s.t1)
+                    row_stage(s, s.r + 1);
+            }
+        };
+        auto token = [&](const Stage &s, int i) { return i < sp.sinks ? i : i + s.skip; };
+        // the table's entry for this lane's k-th token of a stage
+        auto load_id = [&](const Stage &s, int k) {
+            const int at = k * 32 + lane;
+            const bool there = s.hg >= 0 && at < C::kTok && s.tok + at < s.t1;
+            const int pi = page_of_tok(there ? token(s, s.tok + at) : 0);
+            return there && pi < s.npg ? p.kv_indices[s.pg0 + pi] : 0;
+        };
+        int it = pw;
+        Stage cur;
+        row_stage(cur, r0);
+        step(cur, pw);
+        // the ids of this warp's next stage, of another row too, are loaded a stage ahead
+        int ids[IDS];
+#pragma unroll
+        for (int k = 0; k < IDS; ++k)
+            ids[k] = load_id(cur, k);
+        for (; cur.hg >= 0; it += kProducers) {
+            Stage after = cur;
+            step(after, kProducers);
+            const int st = it % NST;
+            int next[IDS];
 #pragma unroll
             for (int k = 0; k < IDS; ++k)
-                ids[k] = load_id(t0 + first * C::kTok, k);
-            for (int tok = t0; tok < t1; tok += C::kTok, ++it) {
-                if (it % kProducers != pw)
-                    continue;
-                const int st = it % NST;
-                int next[IDS];
-#pragma unroll
-                for (int k = 0; k < IDS; ++k)
-                    next[k] = load_id(tok + kProducers * C::kTok, k);
-                if (it >= NST) {
-                    // (a consumer that gave up releases its stages without having
-                    // waited for them, after it has set the abort word)
-                    const bool ok =
-                        mbar_wait_or_abort(&empty[st], (uint32_t)(((it / NST) - 1) & 1),
-                                           p.handoff_wait_ns, abort) &&
-                        !*abort;
-                    if (!__all_sync(kFull, ok)) {
-                        aborted = true;
-                        if (lane == 0) {
-                            *abort = 1;
-                            atomicOr(p.status, kFlagTimeout);
-                        }
-                        break;
+                next[k] = load_id(after, k);
+            if (it >= NST) {
+                // (a consumer that gave up releases its stages without having
+                // waited for them, after it has set the abort word)
+                const bool ok =
+                    mbar_wait_or_abort(&empty[st], (uint32_t)(((it / NST) - 1) & 1),
+                                       p.handoff_wait_ns, abort) &&
+                    !*abort;
+                if (!__all_sync(kFull, ok)) {
+                    if (lane == 0) {
+                        *abort = 1;
+                        atomicOr(p.status, kFlagTimeout);
                     }
+                    break;
                 }
-                unsigned char *stage = smem + st * C::kStageBytes;
-                unsigned char *sc0 = smem + C::kScaleOffset + st * C::kScaleBytes;
-                const int nvalid = min(C::kTok, t1 - tok);
-                // a page id of a token that is there, checked
-                auto checked = [&](int page, bool there) {
-                    if (page < 0 || page >= p.num_pages) {
-                        if (there)
-                            atomicOr(p.status, kFlagBadPage);
-                        page = 0;
-                    }
-                    return page;
-                };
-                // a token's scale bytes of one pool, from byte `at` of it
-                auto copy_scales = [&](const uint8_t *scales, int row, size_t at) {
-                    unsigned char *sc = sc0 + row * C::kScalePitch;
-                    if constexpr (C::kScaleRow >= 16) {
+            }
+            unsigned char *stage = smem + st * C::kStageBytes;
+            unsigned char *sc0 = smem + C::kScaleOffset + st * C::kScaleBytes;
+            const int nvalid = min(C::kTok, cur.t1 - cur.tok);
+            // a page id of a token that is there, checked
+            auto checked = [&](int page, bool there) {
+                if (page < 0 || page >= p.num_pages) {
+                    if (there)
+                        atomicOr(p.status, kFlagBadPage);
+                    page = 0;
+                }
+                return page;
+            };
+            // a token's scale bytes of one pool, from byte `at` of it
+            auto copy_scales = [&](const uint8_t *scales, int row, size_t at) {
+                unsigned char *sc = sc0 + row * C::kScalePitch;
+                if constexpr (C::kScaleRow >= 16) {
 #pragma unroll
-                        for (int j = 0; j < C::kScaleRow; j += 16)
-                            cp_async16(smem_addr(sc + j), scales + at + j, policy);
-                    } else if constexpr (C::kScaleRow == 8) {
-                        cp_async<8>(sc, scales + at, 8);
-                    } else if constexpr (C::kScaleRow == 4) {
-                        cp_async<4>(sc, scales + at, 4);
-                    } else {
-                        // the aligned word around the two bytes (the pool's last may be
-                        // half a word), and where they are in it
-                        const size_t word = at & ~(size_t)3;
-                        const size_t left =
-                            (size_t)p.num_pages * p.page_size * p.Hkv * G32 - word;
-                        cp_async<4>(sc, scales + word, left < 4 ? (int)left : 4);
-                        sc[4] = (unsigned char)(at & 3);
-                    }
-                };
+                    for (int j = 0; j < C::kScaleRow; j += 16)
+                        cp_async16(smem_addr(sc + j), scales + at + j, policy);
+                } else if constexpr (C::kScaleRow == 8) {
+                    cp_async<8>(sc, scales + at, 8);
+                } else if constexpr (C::kScaleRow == 4) {
+                    cp_async<4>(sc, scales + at, 4);
+                } else {
+                    // the aligned word around the two bytes (the pool's last may be
+                    // half a word), and where they are in it
+                    const size_t word = at & ~(size_t)3;
+                    const size_t left =
+                        (size_t)p.num_pages * p.page_size * p.Hkv * G32 - word;
+                    cp_async<4>(sc, scales + word, left < 4 ? (int)left : 4);
+                    sc[4] = (unsigned char)(at & 3);
+                }
+            };
+            if constexpr (C::kBulk) {
+                // Lane l: token l % 16, K or (from lane 16 on) V.  The rows of V that end
+                // the piece's last tile are zeroed: their weights are 0, and what a
+                // stage held may be NaN.
+                const int t16 = lane & 15;
+                const bool of_v = lane >= 16, there = t16 < nvalid;
+                const int t = there ? token(cur, cur.tok + t16) : 0;
+                const int page = checked(__shfl_sync(kFull, ids[0], t16), there);
+                fence_proxy_async_smem();          // the slot's last reads, before the copies
+                unsigned char *to = stage + ((of_v ? C::kTok : 0) + t16) * C::kPitch;
+                if (of_v && !there)
+                    for (int j = 0; j < C::kRowBytes / 16; ++j)
+                        reinterpret_cast<uint4 *>(to)[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[st], (uint32_t)(nvalid * 2 * C::kRowBytes));
+                else
+                    mbar_arrive(&full[st]);
+                if (there) {
+                    const size_t slot = (size_t)page * p.page_size + t - page_of_tok(t) * p.page_size;
+                    const uint8_t *from = (of_v ? p.v_codes : p.k_codes) +
+                                          slot * ((size_t)p.Hkv * C::kHeadBytes) +
+                                          (size_t)cur.hg * C::kRowBytes;
+                    bulk_copy_g2s_hint(to, from, C::kRowBytes, &full[st], policy);
+                }
+            } else {
                 // bf16: the rows of V that end the piece's last tile are zeroed (their
                 // weights are 0, and what a stage held may be NaN)
                 const int filled = BITS == 16 ? (nvalid + 15) & ~15 : nvalid;
                 constexpr int CH = C::kRowBytes / 16;      // 16-byte lines of a token
-                const size_t line0 = (size_t)hg * C::kRowBytes;
+                const size_t line0 = (size_t)cur.hg * C::kRowBytes;
                 const unsigned tok_bytes = (unsigned)(p.Hkv * C::kHeadBytes);
 #pragma unroll
                 for (int k = 0; k < IDS; ++k) {
@@ -299,12 +379,12 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                         break;
                     const int row = k * 32 + lane;
                     const bool there = row < nvalid;
-                    const int t = there ? token(tok + row) : 0;
+                    const int t = there ? token(cur, cur.tok + row) : 0;
                     const int page = checked(ids[k], there);
                     const int slot = page * p.page_size + t - page_of_tok(t) * p.page_size;
                     if constexpr (C::kCodes) {
                         if (there) {
-                            const size_t at = ((size_t)slot * p.Hkv + (size_t)hg * HPC) * G32;
+                            const size_t at = ((size_t)slot * p.Hkv + (size_t)cur.hg * HPC) * G32;
                             copy_scales(p.k_scale, row, at);
                             copy_scales(p.v_scale, C::kTok + row, at);
                         }
@@ -337,17 +417,17 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&full[st]);
-#pragma unroll
-                for (int k = 0; k < IDS; ++k)
-                    ids[k] = next[k];
             }
+#pragma unroll
+            for (int k = 0; k < IDS; ++k)
+                ids[k] = next[k];
+            cur = after;
         }
         // Let this warp's copies land before it exits, with the full time
         // limit: a consumer that gave up skips its stages, and the block must
         // not exit while a copy into its shared memory is in flight.
-        for (int k = (it > NST ? it - NST : 0); k < it; ++k)
-            if (k % kProducers == pw)
-                (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
+        for (int k = it - kProducers, n = 0; k >= 0 && n < NST; k -= kProducers, n += kProducers)
+            (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
         grid_launch_dependents();
         return;
     }
@@ -359,18 +439,22 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
     // Matrix loads: lane l addresses token l % 16 of a tile and the 16-byte
     // column l / 16 of each two; the 32-byte column i of a row whose first is at
     // `addr` is at addr ^ 32 i: the swizzle is in the same bits.
-    auto column = [](uint32_t addr, int i) { return addr ^ (i * 32u); };
+    auto column = [](uint32_t addr, int i) {
+        return C::kBulk ? addr + i * 32u : addr ^ (i * 32u);
+    };
     const int tile0 = tg * 16 * U;                // this warp's first token of a stage
     const uint32_t k_off =
         smem_s + line_addr(tile0 + (lane & 15), hw * C::kHeadBytes + (lane >> 4) * 16);
-    const uint32_t v_off = k_off + C::kTok * C::kRowBytes;
+    const uint32_t v_off = k_off + C::kTok * C::kPitch;
     // a tile further: 16 rows, and their bits of the swizzle
     auto tile = [](uint32_t addr, int u) {
         return (addr + u * 16 * C::kRowBytes) ^ (uint32_t)((u * 16 >> kKeyShift) & 7) << 4;
     };
     // bf16 weights need no room under the largest; f16's end 2^-24 under 1
     constexpr float kUnder = BITS == 16 ? 0.f : 7.f;
-    int it = 0;
+    const Shifts by = shifts();
+    int st = 0;                        // the next stage's slot, and the phase of its filling
+    uint32_t phase = 0;
     bool aborted = false;
 
     for (int r = r0; r < n_rows; ++r) {
@@ -433,22 +517,22 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
             }
         }
 
-        float m_run[NT][2], l_run[NT][2];
+        // the sums carry 2^-m_run; base: m_run, 0 before the first finite score; a
+        // score past `limit` raises it
+        float m_run[NT][2], l_run[NT][2], base[NT][2], limit[NT][2];
         float oacc[NT][D / 16][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m_run[nt][0] = m_run[nt][1] = -INFINITY;
-            l_run[nt][0] = l_run[nt][1] = 0.f;
+            m_run[nt][0] = m_run[nt][1] = limit[nt][0] = limit[nt][1] = -INFINITY;
+            l_run[nt][0] = l_run[nt][1] = base[nt][0] = base[nt][1] = 0.f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
                 oacc[nt][j][0] = oacc[nt][j][1] = oacc[nt][j][2] = oacc[nt][j][3] = 0.f;
         }
 
-        for (int tok = t0; tok < t1; tok += C::kTok, ++it) {
-            const int st = it % NST;
+        for (int tok = t0; tok < t1; tok += C::kTok) {
             if (!aborted) {
-                const bool ok = mbar_wait_or_abort(&full[st], (uint32_t)((it / NST) & 1),
-                                                   p.handoff_wait_ns, abort);
+                const bool ok = mbar_wait_or_abort(&full[st], phase, p.handoff_wait_ns, abort);
                 if (!__all_sync(kFull, ok)) {
                     aborted = true;
                     if (lane == 0) {
@@ -483,8 +567,15 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            y[nt][0][x] = in(g + (x >> 1) * 8) ? sacc[nt][x] * cq[nt][x & 1]
-                                                               : -INFINITY;
+                            y[nt][0][x] = sacc[nt][x] * cq[nt][x & 1];
+                    if (cut) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (!in(g + (x >> 1) * 8))
+                                    y[nt][0][x] = -INFINITY;
+                    }
                 } else {
                     // the scale words of the tokens at rows g and g + 8 of each tile
                     uint32_t wk[U][2];
@@ -497,7 +588,7 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                         else
                             return reinterpret_cast<const uint32_t *>(at)[hw];
                     };
-                    float s[NT][U][4] = {};
+                    float s[NT][U][4];
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -505,21 +596,31 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                             wk[u][k] = scale_word(u * 16 + k * 8 + g);
                             wv[u][k] = scale_word(C::kTok + u * 16 + k * 8 + g);
                         }
+                    // (the scale bytes of a token that is not there may be any: none)
+                    if (cut) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                if (!in(u * 16 + k * 8 + g))
+                                    wv[u][k] = 0;
+                    }
                     auto unit = [&](auto at, int u, uint32_t lo_, uint32_t hi_) {
                         constexpr int i = decltype(at)::value;
                         const uint32_t a0[4] = {f16x2_of_e2m1x2<0>(lo_), f16x2_of_e2m1x2<0>(hi_),
                                                 f16x2_of_e2m1x2<1>(lo_), f16x2_of_e2m1x2<1>(hi_)};
                         const uint32_t a1[4] = {f16x2_of_e2m1x2<2>(lo_), f16x2_of_e2m1x2<2>(hi_),
                                                 f16x2_of_e2m1x2<3>(lo_), f16x2_of_e2m1x2<3>(hi_)};
-                        const float f[2] = {scale_of<i>(wk[u][0]), scale_of<i>(wk[u][1])};
+                        const float f[2] = {scale_of<i>(wk[u][0], by), scale_of<i>(wk[u][1], by)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float acc[4] = {};
-                            mma_f16(acc, a0, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+                            float acc[4];
+                            mma_f16_from_zero(acc, a0, qf[nt][2 * i][0], qf[nt][2 * i][1]);
                             mma_f16(acc, a1, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                s[nt][u][x] = fmaf(acc[x], f[x >> 1], s[nt][u][x]);
+                                s[nt][u][x] = i == 0 ? acc[x] * f[x >> 1]
+                                                     : fmaf(acc[x], f[x >> 1], s[nt][u][x]);
                         }
                     };
 #pragma unroll
@@ -539,26 +640,32 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const bool there = !cut || in(u * 16 + k * 8 + g);
-                            // (the scale bytes of a token that is not there may be any: none)
-                            if (!there)
-                                wv[u][k] = 0;
-                            float top = fmaxf(scale_of<0>(wv[u][k]), scale_of<1>(wv[u][k]));
+                            float top = fmaxf(scale_of<0>(wv[u][k], by), scale_of<1>(wv[u][k], by));
                             if constexpr (G32 == 4)
-                                top = fmaxf(top, fmaxf(scale_of<2>(wv[u][k]),
-                                                       scale_of<3>(wv[u][k])));
+                                top = fmaxf(top, fmaxf(scale_of<2>(wv[u][k], by),
+                                                       scale_of<3>(wv[u][k], by)));
                             const unsigned bits = __float_as_uint(top);
                             // (2^23 + byte) - (2^23 + 127)
                             const float ev = __uint_as_float(0x4b000000u | bits >> 23) - 8388735.f;
-                            inv_v[u][k] = there ? __uint_as_float(0x7f000000u - bits) : 0.f;
+                            inv_v[u][k] = __uint_as_float(0x7f000000u - bits);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    y[nt][u][2 * k + e] =
-                                        there ? fmaf(s[nt][u][2 * k + e], cq[nt][e], ev)
-                                              : -INFINITY;
+                                    y[nt][u][2 * k + e] = fmaf(s[nt][u][2 * k + e], cq[nt][e], ev);
                         }
+                    if (cut) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                if (!in(u * 16 + k * 8 + g)) {
+                                    inv_v[u][k] = 0.f;
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        y[nt][u][2 * k] = y[nt][u][2 * k + 1] = -INFINITY;
+                                }
+                    }
                 }
                 bool raise = false;
 #pragma unroll
@@ -567,7 +674,7 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            raise |= y[nt][u][x] > m_run[nt][x & 1] + kRaise;
+                            raise |= y[nt][u][x] > limit[nt][x & 1];
                 if (__any_sync(kFull, raise)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -583,6 +690,8 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                             const float mn = fmaxf(m_run[nt][e], mx - kUnder);
                             const float a = mn == -INFINITY ? 1.f : exp2_ftz(m_run[nt][e] - mn);
                             m_run[nt][e] = mn;
+                            base[nt][e] = mn == -INFINITY ? 0.f : mn;
+                            limit[nt][e] = mn + kRaise;
                             l_run[nt][e] *= a;
 #pragma unroll
                             for (int j = 0; j < D / 16; ++j) {
@@ -595,13 +704,11 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                 float w[NT][U][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float base0 = m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0];
-                    const float base1 = m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1];
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            w[nt][u][x] = exp2_ftz(y[nt][u][x] - (x & 1 ? base1 : base0));
+                            w[nt][u][x] = exp2_ftz(y[nt][u][x] - base[nt][x & 1]);
                             if constexpr (BITS == 4) {
                                 w[nt][u][x] *= inv_v[u][x >> 1];
                                 l_run[nt][x & 1] += w[nt][u][x];
@@ -637,7 +744,7 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                     // 2i + 1 take codes 4g, 4g + 1 and 4g + 2, 4g + 3 as rows g, g + 8
                     auto unit = [&](auto at, int u, uint32_t lo_, uint32_t hi_) {
                         constexpr int i = decltype(at)::value;
-                        const float f[2] = {scale_of<i>(wv[u][0]), scale_of<i>(wv[u][1])};
+                        const float f[2] = {scale_of<i>(wv[u][0], by), scale_of<i>(wv[u][1], by)};
                         uint32_t pb[NT][2];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -645,17 +752,13 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                             for (int k = 0; k < 2; ++k)
                                 pb[nt][k] = movmatrix_trans(pack_f16x2(
                                     w[nt][u][2 * k] * f[k], w[nt][u][2 * k + 1] * f[k]));
-                        // codes 0, 2 and 1, 3 of the two tokens, in bytes 0 and 1
-                        const uint32_t le = (lo_ & 0x0f0fu) | (lo_ >> 12 & 0xf0f0u);
-                        const uint32_t lod = (lo_ >> 4 & 0x0f0fu) | (lo_ >> 16 & 0xf0f0u);
-                        const uint32_t he = (hi_ & 0x0f0fu) | (hi_ >> 12 & 0xf0f0u);
-                        const uint32_t hod = (hi_ >> 4 & 0x0f0fu) | (hi_ >> 16 & 0xf0f0u);
-                        const uint32_t a0[4] = {
-                            f16x2_of_two_tokens<0>(le, lod), f16x2_of_two_tokens<1>(le, lod),
-                            f16x2_of_two_tokens<0>(he, hod), f16x2_of_two_tokens<1>(he, hod)};
-                        const uint32_t a1[4] = {
-                            f16x2_of_two_tokens<2>(le, lod), f16x2_of_two_tokens<3>(le, lod),
-                            f16x2_of_two_tokens<2>(he, hod), f16x2_of_two_tokens<3>(he, hod)};
+                        uint32_t le, lo, he, ho;
+                        two_tokens(lo_, by, le, lo);
+                        two_tokens(hi_, by, he, ho);
+                        const uint32_t a0[4] = {f16x2_of_e2m1x2<2>(le), f16x2_of_e2m1x2<2>(lo),
+                                                f16x2_of_e2m1x2<2>(he), f16x2_of_e2m1x2<2>(ho)};
+                        const uint32_t a1[4] = {f16x2_of_e2m1x2<3>(le), f16x2_of_e2m1x2<3>(lo),
+                                                f16x2_of_e2m1x2<3>(he), f16x2_of_e2m1x2<3>(ho)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_f16(oacc[nt][2 * i], a0, pb[nt][0], pb[nt][1]);
@@ -680,6 +783,10 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&empty[st]);
+            if (++st == NST) {
+                st = 0;
+                phase ^= 1u;
+            }
         }
 
         // ---- end of the piece: join the head's parts in pairs -----------------

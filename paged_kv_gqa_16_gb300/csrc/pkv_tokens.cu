@@ -315,12 +315,36 @@ __device__ __forceinline__ float odd_of(double x)
     return __uint_as_float(__float_as_uint(f) | ((double)f != x ? 1u : 0u));
 }
 
-// A lane's eight key values in 64 bits, as odd_of them: for the codes that lie too
-// near a border for 32 bits.  Rare (under 1% of a warp's rounds), so it reads the
-// weight and the rotation again.  1 / sqrt from the 32-bit one by two Newton steps.
+// The largest magnitude of the 32 elements of a scale, four lanes', as bits (of
+// which those of a NaN and of infinity are the largest).
+__device__ __forceinline__ unsigned scale_group_max(const float (&y)[8])
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// Eight codes of y at scale byte sb (255: zero codes).
+__device__ __forceinline__ uint32_t q4_encode8(const float (&y)[8], int sb)
+{
+    const float by = q4_unscale(sb);
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        z[j] = y[j] * by;
+    return sb == 255 ? 0u : e2m1x8(z);
+}
+
+// A lane's eight key codes, and their scale byte, from its values in 64 bits: for
+// codes that lie too near a border for 32.  Rare (under 1% of a warp's rounds), so it
+// reads the weight and the rotation again.  1 / sqrt from the 32-bit one by two
+// Newton steps.
 template <int D>
-__device__ __noinline__ void key_values_in_64(const __nv_bfloat16 *weight, const float *cos_sin,
-                                              float eps, uint4 raw, float (&y)[8])
+__device__ __noinline__ uint2 key_codes_in_64(const __nv_bfloat16 *weight, const float *cos_sin,
+                                              float eps, uint4 raw)
 {
     constexpr int LANES = D / 8;
     const int lane = threadIdx.x % LANES;
@@ -330,6 +354,7 @@ __device__ __noinline__ void key_values_in_64(const __nv_bfloat16 *weight, const
     for (int i = 0; i < 4; ++i)
         x[2 * i] = bf16_lo(in[i]), x[2 * i + 1] = bf16_hi(in[i]);
     double r = 1.0;
+    float y[8];
     if (weight != nullptr) {
         double s = 0.0;
 #pragma unroll
@@ -361,29 +386,8 @@ __device__ __noinline__ void key_values_in_64(const __nv_bfloat16 *weight, const
         y[2 * i] = odd_of(a * r);
         y[2 * i + 1] = odd_of(b * r);
     }
-}
-
-// The largest magnitude of the 32 elements of a scale, four lanes', as bits (of
-// which those of a NaN and of infinity are the largest).
-__device__ __forceinline__ unsigned scale_group_max(const float (&y)[8])
-{
-    unsigned m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-}
-
-// Eight codes of y at scale byte sb (255: zero codes).
-__device__ __forceinline__ uint32_t q4_encode8(const float (&y)[8], int sb)
-{
-    const float by = q4_unscale(sb);
-    float z[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        z[j] = y[j] * by;
-    return sb == 255 ? 0u : e2m1x8(z);
+    const int sb = q4_scale_byte(scale_group_max(y));
+    return make_uint2(q4_encode8(y, sb), (unsigned)sb);
 }
 
 // Whether some code of y, or its scale, could be another for a value `off` of y's pair
@@ -405,7 +409,8 @@ __device__ __forceinline__ bool q4_near_border(const float (&y)[8], const float 
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
     const float z = __uint_as_float(amax) * by;
     const bool scale = sb < 255 && (z + most > 6.f || (z - most <= 3.f && sb > 127 + kQ4MinExp));
-    return e2m1x8(lo) != e2m1x8(hi) || scale;
+    // (a zero's sign is no border)
+    return ((e2m1x8(lo) ^ e2m1x8(hi)) & 0x77777777u) != 0 || scale;
 }
 
 // A lane's scale bytes of a head, D / 32 of its four-lane groups, in one word of
@@ -536,8 +541,9 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
             if constexpr (BITS == 4) {
                 float y[8], pair[4], v8[8];
                 values_of(x, f, y);
-                unsigned amax = scale_group_max(y);
+                const unsigned amax = scale_group_max(y);
                 int sk = q4_scale_byte(amax);
+                uint32_t kc = q4_encode8(y, sk);
                 if (p.rope != nullptr || p.k_norm != nullptr) {
                     // What 32-bit operations may be off by, of the pair's magnitudes: the
                     // rotation's two roundings 2^-23, the check's one 2^-24; the norm's nine
@@ -546,17 +552,16 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
                     const float off = turn_gain * (p.k_norm != nullptr ? 0x1.8p-20f : 0x1p-22f);
                     pair_sizes(before, f, pair);
                     if (__any_sync(0xffffffffu, q4_near_border(y, pair, amax, sk, off))) {
-                        key_values_in_64<D>(p.k_norm,
-                                            p.rope != nullptr && row.pos >= 0 && row.bad == 0
-                                                ? p.rope + (size_t)row.pos * D : nullptr,
-                                            p.norm_eps, kraw, y);
-                        amax = scale_group_max(y);
-                        sk = q4_scale_byte(amax);
+                        const float *cos_sin = p.rope != nullptr && row.pos >= 0 && row.bad == 0
+                                                   ? p.rope + (size_t)row.pos * D : nullptr;
+                        const uint2 r = key_codes_in_64<D>(p.k_norm, cos_sin, p.norm_eps, kraw);
+                        kc = r.x;
+                        sk = (int)r.y;
                     }
                 }
                 values_of(unpack(vraw), 1.f, v8);
                 const int sv = q4_scale_byte(scale_group_max(v8));
-                const uint32_t kc = q4_encode8(y, sk), vc = q4_encode8(v8, sv);
+                const uint32_t vc = q4_encode8(v8, sv);
                 const uint32_t ks = q4_scale_word<D>(sk, lane), vs = q4_scale_word<D>(sv, lane);
                 if (store) {
                     reinterpret_cast<uint32_t *>(p.k_pool)[head * LANES + lane] = kc;
