@@ -696,8 +696,9 @@ pkv_status paged_decode_attn_window(const pkv_dims *dims, const void *q, const v
  * `sinks`: key t <= p if t > p - window or t < sinks; window 0 stands for no window.
  * Pages without a key that a query of the row's chunk sees are not read, and their
  * entries of kv_indices may hold anything.  An infinite or NaN value that some
- * queries of a tile see reaches the tile's others too, as one past a query's
- * position does in paged_prefill_attn.  Other arguments, results, errors and flags
+ * queries of a tile see, or that is in a page with a key that they see, may reach
+ * the tile's others too, as one past a query's position does in paged_prefill_attn.
+ * Other arguments, results, errors and flags
  * are those calls'. */
 pkv_status paged_prefill_attn_window(const pkv_dims *dims, const void *q,
                                      const int32_t *qo_indptr, int total_q, int max_q_len,

@@ -405,25 +405,26 @@ struct PrefillUnit {
     bool table_ok;
 };
 
-// A unit's keys under a window: keys in [sinks, low) are seen by none of its
-// queries; entry i of its list of key blocks is block i, from `first` on i + gap.
+// A unit's keys under a window, as a list without the keys that no query of the unit
+// sees: entry i is key i of the first `head`, key i + off behind them.  Both parts
+// are whole boxes of the copies (pages, or parts of one), so some keys at the ends
+// are there without being seen; the softmax masks them.
 struct UnitWindow {
-    int low, first, gap;
-    __device__ __forceinline__ int block(int i) const { return i < first ? i : i + gap; }
-    // whether each of n keys from key0 on is seen by some query
-    __device__ __forceinline__ bool whole(int key0, int n, int sinks) const
-    {
-        return key0 >= low || key0 + n <= sinks;
-    }
+    int head, off;
+    __device__ __forceinline__ int key(int i) const { return i < head ? i : i + off; }
 };
 
 __device__ __forceinline__ UnitWindow unit_window(const PrefillParams &p, int L, int q_len, int tA,
                                                   int tB)
 {
     UnitWindow u;
-    u.low = max(0, L - q_len + max(tA, tA < 0 ? tB : 0) * p.tq - p.window + 1);
-    u.first = (min(p.sinks, u.low) + 127) / 128;
-    u.gap = max(0, u.low / 128 - u.first);
+    const int mask = p.use_tma ? p.tma_rows - 1 : 0;
+    // the first key of the first query's window
+    const int low = max(0, L - q_len + max(tA, tA < 0 ? tB : 0) * p.tq - p.window + 1);
+    u.head = (min(p.sinks, low) + mask) & ~mask;
+    u.off = max(0, (low & ~mask) - u.head);
+    if (u.off == 0)
+        u.head = 0;                    // one run of keys from 0
     return u;
 }
 
@@ -553,7 +554,7 @@ __device__ __forceinline__ bool prefill_whole_unit(const PrefillParams &p, int u
     w.kv_end = w.L - w.q_len + min(w.q_len, (w.tB + 1) * p.tq);
     w.n_kb = (w.kv_end + 127) / 128;
     if constexpr (kWindow)
-        w.n_kb -= unit_window(p, w.L, w.q_len, w.tA, w.tB).gap;
+        w.n_kb = (w.kv_end - unit_window(p, w.L, w.q_len, w.tA, w.tB).off + 127) / 128;
     w.kb0 = 0;
     w.part_id = -1;
     w.pg0 = k0;
@@ -748,6 +749,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
             // 64 bytes are two whole L2 sectors, and the swizzle spreads the 8
             // rows' chunks over all banks
             const int kl = lane & 7, cl = lane >> 3;
+            auto page_of = [&](int tok) {
+                return p.ps_shift >= 0 ? (tok >> p.ps_shift) : (tok / p.page_size);
+            };
             int kb = 0;                                    // blocks issued, over all units
             int qit = 0;                                   // units whose Q the V warp loaded
             for (int r = 0; r * (int)gridDim.x < n_units && !*abort_flag; ++r) {
@@ -826,9 +830,25 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 }
                 if (is_v)
                     ++qit;
-                UnitWindow uw;
+                UnitWindow uw{0, 0};
                 if constexpr (kWindow)
                     uw = unit_window(p, w.L, w.q_len, w.tA, w.tB);
+                const int n_keys = kWindow ? w.kv_end - uw.off : w.kv_end;
+                // the page ids of block j's keys l, 32 + l, ..., where it is copied key by key
+                int ids[C::kKeys / 32];
+                auto load_ids = [&](int j) {
+                    const int key0 = (w.kb0 + j) * C::kKeys;
+                    if (j >= w.n_kb || (p.use_tma && (!is_v || n_keys - key0 >= C::kKeys)))
+                        return;
+#pragma unroll
+                    for (int k = 0; k < C::kKeys / 32; ++k) {
+                        const int i = key0 + k * 32 + lane;
+                        ids[k] = w.table_ok && i < n_keys
+                                     ? __ldg(p.kv_indices + w.pg0 +
+                                             page_of(kWindow ? uw.key(i) : i)) : 0;
+                    }
+                };
+                load_ids(0);
                 for (int j = 0; j < w.n_kb; ++j) {
                     const int slot = kb % ns;
                     if (kb >= ns) {
@@ -840,35 +860,23 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                     if (*abort_flag)
                         break;
                     const uint32_t dst = ring + slot * C::kKVBytes;
-                    const int key0 =
-                        (kWindow ? uw.block(w.kb0 + j) : w.kb0 + j) * C::kKeys;
-                    const int nkeys = min(C::kKeys, w.kv_end - key0);
-                    const bool seen_whole = !kWindow || uw.whole(key0, nkeys, p.sinks);
+                    // (with a window: entries of the unit's list of keys)
+                    const int key0 = (w.kb0 + j) * C::kKeys;
+                    const int nkeys = min(C::kKeys, n_keys - key0);
                     // K rows past kv_end are masked out of S whatever they hold,
                     // so a K block loads whole boxes; V rows past it meet P = 0 and
                     // must be finite, so a partial V block is copied with zero fill
-                    // (and so is one with keys that no query of the unit sees; of K,
-                    // boxes of such keys alone are left out)
-                    if (p.use_tma && (!is_v || (nkeys == C::kKeys && seen_whole))) {
+                    if (p.use_tma && (!is_v || nkeys == C::kKeys)) {
                         const int R = p.tma_rows;
-                        const int nbox = (nkeys + R - 1) / R;      // at most 16
-                        int boxes = nbox;
-                        auto box_seen = [&](int tok) {
-                            return seen_whole || tok < p.sinks || tok + R > uw.low;
-                        };
-                        if constexpr (kWindow)
-                            boxes = __popc(__ballot_sync(
-                                kAllTc, lane < nbox && box_seen(key0 + lane * R)));
+                        const int nbox = (nkeys + R - 1) / R;
                         if (lane == 0)
                             mbar_arrive_expect_tx(&full[slot],
-                                                  (uint32_t)(boxes * (D / 64) * R * 128));
+                                                  (uint32_t)(nbox * (D / 64) * R * 128));
                         else
                             mbar_arrive(&full[slot]);
                         __syncwarp();
                         for (int bx = lane; bx < nbox; bx += 32) {
-                            const int tok = key0 + bx * R;
-                            if (kWindow && !box_seen(tok))
-                                continue;
+                            const int tok = kWindow ? uw.key(key0 + bx * R) : key0 + bx * R;
                             const int pi = tok >> p.ps_shift;
                             int page = w.table_ok ? __ldg(p.kv_indices + w.pg0 + pi) : 0;
                             if (page < 0 || page >= p.num_pages) {
@@ -881,35 +889,39 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                                 tma_load_3d(dst + h * C::kRegionBytes + bx * R * 128, tmap, 64 * h,
                                             w.g, row, &full[slot]);
                         }
+                        load_ids(j + 1);
                     } else {
-                        size_t offs[C::kKeys / 8];
-                        unsigned live = 0u;
+                        // lane l finds the slots of keys l, 32 + l, 64 + l and 96 + l, from
+                        // page ids that were loaded a block ahead; -1: zeros
+                        int slots[C::kKeys / 32];
 #pragma unroll
-                        for (int kg = 0; kg < C::kKeys / 8; ++kg) {
-                            const int tok = key0 + kg * 8 + kl;
-                            offs[kg] = 0;
-                            if (tok < w.kv_end &&
-                                (!kWindow || tok < p.sinks || tok >= uw.low)) {
-                                const int pi =
-                                    p.ps_shift >= 0 ? (tok >> p.ps_shift) : (tok / p.page_size);
-                                const int sl = tok - pi * p.page_size;
-                                int page = w.table_ok ? __ldg(p.kv_indices + w.pg0 + pi) : 0;
+                        for (int k = 0; k < C::kKeys / 32; ++k) {
+                            const int i = key0 + k * 32 + lane;
+                            slots[k] = -1;
+                            if (i < n_keys) {
+                                const int tok = kWindow ? uw.key(i) : i;
+                                const int pi = page_of(tok);
+                                int page = ids[k];
                                 if (page < 0 || page >= p.num_pages) {
                                     tc_flag(p.status, kFlagBadPage);
                                     page = 0;
                                 }
-                                offs[kg] = (((size_t)page * p.page_size + sl) * p.Hkv + w.g) * D;
-                                live |= 1u << kg;
+                                slots[k] = page * p.page_size + tok - pi * p.page_size;
                             }
                         }
+                        load_ids(j + 1);
 #pragma unroll
                         for (int kg = 0; kg < C::kKeys / 8; ++kg) {
+                            const int at =
+                                __shfl_sync(kAllTc, slots[kg / 4], (kg & 3) * 8 + kl);
+                            const __nv_bfloat16 *src =
+                                pool + ((size_t)max(at, 0) * p.Hkv + w.g) * D + cl * 8;
                             const uint32_t row = dst + (kg * 8 + kl) * 128;
 #pragma unroll
                             for (int cq = 0; cq < CH / 4; ++cq) {
                                 const int c = 4 * cq + cl;
                                 cp_async16(row + (c >> 3) * C::kRegionBytes + (((c & 7) ^ kl) << 4),
-                                           pool + offs[kg] + c * 8, ((live >> kg) & 1u) ? 16u : 0u);
+                                           src + cq * 32, at >= 0 ? 16u : 0u);
                             }
                         }
                         cp_async_arrive(&full[slot]);
@@ -1003,9 +1015,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                     w.kv_end = rec[8];
                     w.kb0 = rec[10];
                     w.n_kb = rec[11];
-                    UnitWindow uw;
+                    int n_keys = w.kv_end;
                     if constexpr (kWindow)
-                        uw = unit_window(p, rec[5], rec[4], rec[6], rec[7]);
+                        n_keys -= unit_window(p, rec[5], rec[4], rec[6], rec[7]).off;
                     mbar_arrive(&rec_empty[rs]);
                     if (!have)
                         continue;
@@ -1032,11 +1044,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                         const bool more = j + 1 < n_kb;
                         // this run's data and P, waited for while the other
                         // tile's run is issued
-                        const int key0 =
-                            (kWindow ? uw.block(w.kb0 + j) : w.kb0 + j) * C::kKeys;
                         const bool v_gen =
-                            !p.use_tma || w.kv_end - key0 < C::kKeys ||
-                            (kWindow && !uw.whole(key0, C::kKeys, p.sinks));
+                            !p.use_tma || n_keys - (w.kb0 + j) * C::kKeys < C::kKeys;
                         if (!wait_only(&v_full[kj % VS], (uint32_t)((kj / VS) & 1)))
                             break;
                         if (more &&
@@ -1154,7 +1163,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 (t >= 0 && m < rows_used && tok_m < ntok) ? pos_first + tok_m : kNoQuery;
             float m_run = -INFINITY, l_run = 0.f;
             const int n_kb = rec[11];
-            UnitWindow uw;
+            UnitWindow uw{0, 0};
             if constexpr (kWindow)
                 uw = unit_window(p, rec[5], q_len, rec[6], rec[7]);
             // the partner half has read the previous unit's l (it loaded O
@@ -1176,20 +1185,23 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 tc_fence_after();
                 float sv[64];
                 tmem_ld64(t_s + 64 * h, sv);
-                const int key0 = (kWindow ? uw.block(rec[10] + j) : j) * C::kKeys + 64 * h;
+                // (with a window, entry i of this half of the unit's list stands for key
+                // key0 + i but for the sinks, of which a row sees i < sinks; behind them,
+                // no key of the list's head is one of a row's window)
+                const int key0 =
+                    (kWindow ? rec[10] + j : j) * C::kKeys + 64 * h + (kWindow ? uw.off : 0);
                 if (key0 + 63 > pos_first) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
                         sv[i] = key0 + i > pos ? -INFINITY : sv[i];
                 }
                 if constexpr (kWindow) {
-                    // keys under the window, behind the sinks; none of a tile whose last
-                    // query's window starts at or before the half's first key
-                    if (key0 < pos_first + ntok - p.window && key0 + 63 >= p.sinks) {
+                    const int sinks = p.sinks + uw.off;
+                    if (key0 < pos_first + ntok - p.window && key0 + 63 >= sinks) {
                         const int under = pos - p.window;
 #pragma unroll
                         for (int i = 0; i < 64; ++i)
-                            sv[i] = key0 + i <= under && key0 + i >= p.sinks ? -INFINITY : sv[i];
+                            sv[i] = key0 + i <= under && key0 + i >= sinks ? -INFINITY : sv[i];
                     }
                 }
                 // this half's max: three-input max over 8 independent chains
