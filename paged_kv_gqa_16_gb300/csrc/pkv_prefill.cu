@@ -403,30 +403,13 @@ struct PrefillUnit {
     // a part of a split unit: slot << 9 | parts << 4 | part; -1 for a whole unit
     int part_id;
     bool table_ok;
-};
-
-// A unit's keys under a window, as a list without the keys that no query of the unit
-// sees: entry i is key i of the first `head`, key i + off behind them.  Both parts
-// are whole boxes of the copies (pages, or parts of one), so some keys at the ends
-// are there without being seen; the softmax masks them.
-struct UnitWindow {
-    int head, off;
+    // With a window the unit's keys are a list without those that none of its queries
+    // sees: entry i is key i of the first `head`, key i + off behind them.  Both parts
+    // are whole boxes of the copies (pages, or parts of one), so some keys at their
+    // ends are there without being seen; the softmax masks them.
+    int off, head;
     __device__ __forceinline__ int key(int i) const { return i < head ? i : i + off; }
 };
-
-__device__ __forceinline__ UnitWindow unit_window(const PrefillParams &p, int L, int q_len, int tA,
-                                                  int tB)
-{
-    UnitWindow u;
-    const int mask = p.use_tma ? p.tma_rows - 1 : 0;
-    // the first key of the first query's window
-    const int low = max(0, L - q_len + max(tA, tA < 0 ? tB : 0) * p.tq - p.window + 1);
-    u.head = (min(p.sinks, low) + mask) & ~mask;
-    u.off = max(0, (low & ~mask) - u.head);
-    if (u.off == 0)
-        u.head = 0;                    // one run of keys from 0
-    return u;
-}
 
 // Wait for phase `parity` of `bar`; false if the time limit ran out or
 // another role aborted.  The abort flag is read only once the phase is not
@@ -552,9 +535,17 @@ __device__ __forceinline__ bool prefill_whole_unit(const PrefillParams &p, int u
         return false;
     w.tA = w.tB - 1;
     w.kv_end = w.L - w.q_len + min(w.q_len, (w.tB + 1) * p.tq);
-    w.n_kb = (w.kv_end + 127) / 128;
-    if constexpr (kWindow)
-        w.n_kb = (w.kv_end - unit_window(p, w.L, w.q_len, w.tA, w.tB).off + 127) / 128;
+    w.off = w.head = 0;
+    if constexpr (kWindow) {
+        const int mask = p.use_tma ? p.tma_rows - 1 : 0;
+        // the first key of the first query's window
+        const int low = max(0, w.L - w.q_len + max(w.tA, w.tA < 0 ? w.tB : 0) * p.tq - p.window + 1);
+        const int head = (min(p.sinks, low) + mask) & ~mask;
+        const int off = (low & ~mask) - head;
+        if (off > 0)                   // (else one run of keys from 0)
+            w.off = off, w.head = head;
+    }
+    w.n_kb = (w.kv_end - w.off + 127) / 128;
     w.kb0 = 0;
     w.part_id = -1;
     w.pg0 = k0;
@@ -609,6 +600,8 @@ __device__ __forceinline__ void unit_to_rec(int *rec, bool have, const PrefillUn
     rec[11] = w.n_kb;
     rec[12] = w.part_id;
     rec[13] = w.table_ok ? 1 : 0;
+    rec[14] = w.off;
+    rec[15] = w.head;
 }
 
 __device__ __forceinline__ bool rec_to_unit(const int *rec, PrefillUnit &w)
@@ -626,6 +619,8 @@ __device__ __forceinline__ bool rec_to_unit(const int *rec, PrefillUnit &w)
     w.n_kb = rec[11];
     w.part_id = rec[12];
     w.table_ok = rec[13] != 0;
+    w.off = rec[14];
+    w.head = rec[15];
     return rec[0] != 0;
 }
 
@@ -830,25 +825,21 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 }
                 if (is_v)
                     ++qit;
-                UnitWindow uw{0, 0};
-                if constexpr (kWindow)
-                    uw = unit_window(p, w.L, w.q_len, w.tA, w.tB);
-                const int n_keys = kWindow ? w.kv_end - uw.off : w.kv_end;
+                const int n_keys = kWindow ? w.kv_end - w.off : w.kv_end;
                 // the page ids of block j's keys l, 32 + l, ..., where it is copied key by key
                 int ids[C::kKeys / 32];
                 auto load_ids = [&](int j) {
                     const int key0 = (w.kb0 + j) * C::kKeys;
-                    if (j >= w.n_kb || (p.use_tma && (!is_v || n_keys - key0 >= C::kKeys)))
-                        return;
 #pragma unroll
                     for (int k = 0; k < C::kKeys / 32; ++k) {
                         const int i = key0 + k * 32 + lane;
                         ids[k] = w.table_ok && i < n_keys
                                      ? __ldg(p.kv_indices + w.pg0 +
-                                             page_of(kWindow ? uw.key(i) : i)) : 0;
+                                             page_of(kWindow ? w.key(i) : i)) : 0;
                     }
                 };
-                load_ids(0);
+                if (!p.use_tma)
+                    load_ids(0);
                 for (int j = 0; j < w.n_kb; ++j) {
                     const int slot = kb % ns;
                     if (kb >= ns) {
@@ -876,7 +867,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                             mbar_arrive(&full[slot]);
                         __syncwarp();
                         for (int bx = lane; bx < nbox; bx += 32) {
-                            const int tok = kWindow ? uw.key(key0 + bx * R) : key0 + bx * R;
+                            const int tok = kWindow ? w.key(key0 + bx * R) : key0 + bx * R;
                             const int pi = tok >> p.ps_shift;
                             int page = w.table_ok ? __ldg(p.kv_indices + w.pg0 + pi) : 0;
                             if (page < 0 || page >= p.num_pages) {
@@ -889,8 +880,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                                 tma_load_3d(dst + h * C::kRegionBytes + bx * R * 128, tmap, 64 * h,
                                             w.g, row, &full[slot]);
                         }
-                        load_ids(j + 1);
                     } else {
+                        if (p.use_tma)
+                            load_ids(j);           // a partial block of V, the unit's last
+
                         // lane l finds the slots of keys l, 32 + l, 64 + l and 96 + l, from
                         // page ids that were loaded a block ahead; -1: zeros
                         int slots[C::kKeys / 32];
@@ -899,7 +892,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                             const int i = key0 + k * 32 + lane;
                             slots[k] = -1;
                             if (i < n_keys) {
-                                const int tok = kWindow ? uw.key(i) : i;
+                                const int tok = kWindow ? w.key(i) : i;
                                 const int pi = page_of(tok);
                                 int page = ids[k];
                                 if (page < 0 || page >= p.num_pages) {
@@ -909,7 +902,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                                 slots[k] = page * p.page_size + tok - pi * p.page_size;
                             }
                         }
-                        load_ids(j + 1);
+                        if (!p.use_tma)
+                            load_ids(j + 1);
 #pragma unroll
                         for (int kg = 0; kg < C::kKeys / 8; ++kg) {
                             const int at =
@@ -1012,12 +1006,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                         break;
                     const bool have = rec[0] != 0;
                     PrefillUnit w;
-                    w.kv_end = rec[8];
                     w.kb0 = rec[10];
                     w.n_kb = rec[11];
-                    int n_keys = w.kv_end;
-                    if constexpr (kWindow)
-                        n_keys -= unit_window(p, rec[5], rec[4], rec[6], rec[7]).off;
+                    const int n_keys = kWindow ? rec[8] - rec[14] : rec[8];
                     mbar_arrive(&rec_empty[rs]);
                     if (!have)
                         continue;
@@ -1163,9 +1154,6 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 (t >= 0 && m < rows_used && tok_m < ntok) ? pos_first + tok_m : kNoQuery;
             float m_run = -INFINITY, l_run = 0.f;
             const int n_kb = rec[11];
-            UnitWindow uw{0, 0};
-            if constexpr (kWindow)
-                uw = unit_window(p, rec[5], q_len, rec[6], rec[7]);
             // the partner half has read the previous unit's l (it loaded O
             // after it) before this unit's first max overwrites it
             if (!C::kOnesL && it > 0) {
@@ -1189,14 +1177,14 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 // key0 + i but for the sinks, of which a row sees i < sinks; behind them,
                 // no key of the list's head is one of a row's window)
                 const int key0 =
-                    (kWindow ? rec[10] + j : j) * C::kKeys + 64 * h + (kWindow ? uw.off : 0);
+                    (kWindow ? rec[10] + j : j) * C::kKeys + 64 * h + (kWindow ? rec[14] : 0);
                 if (key0 + 63 > pos_first) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
                         sv[i] = key0 + i > pos ? -INFINITY : sv[i];
                 }
                 if constexpr (kWindow) {
-                    const int sinks = p.sinks + uw.off;
+                    const int sinks = p.sinks + rec[14];
                     if (key0 < pos_first + ntok - p.window && key0 + 63 >= sinks) {
                         const int under = pos - p.window;
 #pragma unroll
