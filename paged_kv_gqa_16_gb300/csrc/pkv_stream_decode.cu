@@ -124,15 +124,30 @@ __device__ __forceinline__ Shifts shifts()
     return {one << 4, one << 7, one << 12, one << 15, one << 16, one << 23};
 }
 
+// The bytes' low halves of a, their high halves of b.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xe4;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// max(a, b, c) in one instruction.
+__device__ __forceinline__ float fmax3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // A transposed word holds four codes of two tokens, A0 .. A3 in its low half, B0 ..
 // B3 in its high half.  `even` and `odd` hold (A0, B0), (A2, B2) and (A1, B1), (A3, B3)
 // in bytes 2 and 3.
 __device__ __forceinline__ void two_tokens(uint32_t w, const Shifts &by, uint32_t &even,
                                            uint32_t &odd)
 {
-    const uint32_t w16 = w * by.by16, w4 = w * by.by4, w12 = w * by.by12;
-    even = (w16 & 0x0f0f0f0fu) | (w4 & 0xf0f0f0f0u);
-    odd = (w12 & 0x0f0f0f0fu) | (w & 0xf0f0f0f0u);
+    even = low_halves(w * by.by16, w * by.by4);
+    odd = low_halves(w * by.by12, w);
 }
 
 template <int N>
@@ -550,9 +565,9 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                 auto in = [&](int t) { return t < left; };
                 // scores (log2 domain) of rows g, g + 8 (x >> 1) and heads 2c, 2c + 1 (x & 1)
                 float y[NT][U][4];
-                // 4 bits: the tokens' scale words of V, and 2^-ev
+                // 4 bits: the tokens' scale words of V, and the scores y - ev without them
                 uint32_t wv[U][2];
-                float inv_v[U][2];
+                float x_[NT][U][4];
                 if constexpr (BITS == 16) {
                     float sacc[NT][4] = {};
 #pragma unroll
@@ -642,17 +657,21 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                         for (int k = 0; k < 2; ++k) {
                             float top = fmaxf(scale_of<0>(wv[u][k], by), scale_of<1>(wv[u][k], by));
                             if constexpr (G32 == 4)
-                                top = fmaxf(top, fmaxf(scale_of<2>(wv[u][k], by),
-                                                       scale_of<3>(wv[u][k], by)));
-                            const unsigned bits = __float_as_uint(top);
-                            // (2^23 + byte) - (2^23 + 127)
-                            const float ev = __uint_as_float(0x4b000000u | bits >> 23) - 8388735.f;
-                            inv_v[u][k] = __uint_as_float(0x7f000000u - bits);
+                                top = fmax3(top, scale_of<2>(wv[u][k], by),
+                                            scale_of<3>(wv[u][k], by));
+                            // 2^23 + 128 times its byte, as a float: the upper half of its
+                            // bits, and from there the exponent ev = byte - 127
+                            const float up = __uint_as_float(
+                                __byte_perm(__float_as_uint(top), 0x4b000000u, 0x7632));
+                            const float ev = fmaf(up, 0x1p-7f, -(65536.f + 127.f));
+                            const float nan = top - top;      // of scale 255, else 0
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    y[nt][u][2 * k + e] = fmaf(s[nt][u][2 * k + e], cq[nt][e], ev);
+                                for (int e = 0; e < 2; ++e) {
+                                    x_[nt][u][2 * k + e] = fmaf(s[nt][u][2 * k + e], cq[nt][e], nan);
+                                    y[nt][u][2 * k + e] = x_[nt][u][2 * k + e] + ev;
+                                }
                         }
                     if (cut) {
 #pragma unroll
@@ -660,10 +679,11 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
                                 if (!in(u * 16 + k * 8 + g)) {
-                                    inv_v[u][k] = 0.f;
 #pragma unroll
                                     for (int nt = 0; nt < NT; ++nt)
-                                        y[nt][u][2 * k] = y[nt][u][2 * k + 1] = -INFINITY;
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e)
+                                            x_[nt][u][2 * k + e] = y[nt][u][2 * k + e] = -INFINITY;
                                 }
                     }
                 }
@@ -708,10 +728,11 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            w[nt][u][x] = exp2_ftz(y[nt][u][x] - base[nt][x & 1]);
                             if constexpr (BITS == 4) {
-                                w[nt][u][x] *= inv_v[u][x >> 1];
+                                w[nt][u][x] = exp2_ftz(x_[nt][u][x] - base[nt][x & 1]);
                                 l_run[nt][x & 1] += w[nt][u][x];
+                            } else {
+                                w[nt][u][x] = exp2_ftz(y[nt][u][x] - base[nt][x & 1]);
                             }
                         }
                 }
