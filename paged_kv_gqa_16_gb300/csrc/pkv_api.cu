@@ -1309,14 +1309,16 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
     return PKV_OK;
 }
 
-// Rows x kv-head groups whose rows the stream decode takes whole, by the bytes of
-// K and V that a row's last token sees (kStreamWholeBytes).
+// Whether the stream decode takes whole rows, by the bytes of K and V that a row's
+// last token sees (kQ4WholeBytes and the others).
 static bool stream_whole(const pkv_dims *dims, int hpc, int bits, int most_seen, int sms)
 {
     const long long rows = (long long)dims->B * (dims->Hkv / hpc);
     const long long head = bits == 4 ? dims->D / 2 + dims->D / 32 : dims->D * 2;
-    return (long long)most_seen * hpc * head * 2 <=
-           (2 * rows >= sms ? 2 : 1) * pkv::kStreamWholeBytes;
+    const long long most = bits == 4 ? pkv::kQ4WholeBytes
+                           : hpc * head >= pkv::kBulkRowBytes ? pkv::kBulkWholeBytes
+                                                              : pkv::kLinesWholeBytes;
+    return most_seen * hpc * head * 2 <= (2 * rows >= sms ? 2 : 1) * most;
 }
 
 // Decode over a 4-bit cache (bits 4) or bf16 pools; window 0: all tokens.

@@ -300,7 +300,21 @@ constexpr int kQ8MaxRows = 1024;
 // tokens are skipped.  f.k_codes and f.v_codes are the pools of either kind.
 constexpr int kQ4RowCost = 64;
 constexpr int kWindowRowCost = 32;
-constexpr long long kStreamWholeBytes = 256 << 10;
+// Rows of which at most this many bytes (K and V of a block's kv heads) are seen are
+// not split, and twice as many where there are rows x kv-head groups for half the SMs.
+// Unsplit against split, us:
+//   4 bits, 8 heads of 128, 128 tokens (136 KB): 1 row 8.6, 9.0; 76 rows 8.8, 11.2; 512
+//   rows 27.1, 33.8.  256 (272 KB): 12.8, 9.2; 13.0, 13.2; 43.7, 48.5.  512: 21.4, 9.6;
+//   21.9, 17.8; 78.3, 77.9.  1 head of 64, 1 row of 1,024 (68 KB) 9.1, 7.8; 76 rows 9.4,
+//   10.8.
+//   bf16, 8 heads of 128 (bulk copies), 128 tokens (512 KB): 1 row 9.6, 9.4; 76 rows
+//   12.4, 14.7; 512 rows 46.1, 51.1.  256: 15.0, 9.6; 20.0, 20.0; 85.5, 88.7.  8 heads
+//   of 64, 64 tokens (128 KB): 8.0, 8.0; 8.1, 9.9.  128: 11.0, 9.7; 11.3, 12.2.
+constexpr long long kQ4WholeBytes = 128 << 10;
+constexpr long long kBulkWholeBytes = 512 << 10;
+constexpr long long kLinesWholeBytes = 192 << 10;
+// Rows of K (or V) that are copied by one bulk copy each: a token's kv heads of a block.
+constexpr int kBulkRowBytes = 2048;
 struct StreamParams {
     FusedParams f;
     int bits;              // 16 (bf16 pools) or 4 (codes and scales)

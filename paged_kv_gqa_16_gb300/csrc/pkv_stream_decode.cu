@@ -62,7 +62,7 @@ struct StreamCfg {
     // Rows of 2 KB go by one bulk copy each, with a pitch that spreads them over the
     // banks: a lane's instruction in place of four of a warp.  (Shorter ones would be
     // slower so: the copy engine takes about 24 copies a microsecond and SM.)
-    static constexpr bool kBulk = BITS == 16 && kRowBytes >= 2048;
+    static constexpr bool kBulk = BITS == 16 && kRowBytes >= kBulkRowBytes;
     static_assert(!kBulk || kTok == 16, "a lane copies a row of K or of V");
     static constexpr int kPitch = kBulk ? kRowBytes + 16 : kRowBytes;
     static constexpr int kStageBytes = 2 * kTok * kPitch;

@@ -168,15 +168,16 @@ def _ptr(x) -> Optional[int]:
 
 # torch's types of bf16, fp32, e4m3 codes and e8m0 scales (set when torch is first needed)
 _bf16 = _fp32 = None
-_codes = _scales = ()
+_codes = _scales = _bytes = ()
 
 
 def _load_types():
-    global _bf16, _fp32, _codes, _scales
+    global _bf16, _fp32, _codes, _scales, _bytes
     import torch
     _bf16, _fp32 = torch.bfloat16, torch.float32
     _codes = torch.float8_e4m3fn, torch.uint8, torch.int8
     _scales = torch.float8_e8m0fnu, torch.uint8, torch.int8
+    _bytes = torch.uint8, torch.int8
 
 
 def _pool_ptr(d: Dims, x) -> Optional[int]:
@@ -224,21 +225,26 @@ def _q8_ptrs(k, v, ks, vs):
     return _q8_ptr(k, _codes), _q8_ptr(v, _codes), _q8_ptr(ks, _scales), _q8_ptr(vs, _scales)
 
 
-def _q4_ptr(x, at_least: int) -> Optional[int]:
-    if x is None or x.__class__ is int:
-        return x
-    if x.element_size() == 1 and x.numel() >= at_least and x.is_contiguous():
-        return x.data_ptr()
-    raise ValueError("a 4-bit cache has contiguous byte tensors, codes [num_pages, page_size, Hkv, D / 2] and "
-                     f"scales [num_pages, page_size, Hkv, D / 32]: got {x.dtype} {tuple(x.shape)}")
-
-
-def _q4_ptrs(d: Dims, k, v, ks, vs):
-    """The pointers of a 4-bit cache's codes and scales (their sizes are checked: an
-    8-bit cache has the same types)."""
-    heads = d.num_pages * d.page_size * d.Hkv
-    codes, scales = heads * (d.D // 2), heads * (d.D // 32)
-    return _q4_ptr(k, codes), _q4_ptr(v, codes), _q4_ptr(ks, scales), _q4_ptr(vs, scales)
+def _q4_ptrs(k, v, ks, vs):
+    """The pointers of a 4-bit cache's codes and scales: bytes, 16 of codes for one of
+    scales (an 8-bit cache's have the same types, and other sizes)."""
+    try:
+        n = k.numel()
+        if (n == v.numel() == 16 * ks.numel() == 16 * vs.numel() and k.dtype in _bytes and
+                v.dtype in _bytes and ks.dtype in _scales and vs.dtype in _scales and
+                k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and
+                vs.is_contiguous()):
+            return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
+    except AttributeError:                        # raw pointers, or a None among tensors
+        if all(x is None or x.__class__ is int for x in (k, v, ks, vs)):
+            return k, v, ks, vs
+        raise ValueError("a 4-bit cache is four tensors, or four pointers") from None
+    if _bf16 is None:
+        _load_types()
+        return _q4_ptrs(k, v, ks, vs)
+    raise ValueError("a 4-bit cache has contiguous uint8 codes [num_pages, page_size, Hkv, D / 2] and e8m0 "
+                     "scales [num_pages, page_size, Hkv, D / 32] (uint8 or torch.float8_e8m0fnu), got "
+                     f"{[(x.dtype, tuple(x.shape)) for x in (k, v, ks, vs)]}")
 
 
 def _find_current_stream():
@@ -619,7 +625,7 @@ def paged_kv_append_q4(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, k
     [num_pages, page_size, Hkv, D / 32] (uint8 or torch.float8_e8m0fnu)."""
     _token_count(d, t, per_row=True)
     _check("paged_kv_append_q4", lib().paged_kv_append_q4(
-        ctypes.byref(d), ctypes.byref(t), *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        ctypes.byref(d), ctypes.byref(t), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -628,7 +634,7 @@ def paged_kv_extend_q4(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale,
     """paged_kv_append_q4 for ragged chunks of new tokens."""
     _check("paged_kv_extend_q4", lib().paged_kv_extend_q4(
         ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
-        *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
+        *_q4_ptrs(k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
         _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -636,7 +642,7 @@ def paged_kv_read_q4(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv
                      seq_lens, k_out, v_out, status=None, stream=None) -> None:
     """paged_kv_read_q8 of a 4-bit cache."""
     _check("paged_kv_read_q4", lib().paged_kv_read_q4(
-        ctypes.byref(d), *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        ctypes.byref(d), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out), _bf16_ptr(v_out),
         _ptr(status), _stream(stream)))
 
@@ -648,7 +654,7 @@ def paged_decode_attn_q4(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indi
     `window` tokens and its first `sinks`."""
     ws_bytes = workspace.numel() * workspace.element_size()
     _check("paged_decode_attn_q4", lib().paged_decode_attn_q4(
-        ctypes.byref(d), _bf16_ptr(q), *_q4_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        ctypes.byref(d), _bf16_ptr(q), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits,
         _ptr(workspace), ws_bytes, _bf16_ptr(out), _stream(stream)))
 

@@ -72,15 +72,20 @@ def test_read_refusals():
 
 
 def test_tensors_of_another_cache_are_refused():
-    """An 8-bit cache has byte tensors too, and scales for a head vector: too few."""
-    d = _d(num_pages=2)
+    """An 8-bit cache has byte tensors too, and one scale for a head vector: too few."""
     codes = torch.zeros(2, 16, 8, 64, dtype=torch.uint8)
     scale = torch.zeros(2, 16, 8, 4, dtype=torch.uint8)
-    assert pkv._q4_ptrs(d, codes, codes, scale, scale) == (codes.data_ptr(),) * 2 + (scale.data_ptr(),) * 2
+    want = (codes.data_ptr(),) * 2 + (scale.data_ptr(),) * 2
+    assert pkv._q4_ptrs(codes, codes, scale, scale) == want
+    e8m0 = scale.view(torch.float8_e8m0fnu)
+    assert pkv._q4_ptrs(codes, codes, e8m0, e8m0) == want
+    assert pkv._q4_ptrs(FAKE, FAKE, FAKE, None) == (FAKE, FAKE, FAKE, None)
     for bad in ([codes, codes, scale[..., 0].contiguous(), scale], [codes[:1], codes, scale, scale],
-                [codes.to(torch.bfloat16), codes, scale, scale], [codes, codes.transpose(1, 2), scale, scale]):
+                [codes.to(torch.bfloat16), codes, scale, scale], [codes, codes.transpose(1, 2), scale, scale],
+                [codes.view(torch.float8_e4m3fn), codes, scale, scale], [codes, None, scale, scale],
+                [codes, codes, scale, FAKE]):
         with pytest.raises(ValueError):
-            pkv._q4_ptrs(d, *bad)
+            pkv._q4_ptrs(*bad)
 
 
 @pytest.mark.parametrize("name", ["paged_decode_attn_q4", "paged_decode_attn_window"])
