@@ -1178,18 +1178,37 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                 // no key of the list's head is one of a row's window)
                 const int key0 =
                     (kWindow ? rec[10] + j : j) * C::kKeys + 64 * h + (kWindow ? rec[14] : 0);
-                if (key0 + 63 > pos_first) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        sv[i] = key0 + i > pos ? -INFINITY : sv[i];
-                }
-                if constexpr (kWindow) {
-                    const int sinks = p.sinks + rec[14];
-                    if (key0 < pos_first + ntok - p.window && key0 + 63 >= sinks) {
-                        const int under = pos - p.window;
+                if constexpr (!kWindow) {
+                    if (key0 + 63 > pos_first) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i)
-                            sv[i] = key0 + i <= under && key0 + i >= sinks ? -INFINITY : sv[i];
+                            sv[i] = key0 + i > pos ? -INFINITY : sv[i];
+                    }
+                } else {
+                    // eight keys at a time that are past some row's of the warp, or under
+                    // some row's window (the rows' positions do not decrease over the lanes;
+                    // rows with no query need no mask: their outputs are not stored)
+                    const int sinks = p.sinks + rec[14];
+                    if (key0 + 63 > pos_first) {
+                        const int first = pos_first + __shfl_sync(kAllTc, tok_m, 0) - key0;
+#pragma unroll
+                        for (int g = 0; g < 64; g += 8)
+                            if (g + 7 > first) {
+#pragma unroll
+                                for (int i = g; i < g + 8; ++i)
+                                    sv[i] = key0 + i > pos ? -INFINITY : sv[i];
+                            }
+                    }
+                    if (key0 < pos_first + ntok - p.window && key0 + 63 >= sinks) {
+                        const int last = pos_first + __shfl_sync(kAllTc, tok_m, 31) - p.window - key0;
+                        const int under = pos - p.window;
+#pragma unroll
+                        for (int g = 0; g < 64; g += 8)
+                            if (g <= last && key0 + g + 7 >= sinks) {
+#pragma unroll
+                                for (int i = g; i < g + 8; ++i)
+                                    sv[i] = key0 + i <= under && key0 + i >= sinks ? -INFINITY : sv[i];
+                            }
                     }
                 }
                 // this half's max: three-input max over 8 independent chains
