@@ -157,7 +157,9 @@ using Const = std::integral_constant<int, N>;
 template <int B>
 __device__ __forceinline__ float scale_of(uint32_t w, const Shifts &by)
 {
-    const uint32_t at = B == 0 ? w * by.by23 : B == 1 ? w * by.by15 : B == 2 ? w * by.by7 : w >> 1;
+    if constexpr (B == 3)
+        return __uint_as_float(__byte_perm(w, 0, 0x4443) * by.by23);
+    const uint32_t at = w * (B == 0 ? by.by23 : B == 1 ? by.by15 : by.by7);
     return __uint_as_float(at & 0x7f800000u);
 }
 
@@ -687,15 +689,17 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                                 }
                     }
                 }
-                bool raise = false;
+                // (a score past its limit: the sign of a difference, as the
+                // comparison would be on the pipe that is short)
+                unsigned raise = 0;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            raise |= y[nt][u][x] > limit[nt][x & 1];
-                if (__any_sync(kFull, raise)) {
+                            raise |= __float_as_uint(limit[nt][x & 1] - y[nt][u][x]);
+                if (__any_sync(kFull, (int)raise < 0)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
