@@ -13,7 +13,7 @@
 //             32 elements.  A step of these codes is up to half their value, so
 //             a key next to a border is decided as the exact value is: where 32
 //             bits do not tell (their error against the distance, one warp's
-//             round in some hundreds) the warp forms its vectors in 64.
+//             round in some hundreds) the warp forms its vectors again in 46.
 //
 // The pass reads and writes every value once and is bound by memory, if the
 // arithmetic is kept small: a head vector belongs to a group of D / 8 lanes with
@@ -271,24 +271,19 @@ __device__ __forceinline__ uint4 pack(const Eight &x, float f)
                       pack_bf16x2(a1.x, b1.x), pack_bf16x2(a1.y, b1.y));
 }
 
-// x f, in order.
-__device__ __forceinline__ void values_of(const Eight &x, float f, float (&y)[8])
+// x f.
+__device__ __forceinline__ Eight scaled(const Eight &x, float f)
 {
     const F2 ff = f2(f, f);
-    const float2 a0 = parts(mul2(x.a[0], ff)), a1 = parts(mul2(x.a[1], ff));
-    const float2 b0 = parts(mul2(x.b[0], ff)), b1 = parts(mul2(x.b[1], ff));
-    y[0] = a0.x, y[1] = b0.x, y[2] = a0.y, y[3] = b0.y;
-    y[4] = a1.x, y[5] = b1.x, y[6] = a1.y, y[7] = b1.y;
+    return {{mul2(x.a[0], ff), mul2(x.a[1], ff)}, {mul2(x.b[0], ff), mul2(x.b[1], ff)}};
 }
 
-// The pairs' sums of magnitudes, times f.
-__device__ __forceinline__ void pair_sizes(const Eight &x, float f, float (&s)[4])
+// The eight values in order.
+__device__ __forceinline__ void values_of(const Eight &x, float (&y)[8])
 {
     const float2 a0 = parts(x.a[0]), a1 = parts(x.a[1]), b0 = parts(x.b[0]), b1 = parts(x.b[1]);
-    s[0] = (fabsf(a0.x) + fabsf(b0.x)) * f;
-    s[1] = (fabsf(a0.y) + fabsf(b0.y)) * f;
-    s[2] = (fabsf(a1.x) + fabsf(b1.x)) * f;
-    s[3] = (fabsf(a1.y) + fabsf(b1.y)) * f;
+    y[0] = a0.x, y[1] = b0.x, y[2] = a0.y, y[3] = b0.y;
+    y[4] = a1.x, y[5] = b1.x, y[6] = a1.y, y[7] = b1.y;
 }
 
 // x f as codes and the scale byte of the group's vector.
@@ -307,18 +302,12 @@ __device__ __forceinline__ uint2 quantise(const Eight &x, float f, int &sb)
     return q8_encode8(y, f, sb, amax == INFINITY);
 }
 
-// The nearest float toward zero, its last bit set if x is not that float: rounding
-// it to fewer bits, and comparing it with numbers of fewer bits, give what x gives.
-__device__ __forceinline__ float odd_of(double x)
-{
-    const float f = __double2float_rz(x);
-    return __uint_as_float(__float_as_uint(f) | ((double)f != x ? 1u : 0u));
-}
-
 // The largest magnitude of the 32 elements of a scale, four lanes', as bits (of
 // which those of a NaN and of infinity are the largest).
-__device__ __forceinline__ unsigned scale_group_max(const float (&y)[8])
+__device__ __forceinline__ unsigned scale_group_max(const Eight &x)
 {
+    float y[8];
+    values_of(x, y);
     unsigned m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -328,89 +317,146 @@ __device__ __forceinline__ unsigned scale_group_max(const float (&y)[8])
 }
 
 // Eight codes of y at scale byte sb (255: zero codes).
-__device__ __forceinline__ uint32_t q4_encode8(const float (&y)[8], int sb)
+__device__ __forceinline__ uint32_t q4_encode8(const Eight &y, int sb)
 {
-    const float by = q4_unscale(sb);
     float z[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        z[j] = y[j] * by;
+    values_of(scaled(y, q4_unscale(sb)), z);
     return sb == 255 ? 0u : e2m1x8(z);
 }
 
-// A lane's eight key codes, and their scale byte, from its values in 64 bits: for
-// codes that lie too near a border for 32.  Rare (under 1% of a warp's rounds), so it
-// reads the weight and the rotation again.  1 / sqrt from the 32-bit one by two
-// Newton steps.
+// A number as the sum of two floats, the second the first's rounding error: about 46
+// bits, in the operations of 32.
+struct Two {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Two two_product(float a, float b)
+{
+    const float p = __fmul_rn(a, b);
+    return {p, __fmaf_rn(a, b, -p)};
+}
+
+__device__ __forceinline__ Two two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+
+// The float toward zero of x, its last bit set if x is not that float: rounding it to
+// fewer bits, and comparing it with numbers of fewer bits, give what x gives.
+__device__ __forceinline__ float odd_of(Two x)
+{
+    x = two_sum(x.hi, x.lo);
+    const unsigned u = __float_as_uint(x.hi);
+    if (!(x.lo != 0.f) || !(fabsf(x.hi) < INFINITY))
+        return x.hi;
+    return __uint_as_float((x.lo < 0.f) == (x.hi < 0.f) ? u | 1u : (u - 1u) | 1u);
+}
+
+// A lane's eight key codes, and their scale byte, from values of 46 bits: for codes
+// that lie too near a border for 24.  Rare (under 1% of a warp's rounds), so it reads
+// the weight and the rotation again.  1 / sqrt from the 32-bit one by a step of Newton's
+// with the second-order term.  (In 64-bit operations: 25.7 us for the 9,537 tokens of D =
+// 64 above in place of 22.6; this GPU has few of them.)
 template <int D>
-__device__ __noinline__ uint2 key_codes_in_64(const __nv_bfloat16 *weight, const float *cos_sin,
+__device__ __noinline__ uint2 key_codes_exact(const __nv_bfloat16 *weight, const float *cos_sin,
                                               float eps, uint4 raw)
 {
     constexpr int LANES = D / 8;
     const int lane = threadIdx.x % LANES;
     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    double x[8];
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         x[2 * i] = bf16_lo(in[i]), x[2 * i + 1] = bf16_hi(in[i]);
-    double r = 1.0;
-    float y[8];
-    if (weight != nullptr) {
-        double s = 0.0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            s = fma(x[j], x[j], s);
-#pragma unroll
-        for (int m = 1; m < LANES; m <<= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, m);
-        s = s * (1.0 / D) + (double)eps;
-        const float r32 = rsqrtf((float)s);
-        r = r32;
-        if (r32 > 0.f && r32 < INFINITY) {          // (else as in 32 bits)
-            r = r * (1.5 - 0.5 * s * r * r);
-            r = r * (1.5 - 0.5 * s * r * r);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] *= (double)__bfloat162float(weight[lane * 8 + j]);
+    float4 cs[2] = {make_float4(1.f, 0.f, 1.f, 0.f), make_float4(1.f, 0.f, 1.f, 0.f)};
+    if (cos_sin != nullptr) {
+        cs[0] = reinterpret_cast<const float4 *>(cos_sin)[2 * lane];
+        cs[1] = reinterpret_cast<const float4 *>(cos_sin)[2 * lane + 1];
     }
+    Two r{1.f, 0.f};
+    if (weight != nullptr) {
+        const uint4 w = reinterpret_cast<const uint4 *>(weight)[lane];
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        Two s{0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        double a = x[2 * i], b = x[2 * i + 1];
-        if (cos_sin != nullptr) {
-            const double c = cos_sin[lane * 8 + 2 * i], t = cos_sin[lane * 8 + 2 * i + 1];
-            const double u = a * c - b * t;
-            b = a * t + b * c;
-            a = u;
+        for (int j = 0; j < 8; ++j) {
+            const Two t = two_sum(s.hi, __fmul_rn(x[j], x[j]));       // (squares of 8 bits: exact)
+            s = {t.hi, __fadd_rn(s.lo, t.lo)};
         }
-        y[2 * i] = odd_of(a * r);
-        y[2 * i + 1] = odd_of(b * r);
+#pragma unroll
+        for (int m = 1; m < LANES; m <<= 1) {
+            const float hi = __shfl_xor_sync(0xffffffffu, s.hi, m);
+            const float lo = __shfl_xor_sync(0xffffffffu, s.lo, m);
+            const Two t = two_sum(s.hi, hi);
+            s = {t.hi, __fadd_rn(__fadd_rn(s.lo, lo), t.lo)};
+        }
+        const Two t = two_sum(__fmul_rn(s.hi, 1.f / D), eps);
+        s = two_sum(t.hi, __fmaf_rn(s.lo, 1.f / D, t.lo));
+        r.hi = rsqrtf(s.hi);
+        if (r.hi > 0.f && r.hi < INFINITY) {         // (else as in 32 bits)
+            // e = 1 - s r^2, r (1 + e / 2 + 3 e^2 / 8)
+            const Two q = two_product(r.hi, r.hi), p = two_product(s.hi, q.hi);
+            const float rest = __fmaf_rn(s.hi, q.lo, __fmaf_rn(s.lo, q.hi, p.lo));
+            const float e = __fsub_rn(__fsub_rn(1.f, p.hi), rest);
+            r.lo = __fmul_rn(r.hi, __fmul_rn(e, __fmaf_rn(e, 0.375f, 0.5f)));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                // (16 bits: exact)
+            x[2 * i] = __fmul_rn(x[2 * i], bf16_lo(ws[i]));
+            x[2 * i + 1] = __fmul_rn(x[2 * i + 1], bf16_hi(ws[i]));
+        }
+    }
+    // (a c - b s) r and the like
+    auto value = [&](float a, float c, float b, float s) {
+        if (cos_sin == nullptr)
+            c = 1.f, b = 0.f, s = 0.f;               // (0 times an infinity stays out)
+        const Two p = two_product(a, c), q = two_product(b, s), d = two_sum(p.hi, q.hi);
+        const float lo = __fadd_rn(d.lo, __fadd_rn(p.lo, q.lo));
+        const Two m = two_product(d.hi, r.hi);
+        return odd_of({m.hi, __fmaf_rn(d.hi, r.lo, __fmaf_rn(lo, r.hi, m.lo))});
+    };
+    Eight y;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 t = cs[i];
+        const float *v = x + 4 * i;
+        y.a[i] = f2(value(v[0], t.x, v[1], -t.y), value(v[2], t.z, v[3], -t.w));
+        y.b[i] = f2(value(v[1], t.x, v[0], t.y), value(v[3], t.z, v[2], t.w));
     }
     const int sb = q4_scale_byte(scale_group_max(y));
     return make_uint2(q4_encode8(y, sb), (unsigned)sb);
 }
 
-// Whether some code of y, or its scale, could be another for a value `off` of y's pair
-// away (relative to the sum of the pair's magnitudes).
-__device__ __forceinline__ bool q4_near_border(const float (&y)[8], const float (&pair)[4],
-                                               unsigned amax, int sb, float off)
+// Eight codes of y at scale byte sb of the group whose largest magnitude's bits are
+// amax; near: some code, or the scale, could be another for a value that is `off` of
+// its pair's two magnitudes away.
+__device__ __forceinline__ uint32_t q4_encode8_near(const Eight &y, unsigned amax, int sb,
+                                                    float off, bool &near)
 {
     const float by = q4_unscale(sb);
-    float lo[8], hi[8], most = 0.f;
+    const Eight z = scaled(y, by);
+    const F2 up = f2(off, off), down = f2(-off, -off);
+    Eight lo, hi;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float z = y[j] * by, t = pair[j / 2] * (by * off);
-        lo[j] = z - t;
-        hi[j] = z + t;
-        most = fmaxf(most, t);
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = parts(z.a[i]), b = parts(z.b[i]);
+        const F2 pair = f2(fabsf(a.x) + fabsf(b.x), fabsf(a.y) + fabsf(b.y));
+        lo.a[i] = fma2(pair, down, z.a[i]);
+        lo.b[i] = fma2(pair, down, z.b[i]);
+        hi.a[i] = fma2(pair, up, z.a[i]);
+        hi.b[i] = fma2(pair, up, z.b[i]);
     }
-    // (the group's largest is one of four lanes'; any of them may find it near)
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    const float z = __uint_as_float(amax) * by;
-    const bool scale = sb < 255 && (z + most > 6.f || (z - most <= 3.f && sb > 127 + kQ4MinExp));
-    // (a zero's sign is no border)
-    return ((e2m1x8(lo) ^ e2m1x8(hi)) & 0x77777777u) != 0 || scale;
+    float l[8], h[8];
+    values_of(lo, l);
+    values_of(hi, h);
+    const uint32_t code = e2m1x8(l);
+    // (the group's largest is off by at most 2 off of itself; a zero's sign is no border)
+    const float top = __uint_as_float(amax) * by;
+    const bool scale = fmaf(top, 2.f * off, top) > 6.f ||
+                       (fmaf(top, -2.f * off, top) <= 3.f && sb > 127 + kQ4MinExp);
+    near = sb < 255 && (((code ^ e2m1x8(h)) & 0x77777777u) != 0 || scale);
+    return sb == 255 ? 0u : code;
 }
 
 // A lane's scale bytes of a head, D / 32 of its four-lane groups, in one word of
@@ -510,13 +556,6 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
     // the weight in the coefficients, 7.7 in plain 32-bit operations, at the same time)
     const Eight wk8 = unpack(wk);
     const Turn turn = turn_of(c01, c23, BITS < 16 ? unpack(ones) : wk8);
-    // (tables may be scaled: the largest of the lane's factors, at least 1)
-    float turn_gain = 1.f;
-    if constexpr (BITS == 4) {
-        turn_gain = fmaxf(fmaxf(fmaxf(fabsf(c01.x), fabsf(c01.y)), fmaxf(fabsf(c01.z), fabsf(c01.w))),
-                          fmaxf(fmaxf(fabsf(c23.x), fabsf(c23.y)), fmaxf(fabsf(c23.z), fabsf(c23.w))));
-        turn_gain = fmaxf(turn_gain, 1.f);
-    }
     for (int h0 = 0; h0 < p.Hkv; h0 += kKv * width) {
 #pragma unroll
         for (int u = 0; u < kKv; ++u) {
@@ -534,32 +573,32 @@ __global__ void __launch_bounds__(kMaxThreads, 3) token_write_kernel(const Token
                     x.b[i] = mul2(x.b[i], wk8.b[i]);
                 }
             }
-            const Eight before = x;
             apply(x, turn, p.rope != nullptr);
             const bool store = live && h < p.Hkv;
             const size_t head = (size_t)slot * p.Hkv + h;
             if constexpr (BITS == 4) {
-                float y[8], pair[4], v8[8];
-                values_of(x, f, y);
+                const Eight y = scaled(x, f), v8 = unpack(vraw);
                 const unsigned amax = scale_group_max(y);
                 int sk = q4_scale_byte(amax);
-                uint32_t kc = q4_encode8(y, sk);
+                uint32_t kc;
                 if (p.rope != nullptr || p.k_norm != nullptr) {
-                    // What 32-bit operations may be off by, of the pair's magnitudes: the
-                    // rotation's two roundings 2^-23, the check's one 2^-24; the norm's nine
-                    // of the sum (halved by the root), rsqrtf's two units and the product
-                    // 2^-20.7 more.
-                    const float off = turn_gain * (p.k_norm != nullptr ? 0x1.8p-20f : 0x1p-22f);
-                    pair_sizes(before, f, pair);
-                    if (__any_sync(0xffffffffu, q4_near_border(y, pair, amax, sk, off))) {
+                    // What 32-bit operations may be off by, of the pair's two magnitudes: the
+                    // rotation's two roundings 2^-23 (of |a c| and |b s|, together at most the
+                    // turned pair's length), the check's 2^-24; the norm's nine of the sum,
+                    // halved by the root, rsqrtf's two units and the product 9.5 2^-24 more.
+                    bool near;
+                    kc = q4_encode8_near(y, amax, sk, p.k_norm != nullptr ? 0x1p-20f : 0x1p-22f,
+                                         near);
+                    if (__any_sync(0xffffffffu, near)) {
                         const float *cos_sin = p.rope != nullptr && row.pos >= 0 && row.bad == 0
                                                    ? p.rope + (size_t)row.pos * D : nullptr;
-                        const uint2 r = key_codes_in_64<D>(p.k_norm, cos_sin, p.norm_eps, kraw);
+                        const uint2 r = key_codes_exact<D>(p.k_norm, cos_sin, p.norm_eps, kraw);
                         kc = r.x;
                         sk = (int)r.y;
                     }
+                } else {
+                    kc = q4_encode8(y, sk);
                 }
-                values_of(unpack(vraw), 1.f, v8);
                 const int sv = q4_scale_byte(scale_group_max(v8));
                 const uint32_t vc = q4_encode8(v8, sv);
                 const uint32_t ks = q4_scale_word<D>(sk, lane), vs = q4_scale_word<D>(sv, lane);
