@@ -55,7 +55,10 @@ struct StreamCfg {
     // tiles of 16 tokens that a warp takes at a time
     static constexpr int kTiles = kCodes && NT == 1 ? QT : 1;
     static constexpr int kTok = 16 * kTiles * kWph;       // tokens of a stage
-    static constexpr int kProducers = 3;                  // producer warps, a stage each in turn
+    // producer warps, a stage each in turn: the serving batch of 4 bits takes 78, 51.7,
+    // 48.3, 47.8 and 51.9 us with 1, 2, 3, 4 and 6; groups of 16 heads 39.6 with 2 or 3
+    // and 42.2 with 4, heads of 64 30.8 with 3 and 31.1 with 4
+    static constexpr int kProducers = kCodes && NT == 1 && D == 128 ? 4 : 3;
     static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kHeadBytes = D * BITS / 8;
     static constexpr int kRowBytes = HPC * kHeadBytes;    // one token, HPC kv heads
