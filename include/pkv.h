@@ -668,8 +668,8 @@ pkv_status paged_kv_read_q4(const pkv_dims *dims, const void *k_codes, const voi
  * num_splits > 1, the piece combine; a batch of more than 1024 rows x kv-head groups
  * (a group: 8, 4, 2 or 1 kv heads, the most that divide Hkv) takes several such
  * pairs, one after the other.  PKV_ERR_UNSUPPORTED: Hkv of more than 1024 groups, or
- * seen tokens x groups or num_pages x page_size past 2^31.  The workspace's plan of
- * a bf16 decode stays as it is. */
+ * seen tokens x groups or num_pages x page_size past 2^31.  A plan that a bf16 or an
+ * 8-bit decode has in the workspace stays as it is. */
 pkv_status paged_decode_attn_q4(const pkv_dims *dims, const void *q, const void *k_codes,
                                 const void *v_codes, const void *k_scale, const void *v_scale,
                                 const int32_t *kv_indices, const int32_t *kv_indptr,

@@ -81,14 +81,16 @@ int log2_exact(int x)
 // it must leave the row info of a bf16 plan as it is, and the other way round.
 // It is in the rotated-q scratch, which is at least as large (8 bytes a virtual
 // row against 128 and more a query head) and which only shapes off the
-// persistent path use, whose 8-bit calls have no plan.
+// persistent path use, whose 8-bit calls have no plan.  The row info of a decode over
+// the 4-bit cache or through a window is behind it, as it must leave that of an 8-bit
+// plan (2 x 8 bytes a virtual row, of at least 128).
 // The partial region holds either layout: the per-split one [B,Hq,S,(2|D)]
 // of paged_decode_partials, or the piece one [(S+Bv)*HQV, (2|D)] of the
 // persistent path.  Every region starts on a 256-byte boundary.
 struct Layout {
     int hpc, Bv, HQV;
-    size_t rowinfo_off, plan_off, qscratch_off, rowinfo_q8_off, table_off, split_ml_off,
-        split_o_off, piece_ml_off, piece_o_off, total;
+    size_t rowinfo_off, plan_off, qscratch_off, rowinfo_q8_off, rowinfo_stream_off, table_off,
+        split_ml_off, split_o_off, piece_ml_off, piece_o_off, total;
 };
 
 Layout layout_for(const pkv_dims *d, int num_splits)
@@ -104,6 +106,7 @@ Layout layout_for(const pkv_dims *d, int num_splits)
                             ? pkv::plan_words(L.Bv, num_splits) * sizeof(int32_t) : 0;
     L.qscratch_off = L.plan_off + round_up(plan, 256);
     L.rowinfo_q8_off = L.qscratch_off;
+    L.rowinfo_stream_off = L.qscratch_off + round_up((size_t)L.Bv * 2 * sizeof(int32_t), 16);
     L.table_off = L.qscratch_off + round_up((size_t)d->B * d->Hq * d->D * 2, 256);
     const size_t part = L.table_off + round_up(((size_t)2 * d->B + 1) * sizeof(int32_t), 256);
     const size_t rows = (size_t)d->B * d->Hq * num_splits;
@@ -1370,6 +1373,7 @@ static pkv_status decode_stream(const pkv_dims *dims, int bits, const void *q, c
         sp.sinks = windowed ? sinks : 0;
         pkv::FusedParams &p = sp.f;
         p.Bv = d.B * groups;
+        p.row_info = reinterpret_cast<int32_t *>(ws + L.rowinfo_stream_off);
         p.row_cost = (int)cost;
         p.q = static_cast<const __nv_bfloat16 *>(q) + (size_t)b0 * d.Hq * d.D;
         p.out = static_cast<__nv_bfloat16 *>(out) + (size_t)b0 * d.Hq * d.D;

@@ -231,3 +231,76 @@ def test_a_wait_that_runs_out_is_reported():
     out, status = decode(c, q)
     assert status == 0
     check(c, q, out)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("shape", [(16, 4, 128, 16), (1, 1, 64, 16)])
+def test_a_plan_of_the_8_bit_decode_stays(shape, bits):
+    """A step whose 8-bit layers run on their plan, with other layers between them."""
+    import q8_cases
+    lens = [30000, 90, 21000, 4]
+    c8 = q8_cases.Cache(lens, *shape, seed=22, max_seq_len=50000).fill()
+    c = _cache(shape, [700, 0, 33000, 900], bits, seed=23, max_seq_len=50000)
+    q = _q(c, 24)
+    S = pkv.plan(c8.d)[0]
+    ws = pkv.alloc_workspace(c8.d, S, DEV)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    pkv.paged_decode_attn_q8(c8.d, q, *c8.q8, *c8.rows, S, ws, a)
+    window = 0 if bits == 4 else 32000
+    out, status = decode(c, q, bits, window, 4, splits=S, ws=ws)
+    pkv.paged_decode_attn_q8_planned(c8.d, q, *c8.q8, *c8.rows, S, ws, b)
+    assert torch.equal(a, b) and status == 0
+    check(c, q, out, bits, window, 4)
+
+
+def test_offsets_past_2_31_bytes():
+    """Rows in the last pages of pools of more than 2^31 bytes each."""
+    Hq, Hkv, D, ps, L = 16, 8, 128, 16, 40
+    pages = (1 << 31) // (ps * Hkv * D // 2) + 1000
+    c = Cache([L, 3], Hq, Hkv, D, ps, seed=25)
+    small = [x.clone() for x in c.q4]
+    big = [torch.empty(pages, *x.shape[1:], dtype=torch.uint8, device=DEV) for x in c.q4]
+    c.kc, c.vc, c.ks, c.vs = big
+    at = pages - len(small[0])
+    for x, y in zip(big, small):
+        x[at:] = y
+    table = c.kv_indices + at
+    d = pkv.dims(2, Hq, Hkv, D, ps, pages, c.n_ref, 64)
+    rows = (table, c.kv_indptr, c.seq_lens)
+    k, v = (c.randn(L + 3, Hkv, D).to(torch.bfloat16).to(DEV) for _ in range(2))
+    ends = torch.tensor([0, L, L + 3], dtype=torch.int32, device=DEV)
+    pkv.paged_kv_extend_q4(d, pkv.tokens(None, k, v), ends, *big, *rows, status=c.status)
+    k16, v16 = (torch.zeros(c.n_ref, ps, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pkv.paged_kv_read_q4(d, *big, *rows, k16, v16, status=c.status)
+    q = _q(c, 26)
+    out, status = decode(c, q, 4, rows=rows, d=d)
+    assert int(c.status) == 0 and status == 0
+    for x, y in zip(big, small):
+        y.copy_(x[at:])
+    c.kc, c.vc, c.ks, c.vs = small
+    for b, (a, e) in enumerate(((0, L), (L, L + 3))):
+        for got, want in zip(c.held(b), (k, v)):
+            code, scale = q4_cases.quantise(want[a:e].cpu())
+            assert torch.equal(got, q4_cases.values(code, scale))
+    check(c, q, out)
+    flat = k16.cpu().flatten(0, 1)
+    assert torch.equal(flat[:L], q4_cases.bf16_of(c.held(0)[0]))
+    # bf16 pools, through a window
+    pages = (1 << 30) // (ps * Hkv * D) + 1000
+    big = [torch.empty(pages, ps, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    at = pages - c.n_pool
+    fill16(c)
+    for x, y in zip(big, (c.k16, c.v16)):
+        x[at:] = y
+    d = pkv.dims(2, Hq, Hkv, D, ps, pages, c.n_ref, 64)
+    rows = (c.kv_indices + at, c.kv_indptr, c.seq_lens)
+    S = pkv.plan(d)[0]
+    ws = pkv.alloc_workspace(d, S, DEV)
+    out = torch.empty_like(q)
+    pkv.paged_decode_attn_window(d, q, *big, *rows, 20, 3, S, ws, out)
+    check(c, q, out, 16, 20, 3)
+    assert pkv.status_word(ws) == 0
+    chunk = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    pkv.paged_prefill_attn_window(d, q, chunk, *big, *rows, 20, 3, out, status=c.status, max_q_len=1)
+    check(c, q, out, 16, 20, 3)
+    assert int(c.status) == 0

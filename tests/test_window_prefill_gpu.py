@@ -177,3 +177,11 @@ def test_long_row_past_a_window():
         out, status = _run(c, q, ends, window, sinks, ws=_workspace(128), max_q=130)
         assert status == 0
         _check(c, q, out, ends, window, sinks)
+
+
+def test_rows_behind_the_last_chunk_stay():
+    c, q, ends = _case(8, 2, 128, 16, [300, 200], [70, 33], seed=6)
+    more = torch.cat([q, torch.full((9, 8, 128), float("nan"), dtype=torch.bfloat16, device=DEV)])
+    out, status = _run(c, more, ends, 64, 4)
+    assert status == 0 and bool(out[-9:].isnan().all())
+    _check(c, q, out[:-9], ends, 64, 4)
