@@ -35,10 +35,15 @@
 //     taking turns one run at a time, so each makes its waits and commits
 //     while the other's run goes out.
 // With a window (paged_prefill_attn_window) query p sees keys p - window + 1 .. p
-// and the first `sinks`: a unit's list of key blocks is then the blocks of the
-// sinks and those from its first query's window on, the blocks between are never
-// read, keys that no query of the unit sees are zeroed (their page is not read
-// either), and the softmax masks the rest of a row's unseen keys.
+// and the first `sinks`.  A unit's keys are then a list, cut into blocks of 128: the
+// sinks, then the keys from its first query's window on, both in whole boxes of
+// the copies (a page, or a part of one), so that only pages with a seen key are
+// read; the softmax masks what a row does not see, eight keys at a time where a
+// warp's rows have an edge.  4 prompts of 4,096 tokens, 32 over 8 heads of 128, window
+// 1,024, 4 sinks: 237 us, 1,019 TF/s of seen products (nine blocks a unit, which hold
+// 89% seen ones; the plain prefill makes 1,360); with sinks and window in blocks of
+// their own 294 us.  16 chunks of 129 to 509 of heads of 64, pages of 24 tokens, window
+// 250: 50.7 us, three blocks a unit, which waits as long as it computes.
 // With a workspace (paged_prefill_attn_ws), a list whose last round would
 // leave at least half the SMs idle cuts that round's units along their key
 // blocks (the split-KV of the decode, applied to prefill): each part stores

@@ -6,11 +6,12 @@
 // and the first `sinks`.  A step reads each of them once, so it is bound by memory.
 // The work is split as in the 8-bit decode (pkv_q8_decode.cu): one persistent block
 // per SM takes an equal range of the seen tokens of all rows laid end to end;
-// producer warps copy the tokens of HPC kv heads in 16-byte lines into a ring of
-// stages, and the piece combine joins the rows that several blocks share.  The i-th
-// seen token of a row is its token i for i < sinks, i + L - seen behind: only the
-// producers know, as they look up each token's page.  Pages without a seen token
-// are not looked up.
+// producer warps copy the tokens of HPC kv heads in 16-byte lines (2 KB rows: one bulk
+// copy each) into a ring of stages, and the piece combine joins the rows that several
+// blocks share.  The i-th seen token of a row is its token i for i < sinks, i + L -
+// seen behind: only the producers know, as they look up each token's page, a stage of
+// their own ahead, over the ends of rows too.  Pages without a seen token are not
+// looked up.
 //
 // The tokens are the M rows of the products (S^T = K Q^T, O^T = V^T P^T, m16n8k16)
 // and the query heads the eight columns; a kv head has WPH = 8 / HPC warps with sums
@@ -29,13 +30,26 @@
 //    once a unit.  y = x + ev, ev the largest exponent of the token's units, decides
 //    the base, so a weight of a unit is at most 2^15; under f16's normal range it is
 //    rounded to steps of 2^-24, 2^-31 of the largest.
+//
+// What bounds it.  The windows over bf16 pools: memory.  The 4-bit cache: instructions.
+// A warp makes 350 for 16 tokens of a head of 128, of which 160 go to the
+// arithmetic-logic pipe at two cycles each (64 conversions, 16 to gather two tokens'
+// codes, 16 for scales, 8 to round weights); issue slots are 58% busy, that pipe 51%,
+// the tensor cores 20%.  On the serving batch the copies alone take 35.6 us, the
+// arithmetic alone 44, neither 18.
+//
+// Measured (CUDA-graph replay, K and V larger than L2 or rotating): 4 bits, 128 rows,
+// lognormal, 154,103 tokens, 64 over 8 heads of 128, 168 MB: 47.7 us, 3,510 GB/s, 53% of
+// the copy bandwidth (the 8-bit cache's 322 MB: 57.7, bf16's 631 MB: 97); one row of
+// 32,768, 32 heads: 17.4 us; 32 rows through a window of 1,024 and 4 sinks: 17.3; 8 rows of
+// 513 to 1,025, heads of 64: 8.6.  bf16, 128 rows of at most 1,028 seen tokens, 312 MB:
+// 56.3 us, 5,540 GB/s, 83%; 64 rows of 4,100 seen tokens, 1,076 MB: 158.6 us, 6,785 GB/s.
 #include <cmath>
 #include <type_traits>
 
 #include "pkv_decode.cuh"
 #include "pkv_partition.cuh"
 #include "pkv_q4.cuh"
-#include "pkv_q8.cuh"
 
 namespace pkv {
 
@@ -46,14 +60,13 @@ constexpr float kRaise = 15.f;            // how far a score may exceed its base
 template <int BITS, int D, int HPC, int NT>
 struct StreamCfg {
     static constexpr bool kCodes = BITS == 4;
-#ifndef QW
-#define QW 8
-#define QT 2
-#endif
-    static constexpr int kWarps = kCodes && NT == 1 ? QW : 8;   // consumer warps
+    static constexpr int kWarps = 8;                      // consumer warps
     static constexpr int kWph = kWarps / HPC;             // warps of a kv head
-    // tiles of 16 tokens that a warp takes at a time
-    static constexpr int kTiles = kCodes && NT == 1 ? QT : 1;
+    // Tiles of 16 tokens that a warp takes at a time: with two, the loop's steps serve
+    // both (68 instructions of 700), and the products of one overlap the other's
+    // exponentials.  The serving batch of 4 bits: 52.0 us, one tile 59.3, 16 warps of one
+    // 57.9, four tiles 55.
+    static constexpr int kTiles = kCodes && NT == 1 ? 2 : 1;
     static constexpr int kTok = 16 * kTiles * kWph;       // tokens of a stage
     // producer warps, a stage each in turn: the serving batch of 4 bits takes 78, 51.7,
     // 48.3, 47.8 and 51.9 us with 1, 2, 3, 4 and 6; groups of 16 heads 39.6 with 2 or 3

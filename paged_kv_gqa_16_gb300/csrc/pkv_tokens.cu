@@ -33,7 +33,9 @@
 // norms, 405 MB: 66.5 us, 6,090 GB/s, 90% of the copy bandwidth; the 8-bit form on
 // 18,425 tokens, 416 MB: 67.7 us, 91%; 9,537 tokens of 32 + 8 heads of 64, 108 MB:
 // 21.3 us, 75% (an elementwise kernel of as many bytes takes 18 us); one token of 8
-// to 128 rows: 2.4 to 3.6 us, the launch and three dependent loads.
+// to 128 rows: 2.4 to 3.6 us, the launch and three dependent loads.  The 4-bit form on
+// the same 18,425 tokens, 397 MB: 70.6 us, 84% (68 without the look at the borders);
+// 9,537 of D = 64, 101 MB: 22.6; one token of 8 to 128 rows: 2.4 to 3.5.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_q4.cuh"
