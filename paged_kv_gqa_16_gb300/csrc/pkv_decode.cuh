@@ -45,6 +45,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
                  : "memory");
 }
 
+// Wait for this thread's cp.async copies.
+__device__ __forceinline__ void cp_async_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // 16 bytes global -> shared.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint64_t policy)
 {

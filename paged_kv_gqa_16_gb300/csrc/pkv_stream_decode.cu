@@ -68,18 +68,25 @@ struct StreamCfg {
     // 57.9, four tiles 55.
     static constexpr int kTiles = kCodes && NT == 1 ? 2 : 1;
     static constexpr int kTok = 16 * kTiles * kWph;       // tokens of a stage
-    // producer warps, a stage each in turn: the serving batch of 4 bits takes 78, 51.7,
-    // 48.3, 47.8 and 51.9 us with 1, 2, 3, 4 and 6; groups of 16 heads 39.6 with 2 or 3
-    // and 42.2 with 4, heads of 64 30.8 with 3 and 31.1 with 4
-    static constexpr int kProducers = kCodes && NT == 1 && D == 128 ? 4 : 3;
-    static constexpr int kThreads = (kWarps + kProducers) * 32;
-    static constexpr int kHeadBytes = D * BITS / 8;
-    static constexpr int kRowBytes = HPC * kHeadBytes;    // one token, HPC kv heads
     // Rows of 2 KB go by one bulk copy each, with a pitch that spreads them over the
     // banks: a lane's instruction in place of four of a warp.  (Shorter ones would be
     // slower so: the copy engine takes about 24 copies a microsecond and SM.)
-    static constexpr bool kBulk = BITS == 16 && kRowBytes >= kBulkRowBytes;
+    static constexpr bool kBulk = BITS == 16 && HPC * D * BITS / 8 >= kBulkRowBytes;
     static_assert(!kBulk || kTok == 16, "a lane copies a row of K or of V");
+    // Producer warps, and how many fill a stage together, a part of its tokens each.
+    // Together they bring the first stage sooner and issue more in flight: bf16, 512 rows
+    // of 2048 tokens, 8 heads of D = 64, 402 us -> 330 with four a stage, one row of 64 8.0
+    // -> 5.8.  A stage of codes is smaller, and each share costs its own steps: two a
+    // stage 17.45 us -> 17.1 for a row of 32768, 4 bits, and four 16.5, but a batch of 512
+    // 166 us -> 198.  (Two tiles of heads at D = 128 take 437 us with three warps and 462
+    // with four.)
+    static constexpr int kProducers = kTok == 16 && D == 128 ? 3 : 4;
+    static constexpr int kSplit = kBulk ? 1 : BITS == 16 ? 4 : kTok >= 32 ? 2 : 1;
+    static constexpr int kShare = kTok / kSplit;           // tokens of a warp
+    static constexpr int kTurn = kProducers / kSplit;      // stages from a warp's one to its next
+    static constexpr int kThreads = (kWarps + kProducers) * 32;
+    static constexpr int kHeadBytes = D * BITS / 8;
+    static constexpr int kRowBytes = HPC * kHeadBytes;    // one token, HPC kv heads
     static constexpr int kPitch = kBulk ? kRowBytes + 16 : kRowBytes;
     static constexpr int kStageBytes = 2 * kTok * kPitch;
     // a token's scale bytes (of K, and of V), and its room for them
@@ -92,10 +99,10 @@ struct StreamCfg {
     static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 16;
     static constexpr int kStagesFit =
         (kSmemLimit - kFixedBytes) / (kStageBytes + kScaleBytes + 16);
-    // A multiple of the producers: a slot then always belongs to the same one.
-    static constexpr int kStages =
-        (kStagesFit > 12 ? 12 : kStagesFit) / kProducers * kProducers;
-    static_assert(kStages >= 3, "a slot has one producer");
+    // A multiple of the turns: a slot then always belongs to the same producers.
+    static constexpr int kStages = (kStagesFit > 12 ? 12 : kStagesFit) / kTurn * kTurn;
+    static_assert(kStages >= 3 && kStages % kTurn == 0, "a slot has its producers");
+    static_assert(kShare >= 4 && (kShare & (kShare - 1)) == 0, "no carry in the swizzle");
     static constexpr int kScaleOffset = kStages * kStageBytes;
     static constexpr int kJoinOffset = kScaleOffset + kStages * kScaleBytes;
     static constexpr int kBarOffset = kJoinOffset + kJoinBytes;
@@ -184,7 +191,6 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
     stream_decode_kernel(const __grid_constant__ StreamParams sp)
 {
     using C = StreamCfg<BITS, D, HPC, NT>;
-    constexpr int kProducers = C::kProducers;
     constexpr int kWarps = C::kWarps;
     constexpr int NST = C::kStages;
     constexpr int U = C::kTiles;
@@ -211,8 +217,8 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
-            // a producer warp's lanes, or it once and each of its lanes' copies
-            mbar_init(&full[i], C::kBulk ? 32 : 33);
+            // a producer warp's lanes, or kSplit warps once and their lanes' copies
+            mbar_init(&full[i], C::kBulk ? 32 : 33 * C::kSplit);
             mbar_init(&empty[i], kWarps);
         }
         fence_mbar_init();
@@ -257,12 +263,13 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
 
     if (warp >= kWarps) {
         // ======================= producer warps ===========================
-        // Stage i belongs to warp i % kProducers.  Lane l looks up the stage's
-        // tokens l, 32 + l, ... and copies their scales; the copies of the rows
-        // take the tokens' slots from it.
+        // A warp has the tokens first .. first + kShare - 1 of every kTurn-th stage.  Lane l
+        // looks up its tokens l, 32 + l, ... and copies their scales; the copies of the
+        // rows take the tokens' slots from it.
         const int pw = warp - kWarps;
+        const int first = pw % C::kSplit * C::kShare;
         const uint64_t policy = policy_evict_first();
-        constexpr int IDS = (C::kTok + 31) / 32;      // page ids a lane holds
+        constexpr int IDS = (C::kShare + 31) / 32;    // page ids a lane holds
         auto page_of_tok = [&](int t) {
             return p.ps_shift >= 0 ? (t >> p.ps_shift) : (t / p.page_size);
         };
@@ -306,23 +313,23 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
         // the table's entry for this lane's k-th token of a stage
         auto load_id = [&](const Stage &s, int k) {
             const int at = k * 32 + lane;
-            const bool there = s.hg >= 0 && at < C::kTok && s.tok + at < s.t1;
-            const int pi = page_of_tok(there ? token(s, s.tok + at) : 0);
+            const bool there = s.hg >= 0 && at < C::kShare && s.tok + first + at < s.t1;
+            const int pi = page_of_tok(there ? token(s, s.tok + first + at) : 0);
             return there && pi < s.npg ? p.kv_indices[s.pg0 + pi] : 0;
         };
-        int it = pw;
+        int it = pw / C::kSplit;
         Stage cur;
         row_stage(cur, r0);
-        step(cur, pw);
-        // the ids of this warp's next stage, of another row too, are loaded a stage ahead
+        step(cur, it);
         int ids[IDS];
 #pragma unroll
         for (int k = 0; k < IDS; ++k)
             ids[k] = load_id(cur, k);
-        for (; cur.hg >= 0; it += kProducers) {
-            Stage after = cur;
-            step(after, kProducers);
+        for (; cur.hg >= 0; it += C::kTurn) {
             const int st = it % NST;
+            // the ids of this warp's next stage, of another row too, are on their way
+            Stage after = cur;
+            step(after, C::kTurn);
             int next[IDS];
 #pragma unroll
             for (int k = 0; k < IDS; ++k)
@@ -344,7 +351,9 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
             }
             unsigned char *stage = smem + st * C::kStageBytes;
             unsigned char *sc0 = smem + C::kScaleOffset + st * C::kScaleBytes;
-            const int nvalid = min(C::kTok, cur.t1 - cur.tok);
+            // (of this warp's share)
+            const int tok0 = cur.tok + first;
+            const int nvalid = max(0, min(C::kShare, cur.t1 - tok0));
             // a page id of a token that is there, checked
             auto checked = [&](int page, bool there) {
                 if (page < 0 || page >= p.num_pages) {
@@ -402,32 +411,35 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
             } else {
                 // bf16: the rows of V that end the piece's last tile are zeroed (their
                 // weights are 0, and what a stage held may be NaN)
-                const int filled = BITS == 16 ? (nvalid + 15) & ~15 : nvalid;
+                const int tiles_end = (min(C::kTok, cur.t1 - cur.tok) + 15) & ~15;
+                const int filled = BITS == 16 ? min(C::kShare, tiles_end - first) : nvalid;
                 constexpr int CH = C::kRowBytes / 16;      // 16-byte lines of a token
                 const size_t line0 = (size_t)cur.hg * C::kRowBytes;
                 const unsigned tok_bytes = (unsigned)(p.Hkv * C::kHeadBytes);
 #pragma unroll
                 for (int k = 0; k < IDS; ++k) {
-                    if (k * 32 >= nvalid)
+                    if (k * 32 >= filled)
                         break;
                     const int row = k * 32 + lane;
                     const bool there = row < nvalid;
-                    const int t = there ? token(cur, cur.tok + row) : 0;
+                    const int t = there ? token(cur, tok0 + row) : 0;
                     const int page = checked(ids[k], there);
                     const int slot = page * p.page_size + t - page_of_tok(t) * p.page_size;
                     if constexpr (C::kCodes) {
                         if (there) {
                             const size_t at = ((size_t)slot * p.Hkv + (size_t)cur.hg * HPC) * G32;
-                            copy_scales(p.k_scale, row, at);
-                            copy_scales(p.v_scale, C::kTok + row, at);
+                            copy_scales(p.k_scale, first + row, at);
+                            copy_scales(p.v_scale, C::kTok + first + row, at);
                         }
                     }
                     // 32 lines at a time, 32 / CH tokens' (or part of one): line
                     // 32 j + lane lies at byte 16 (32 j + lane) of these tokens'
-                    // rows, its swizzle that of the lane and of j (no carry)
-                    constexpr int ROUNDS = (C::kTok < 32 ? C::kTok : 32) * CH / 32;
-                    const uint32_t lane_key = (uint32_t)((lane / CH) >> kKeyShift & 7) << 4;
-                    const uint32_t to = smem_addr(stage) + k * 32 * C::kRowBytes;
+                    // rows, its swizzle that of the lane, of j and of the share, which
+                    // starts at a multiple of its size (no carry)
+                    constexpr int ROUNDS = (C::kShare < 32 ? C::kShare : 32) * CH / 32;
+                    const uint32_t lane_key =
+                        (uint32_t)(((lane / CH) >> kKeyShift ^ first >> kKeyShift) & 7) << 4;
+                    const uint32_t to = smem_addr(stage) + (first + k * 32) * C::kRowBytes;
 #pragma unroll 8
                     for (int j = 0; j < ROUNDS; ++j) {
                         const int from = (j * 32 + lane) / CH, ch = (j * 32 + lane) % CH;
@@ -459,8 +471,21 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
         // Let this warp's copies land before it exits, with the full time
         // limit: a consumer that gave up skips its stages, and the block must
         // not exit while a copy into its shared memory is in flight.
-        for (int k = it - kProducers, n = 0; k >= 0 && n < NST; k -= kProducers, n += kProducers)
-            (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
+        if constexpr (C::kSplit == 1) {
+            for (int k = it - C::kTurn, n = 0; k >= 0 && n < NST; k -= C::kTurn, n += C::kTurn)
+                (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
+        } else {
+            // A stage is kSplit warps': one that gave up leaves the others' last stages
+            // open, so what is waited for is this thread's copies, and then the
+            // arrivals that they trigger, unless somebody gave up.
+            cp_async_wait_all();
+            for (int k = it - C::kTurn, n = 0; k >= 0 && n < NST && !*abort;
+                 k -= C::kTurn, n += C::kTurn)
+                (void)mbar_wait_or_abort(&full[k % NST], (uint32_t)((k / NST) & 1),
+                                         kWaitLimitNs, abort);
+            if (*abort)
+                __nanosleep(1000);
+        }
         grid_launch_dependents();
         return;
     }
