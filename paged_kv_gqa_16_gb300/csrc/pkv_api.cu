@@ -1313,15 +1313,13 @@ static pkv_status decode_q8_impl(const pkv_dims *dims, const void *q, const void
 }
 
 // Whether the stream decode takes whole rows, by the bytes of K and V that a row's
-// last token sees (kQ4WholeBytes and the others).
+// last token sees (stream_whole_bytes).
 static bool stream_whole(const pkv_dims *dims, int hpc, int bits, int most_seen, int sms)
 {
     const long long rows = (long long)dims->B * (dims->Hkv / hpc);
     const long long head = bits == 4 ? dims->D / 2 + dims->D / 32 : dims->D * 2;
-    const long long most = bits == 4 ? pkv::kQ4WholeBytes
-                           : hpc * head >= pkv::kBulkRowBytes ? pkv::kBulkWholeBytes
-                                                              : pkv::kLinesWholeBytes;
-    return most_seen * hpc * head * 2 <= (2 * rows >= sms ? 2 : 1) * most;
+    return most_seen * hpc * head * 2 <=
+           pkv::stream_whole_bytes(bits, hpc, hpc * head >= pkv::kBulkRowBytes, 2 * rows >= sms);
 }
 
 // Decode over a 4-bit cache (bits 4) or bf16 pools; window 0: all tokens.

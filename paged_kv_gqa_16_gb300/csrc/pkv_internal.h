@@ -300,19 +300,27 @@ constexpr int kQ8MaxRows = 1024;
 // tokens are skipped.  f.k_codes and f.v_codes are the pools of either kind.
 constexpr int kQ4RowCost = 64;
 constexpr int kWindowRowCost = 32;
-// Rows of which at most this many bytes (K and V of a block's kv heads) are seen are
-// not split, and twice as many where there are rows x kv-head groups for half the SMs.
-// Unsplit against split, us:
-//   4 bits, 8 heads of 128, 128 tokens (136 KB): 1 row 8.6, 9.0; 76 rows 8.8, 11.2; 512
-//   rows 27.1, 33.8.  256 (272 KB): 12.8, 9.2; 13.0, 13.2; 43.7, 48.5.  512: 21.4, 9.6;
-//   21.9, 17.8; 78.3, 77.9.  1 head of 64, 1 row of 1,024 (68 KB) 9.1, 7.8; 76 rows 9.4,
-//   10.8.
-//   bf16, 8 heads of 128 (bulk copies), 128 tokens (512 KB): 1 row 9.6, 9.4; 76 rows
-//   12.4, 14.7; 512 rows 46.1, 51.1.  256: 15.0, 9.6; 20.0, 20.0; 85.5, 88.7.  8 heads
-//   of 64, 64 tokens (128 KB): 8.0, 8.0; 8.1, 9.9.  128: 11.0, 9.7; 11.3, 12.2.
-constexpr long long kQ4WholeBytes = 128 << 10;
-constexpr long long kBulkWholeBytes = 512 << 10;
-constexpr long long kLinesWholeBytes = 192 << 10;
+// Rows of which at most so many bytes (K and V of a block's kv heads) are seen are not
+// split, and twice as many (by lines 1.5 times) where there are `many`: rows x kv-head
+// groups for half the SMs.  4 bits: 56 KB and 8 for each head of the block; bf16 by
+// 16-byte lines 128 KB and 16, by bulk copies 512 KB.  (With fewer heads a block, more
+// warps join their parts at a row's end.)  Unsplit against split, us:
+//   4 bits, 8 heads of 128, 128 tokens (136 KB): 1 row 8.1, 9.0; 76 rows 8.2, 10.9; 512
+//   rows 26.0, 33.0.  192 (204 KB): 10.1, 9.4; 10.4, 11.8; 34.4, 40.1.  256: 12.2, 9.0;
+//   12.6, 13.0; 43.2, 47.3.  8 heads of 64, 192 (102 KB): 7.7, 7.8; 7.9, 9.7.  384 (204
+//   KB): 11.8, 7.7; 12.0, 12.2; 40.9, 44.2.  1 head of 128, 384 (51 KB): 8.9, 9.0.  512
+//   (68 KB): 9.9, 9.1; 10.2, 12.1.  1,024 (136 KB): 13.9, 9.4; 14.1, 14.1; 47.8, 52.6.
+//   bf16, 8 heads of 64, 96 (192 KB): 6.8, 7.3; 128: 8.2, 8.1; 8 rows 8.2, 8.4; 76 rows
+//   8.7, 9.9.  192 (384 KB): 10.9, 8.4; 76 rows 11.8, 11.3; 512 rows 39.3, 41.4.  4 of 64,
+//   192 (192 KB): 7.0, 7.2.  256: 8.4, 7.3; 8.8, 9.4; 28.7, 29.8.  1 of 128, 256 (128
+//   KB): 7.2, 7.3.  512: 10.3, 7.7; 11.0, 11.4; 34.7, 35.9.
+//   By bulk copies, 8 heads of 128, 128 tokens (512 KB): 1 row 9.6, 9.4; 76 rows 12.4,
+//   14.7; 512 rows 46.1, 51.1.  256: 15.0, 9.6; 20.0, 20.0; 85.5, 88.7.
+inline long long stream_whole_bytes(int bits, int hpc, bool bulk, bool many)
+{
+    const long long kb = bits == 4 ? 56 + 8 * hpc : bulk ? 512 : 128 + 16 * hpc;
+    return (bits == 4 || bulk ? many ? 2 * kb : kb : many ? kb * 3 / 2 : kb) << 10;
+}
 // Rows of K (or V) that are copied by one bulk copy each: a token's kv heads of a block.
 constexpr int kBulkRowBytes = 2048;
 struct StreamParams {
