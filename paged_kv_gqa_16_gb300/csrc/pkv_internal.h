@@ -180,11 +180,13 @@ struct PrefillParams {
     int sinks;
     // the pools as 3-D tiled tensors {D, Hkv, pages x page_size} with a box of
     // {64, 1, tma_rows} and 128-byte swizzle (use_tma != 0; set by
-    // launch_prefill when the page size is a power of two >= 8)
+    // launch_prefill when the page size is a multiple of 8)
     CUtensorMap tmap_k;
     CUtensorMap tmap_v;
     int use_tma;
-    int tma_rows;                  // min(page_size, 128)
+    unsigned ps_magic;             // token / page_size by a product (set by launch_prefill)
+    int ps_magic_shift;
+    int tma_rows;                  // the power of two dividing page_size, at most 128
     // q as {D, Hq, total_q} with a box of {64, n_rep, tq}: one query tile's
     // rows (token-major, head-minor), 128-byte swizzled (q_tma != 0)
     CUtensorMap tmap_q;

@@ -16,9 +16,10 @@
 // whose keys stream in blocks of 128; one persistent block per SM walks a
 // list of units:
 //   - Q, K and V are loaded by TMA (3-D tiled tensor maps, 128-byte swizzle):
-//     Q as one box per tile and 64 dims, K and V as one box per page and 64
-//     dims; page sizes that are not a power of two >= 8 are gathered with
-//     16-byte cp.async into the same swizzled layout;
+//     Q as one box per tile and 64 dims, K and V as one box per page (or the
+//     power of two that divides its size) and 64 dims; page sizes that are not
+//     a multiple of 8 are gathered with 16-byte cp.async into the same
+//     swizzled layout;
 //   - S = Q K^T (M 128, N 128, K = D in steps of 16) goes to tensor memory;
 //   - a row's two threads each read half of its S (64 keys), mask keys past
 //     its position, exchange their halves' max, update the fp32 online
@@ -749,8 +750,12 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
             // 64 bytes are two whole L2 sectors, and the swizzle spreads the 8
             // rows' chunks over all banks
             const int kl = lane & 7, cl = lane >> 3;
+            // tok / page_size (page_size 2 or more)
+            auto page_by_product = [&](int tok) {
+                return (int)(__umulhi((unsigned)tok, p.ps_magic) >> p.ps_magic_shift);
+            };
             auto page_of = [&](int tok) {
-                return p.ps_shift >= 0 ? (tok >> p.ps_shift) : (tok / p.page_size);
+                return p.ps_shift >= 0 ? (tok >> p.ps_shift) : page_by_product(tok);
             };
             int kb = 0;                                    // blocks issued, over all units
             int qit = 0;                                   // units whose Q the V warp loaded
@@ -873,13 +878,13 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
                         __syncwarp();
                         for (int bx = lane; bx < nbox; bx += 32) {
                             const int tok = kWindow ? w.key(key0 + bx * R) : key0 + bx * R;
-                            const int pi = tok >> p.ps_shift;
+                            const int pi = page_by_product(tok);
                             int page = w.table_ok ? __ldg(p.kv_indices + w.pg0 + pi) : 0;
                             if (page < 0 || page >= p.num_pages) {
                                 tc_flag(p.status, kFlagBadPage);
                                 page = 0;
                             }
-                            const int row = (page << p.ps_shift) + (tok - (pi << p.ps_shift));
+                            const int row = page * p.page_size + (tok - pi * p.page_size);
 #pragma unroll
                             for (int h = 0; h < D / 64; ++h)
                                 tma_load_3d(dst + h * C::kRegionBytes + bx * R * 128, tmap, 64 * h,
@@ -1592,16 +1597,27 @@ bool prefill_plan(int B, int Hkv, int tq, int max_q_len, int sms, int D, size_t 
 cudaError_t launch_prefill(const PrefillParams &p_in, int D, int max_q_len, void *workspace,
                            size_t ws_bytes, cudaStream_t stream)
 {
-    // K/V pages by TMA when a page is a power of two >= 8 rows (whole 8-row
-    // swizzle atoms; a 128-key block is whole pages or a part of one) and
-    // every row index fits the copy's 32-bit coordinate
+    // K/V by TMA when a page is a multiple of 8 rows (whole 8-row swizzle
+    // atoms), in boxes of the largest power of two that divides it (a 128-key
+    // block is whole boxes, a box in one page), and every row index fits the
+    // copy's 32-bit coordinate
     PrefillParams p = p_in;
     p.out_align32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     p.use_tma = 0;
     p.tma_rows = 0;
+    // t / page_size for 0 <= t < 2^31 as (t m) >> (31 + s), s = ceil(log2 page_size),
+    // m = ceil(2^(31 + s) / page_size) < 2^32: e = m page_size - 2^(31 + s) is under
+    // page_size <= 2^s, so t m / 2^(31 + s) = (t + t e / 2^(31 + s)) / page_size, whose
+    // excess t e / 2^(31 + s) is under 1
+    int s = 1;
+    while (s < 31 && (1LL << s) < p.page_size)
+        ++s;
+    p.ps_magic = (unsigned)(((1ULL << (31 + s)) + p.page_size - 1) / p.page_size);
+    p.ps_magic_shift = s - 1;
     const long long rows = (long long)p.num_pages * p.page_size;
-    if ((D == 64 || D == 128) && p.ps_shift >= 3 && rows > 0 && rows < (1LL << 31)) {
-        const int box_rows = p.page_size < 128 ? p.page_size : 128;
+    if ((D == 64 || D == 128) && p.page_size % 8 == 0 && rows > 0 && rows < (1LL << 31)) {
+        const int even = p.page_size & -p.page_size;
+        const int box_rows = even < 128 ? even : 128;
         if (encode_map(&p.tmap_k, p.k_pool, D, p.Hkv, rows, 1, box_rows) &&
             encode_map(&p.tmap_v, p.v_pool, D, p.Hkv, rows, 1, box_rows)) {
             p.use_tma = 1;

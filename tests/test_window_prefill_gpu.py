@@ -98,6 +98,29 @@ def test_against_64_bits(shape, rows, split):
         _check(c, q, out, ends, window, sinks)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ps", [3, 24, 40, 136, 384, 1000])
+def test_page_sizes(ps, D):
+    """Sizes with a power-of-two part are copied by its boxes, others key by key; the keys
+    and their blocks, so the sums, are those of any page size."""
+    lens, chunks = [700, 300, 1, 0, 64, 513, 2050], [700, 129, 1, 0, 64, 40, 130]
+    ref, q, ends = _case(8, 2, D, 16, lens, chunks, seed=2)
+    c, _, _ = _case(8, 2, D, ps, lens, chunks, seed=3)
+    for b, L in enumerate(lens):
+        if L:
+            for of, to in ((ref.k16, c.k16), (ref.v16, c.v16)):
+                to[tuple(x.to(DEV) for x in c.places(b, 0, L))] = of[tuple(x.to(DEV) for x in ref.places(b, 0, L))]
+    want, status = _run(ref, q, ends, 0, 0)
+    assert status == 0
+    out, status = _run(c, q, ends, 0, 0)
+    assert status == 0 and torch.equal(out, want)
+    for window, sinks in [(1, 1), (64, 4), (129, 0), (300, 130)]:
+        table = (_unread(c, chunks, window, sinks), c.kv_indptr, c.seq_lens)
+        out, status = _run(c, q, ends, window, sinks, rows=table)
+        assert status == 0
+        _check(c, q, out, ends, window, sinks)
+
+
 def test_no_window_is_the_prefill():
     c, q, ends = _case(16, 4, 128, 16, [500, 77], [200, 77], seed=1)
     for window, sinks in ((0, 0), (0, 9), (c.d.max_seq_len, 0), (c.d.max_seq_len - 4, 4)):
