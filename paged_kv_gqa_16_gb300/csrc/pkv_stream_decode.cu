@@ -10,7 +10,7 @@
 // copy each) into a ring of stages, and the piece combine joins the rows that several
 // blocks share.  The i-th seen token of a row is its token i for i < sinks, i + L -
 // seen behind: only the producers know, as they look up each token's page, a stage of
-// their own ahead, over the ends of rows too.  Pages without a seen token are not
+// their own ahead, over the ends of rows too; several fill a stage together.  Pages without a seen token are not
 // looked up.
 //
 // The tokens are the M rows of the products (S^T = K Q^T, O^T = V^T P^T, m16n8k16)
@@ -34,16 +34,16 @@
 // What bounds it.  The windows over bf16 pools: memory.  The 4-bit cache: instructions.
 // A warp makes 350 for 16 tokens of a head of 128, of which 160 go to the
 // arithmetic-logic pipe at two cycles each (64 conversions, 16 to gather two tokens'
-// codes, 16 for scales, 8 to round weights); issue slots are 58% busy, that pipe 51%,
-// the tensor cores 20%.  On the serving batch the copies alone take 35.6 us, the
+// codes, 16 for scales, 8 to round weights); issue slots are 60% busy, that pipe 54%,
+// the tensor cores 21%.  On the serving batch the copies alone take 35.6 us, the
 // arithmetic alone 44, neither 18.
 //
 // Measured (CUDA-graph replay, K and V larger than L2 or rotating): 4 bits, 128 rows,
-// lognormal, 154,103 tokens, 64 over 8 heads of 128, 168 MB: 47.7 us, 3,510 GB/s, 53% of
+// lognormal, 154,103 tokens, 64 over 8 heads of 128, 168 MB: 47.1 us, 3,560 GB/s, 53% of
 // the copy bandwidth (the 8-bit cache's 322 MB: 57.7, bf16's 631 MB: 97); one row of
-// 32,768, 32 heads: 17.4 us; 32 rows through a window of 1,024 and 4 sinks: 17.3; 8 rows of
-// 513 to 1,025, heads of 64: 8.6.  bf16, 128 rows of at most 1,028 seen tokens, 312 MB:
-// 56.3 us, 5,540 GB/s, 83%; 64 rows of 4,100 seen tokens, 1,076 MB: 158.6 us, 6,785 GB/s.
+// 32,768, 32 heads: 17.0 us; 32 rows through a window of 1,024 and 4 sinks: 16.9; 8 rows of
+// 513 to 1,025, heads of 64: 8.5.  bf16, 128 rows of at most 1,028 seen tokens, 312 MB:
+// 56.8 us, 5,490 GB/s, 82%; 64 rows of 4,100 seen tokens, 1,076 MB: 158.6 us, 6,785 GB/s.
 #include <cmath>
 #include <type_traits>
 
