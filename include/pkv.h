@@ -661,10 +661,10 @@ pkv_status paged_kv_read_q4(const pkv_dims *dims, const void *k_codes, const voi
  * outputs of the query heads that read it.  A token's weight, with its value's scale,
  * is rounded to 11 significant bits or to 2^-31 of the row's largest, whichever is
  * more; a query element under 2^-32 of its head's largest is off by up to 2^-40 of
- * that.  Rows short by the tokens that their last one sees (128 KB of K and V in a
- * group of kv heads, 256 KB with rows x groups for half the SMs; bf16 pools: 192 KB,
- * 512 KB for 8 heads of 128, and twice as many) are not split whatever num_splits is:
- * one kernel.  Otherwise one persistent kernel plus, when
+ * that.  Rows short by the tokens that their last one sees (56 KB of K and V in a
+ * group of kv heads and 8 KB a head of it, twice as many with rows x groups for half
+ * the SMs; bf16 pools: 128 KB and 16 KB a head, 1.5 times as many, 8 heads of 128
+ * 512 KB and 1024 KB) are not split whatever num_splits is: one kernel.  Otherwise one persistent kernel plus, when
  * num_splits > 1, the piece combine; a batch of more than 1024 rows x kv-head groups
  * (a group: 8, 4, 2 or 1 kv heads, the most that divide Hkv) takes several such
  * pairs, one after the other.  PKV_ERR_UNSUPPORTED: Hkv of more than 1024 groups, or

@@ -1318,7 +1318,7 @@ static bool stream_whole(const pkv_dims *dims, int hpc, int bits, int most_seen,
 {
     const long long rows = (long long)dims->B * (dims->Hkv / hpc);
     const long long head = bits == 4 ? dims->D / 2 + dims->D / 32 : dims->D * 2;
-    return most_seen * hpc * head * 2 <=
+    return head * most_seen * hpc * 2 <=
            pkv::stream_whole_bytes(bits, hpc, hpc * head >= pkv::kBulkRowBytes, 2 * rows >= sms);
 }
 

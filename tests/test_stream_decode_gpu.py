@@ -234,6 +234,39 @@ def test_a_wait_that_runs_out_is_reported():
 
 
 @pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("shape", [(32, 8, 64, 16), (32, 8, 128, 16), (16, 1, 128, 16), (128, 8, 128, 16), (4, 4, 64, 3)])
+def test_waits_that_run_out_on_shared_stages(shape, bits):
+    """Warps that fill a stage together, and one each: all of them end, and the next call is right."""
+    c = _cache(shape, [3000] * 4, bits, seed=26, max_seq_len=20000)
+    q = _q(c, 27)
+    try:
+        pkv.testing_set_handoff_wait_ns(0)
+        _, status = decode(c, q, bits)
+    finally:
+        pkv.testing_set_handoff_wait_ns(pkv.DEFAULT_HANDOFF_WAIT_NS)
+    assert status == pkv.FLAG_TIMEOUT
+    out, status = decode(c, q, bits)
+    assert status == 0
+    check(c, q, out, bits)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("bound", [20000, 1 << 28, (1 << 30) - 1000])
+def test_a_wide_length_bound_splits_rows(bound, bits):
+    """The bytes of a row of 2^28 tokens and more pass 31 bits: it is not a short one. Pieces of a
+    split row are left in the workspace, a whole row leaves none."""
+    c = _cache((8, 8, 64, 16), [3000], bits, seed=28, max_seq_len=bound)
+    q = _q(c, 29)
+    ws = pkv.alloc_workspace(c.d, 8, DEV)
+    pkv.workspace_init(ws)
+    ws[256:] = 0x5a
+    out, status = decode(c, q, bits, splits=8, ws=ws)
+    assert status == 0
+    check(c, q, out, bits)
+    assert bool((ws[256:] != 0x5a).any())
+
+
+@pytest.mark.parametrize("bits", [4, 16])
 @pytest.mark.parametrize("shape", [(16, 4, 128, 16), (1, 1, 64, 16)])
 def test_a_plan_of_the_8_bit_decode_stays(shape, bits):
     """A step whose 8-bit layers run on their plan, with other layers between them."""
