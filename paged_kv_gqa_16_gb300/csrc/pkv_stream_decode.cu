@@ -43,7 +43,7 @@
 // the copy bandwidth (the 8-bit cache's 322 MB: 57.7, bf16's 631 MB: 97); one row of
 // 32,768, 32 heads: 17.0 us; 32 rows through a window of 1,024 and 4 sinks: 16.9; 8 rows of
 // 513 to 1,025, heads of 64: 8.5.  bf16, 128 rows of at most 1,028 seen tokens, 312 MB:
-// 56.8 us, 5,490 GB/s, 82%; 64 rows of 4,100 seen tokens, 1,076 MB: 158.6 us, 6,785 GB/s.
+// 55.9 us, 5,580 GB/s, 84%; 64 rows of 4,100 seen tokens, 1,076 MB: 158.6 us, 6,785 GB/s.
 #include <cmath>
 #include <type_traits>
 
@@ -72,16 +72,21 @@ struct StreamCfg {
     // banks: a lane's instruction in place of four of a warp.  (Shorter ones would be
     // slower so: the copy engine takes about 24 copies a microsecond and SM.)
     static constexpr bool kBulk = BITS == 16 && HPC * D * BITS / 8 >= kBulkRowBytes;
-    static_assert(!kBulk || kTok == 16, "a lane copies a row of K or of V");
+    static_assert(!kBulk || kTok == 16, "a stage is one tile, zeroed to its end");
     // Producer warps, and how many fill a stage together, a part of its tokens each.
     // Together they bring the first stage sooner and issue more in flight: bf16, 512 rows
     // of 2048 tokens, 8 heads of D = 64, 402 us -> 330 with four a stage, one row of 64 8.0
-    // -> 5.8.  A stage of codes is smaller, and each share costs its own steps: two a
+    // -> 5.8; 8 heads of 128 by bulk copies, 76 rows of 256, 20.0 (three warps, a stage
+    // each in turn) -> 17.0, one row of 64 7.2 -> 6.6, the windows' serving batch 56.8 ->
+    // 55.9.  A stage of codes is smaller, and each share costs its own steps: two a
     // stage 17.45 us -> 17.1 for a row of 32768, 4 bits, and four 16.5, but a batch of 512
     // 166 us -> 198.  (Two tiles of heads at D = 128 take 437 us with three warps and 462
     // with four.)
-    static constexpr int kProducers = kTok == 16 && D == 128 ? 3 : 4;
-    static constexpr int kSplit = kBulk ? 1 : BITS == 16 ? 4 : kTok >= 32 ? 2 : 1;
+    static constexpr int kProducers = BITS == 4 && kTok == 16 && D == 128 ? 3 : 4;
+    static constexpr int kSplit = BITS == 16 ? 4 : kTok >= 32 ? 2 : 1;
+    // Barriers of a full stage.  By bulk copies one for each of its producers: each can
+    // then wait for its own copies, whatever the others did.
+    static constexpr int kFulls = kBulk ? kSplit : 1;
     static constexpr int kShare = kTok / kSplit;           // tokens of a warp
     static constexpr int kTurn = kProducers / kSplit;      // stages from a warp's one to its next
     static constexpr int kThreads = (kWarps + kProducers) * 32;
@@ -96,17 +101,18 @@ struct StreamCfg {
     // joining parts: half of them leave half of their registers, a slot a warp
     static constexpr int kJoinFloats = NT * (D / 16 * 2 + 2);
     static constexpr int kJoinBytes = kWph == 1 ? 0 : kWarps / 2 * kJoinFloats * 32 * 4;
-    static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 16;
+    static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 32;
     static constexpr int kStagesFit =
-        (kSmemLimit - kFixedBytes) / (kStageBytes + kScaleBytes + 16);
+        (kSmemLimit - kFixedBytes) / (kStageBytes + kScaleBytes + 8 * (kFulls + 1));
     // A multiple of the turns: a slot then always belongs to the same producers.
     static constexpr int kStages = (kStagesFit > 12 ? 12 : kStagesFit) / kTurn * kTurn;
     static_assert(kStages >= 3 && kStages % kTurn == 0, "a slot has its producers");
+    static_assert(!kBulk || (2 * kShare <= 32 && kTurn == 1), "a lane copies a row of K or of V");
     static_assert(kShare >= 4 && (kShare & (kShare - 1)) == 0, "no carry in the swizzle");
     static constexpr int kScaleOffset = kStages * kStageBytes;
     static constexpr int kJoinOffset = kScaleOffset + kStages * kScaleBytes;
     static constexpr int kBarOffset = kJoinOffset + kJoinBytes;
-    static constexpr int kAbortOffset = kBarOffset + 2 * kStages * 8;
+    static constexpr int kAbortOffset = kBarOffset + (((kFulls + 1) * kStages * 8 + 15) & ~15);
     static constexpr int kPrefixOffset = kAbortOffset + 16;
     static constexpr int kSmemBytes = kPrefixOffset + (kQ8MaxRows + 1) * 4;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
     const FusedParams &p = sp.f;
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOffset);
-    uint64_t *empty = full + NST;
+    uint64_t *empty = full + NST * C::kFulls;
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kAbortOffset);
     int *prefix = reinterpret_cast<int *>(smem + C::kPrefixOffset);
 
@@ -218,7 +224,8 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             // a producer warp's lanes, or kSplit warps once and their lanes' copies
-            mbar_init(&full[i], C::kBulk ? 32 : 33 * C::kSplit);
+            for (int j = 0; j < C::kFulls; ++j)
+                mbar_init(&full[i * C::kFulls + j], C::kBulk ? 32 : 33 * C::kSplit);
             mbar_init(&empty[i], kWarps);
         }
         fence_mbar_init();
@@ -385,28 +392,30 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                 }
             };
             if constexpr (C::kBulk) {
-                // Lane l: token l % 16, K or (from lane 16 on) V.  The rows of V that end
-                // the piece's last tile are zeroed: their weights are 0, and what a
-                // stage held may be NaN.
-                const int t16 = lane & 15;
-                const bool of_v = lane >= 16, there = t16 < nvalid;
-                const int t = there ? token(cur, cur.tok + t16) : 0;
-                const int page = checked(__shfl_sync(kFull, ids[0], t16), there);
+                // Lane l: token first + l % kShare, K, or from lane kShare on V.  The rows
+                // of V that end the piece's last tile are zeroed: their weights are 0,
+                // and what a stage held may be NaN.
+                const int at = lane % C::kShare;
+                const bool mine = lane < 2 * C::kShare, of_v = lane >= C::kShare;
+                const bool there = mine && at < nvalid;
+                const int t = there ? token(cur, tok0 + at) : 0;
+                const int page = checked(__shfl_sync(kFull, ids[0], at), there);
+                uint64_t *bar = &full[st * C::kFulls + pw];
                 fence_proxy_async_smem();          // the slot's last reads, before the copies
-                unsigned char *to = stage + ((of_v ? C::kTok : 0) + t16) * C::kPitch;
-                if (of_v && !there)
+                unsigned char *to = stage + ((of_v ? C::kTok : 0) + first + at) * C::kPitch;
+                if (mine && of_v && !there)
                     for (int j = 0; j < C::kRowBytes / 16; ++j)
                         reinterpret_cast<uint4 *>(to)[j] = make_uint4(0u, 0u, 0u, 0u);
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&full[st], (uint32_t)(nvalid * 2 * C::kRowBytes));
+                    mbar_arrive_expect_tx(bar, (uint32_t)(nvalid * 2 * C::kRowBytes));
                 else
-                    mbar_arrive(&full[st]);
+                    mbar_arrive(bar);
                 if (there) {
                     const size_t slot = (size_t)page * p.page_size + t - page_of_tok(t) * p.page_size;
                     const uint8_t *from = (of_v ? p.v_codes : p.k_codes) +
                                           slot * ((size_t)p.Hkv * C::kHeadBytes) +
                                           (size_t)cur.hg * C::kRowBytes;
-                    bulk_copy_g2s_hint(to, from, C::kRowBytes, &full[st], policy);
+                    bulk_copy_g2s_hint(to, from, C::kRowBytes, bar, policy);
                 }
             } else {
                 // bf16: the rows of V that end the piece's last tile are zeroed (their
@@ -471,9 +480,10 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
         // Let this warp's copies land before it exits, with the full time
         // limit: a consumer that gave up skips its stages, and the block must
         // not exit while a copy into its shared memory is in flight.
-        if constexpr (C::kSplit == 1) {
+        if constexpr (C::kBulk || C::kSplit == 1) {
+            const int f = C::kBulk ? pw : 0;
             for (int k = it - C::kTurn, n = 0; k >= 0 && n < NST; k -= C::kTurn, n += C::kTurn)
-                (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
+                (void)mbar_wait_bounded(&full[k % NST * C::kFulls + f], (uint32_t)((k / NST) & 1));
         } else {
             // A stage is kSplit warps': one that gave up leaves the others' last stages
             // open, so what is waited for is this thread's copies, and then the
@@ -590,7 +600,11 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
 
         for (int tok = t0; tok < t1; tok += C::kTok) {
             if (!aborted) {
-                const bool ok = mbar_wait_or_abort(&full[st], phase, p.handoff_wait_ns, abort);
+                bool ok = true;
+#pragma unroll
+                for (int f = 0; f < C::kFulls; ++f)
+                    ok = ok && mbar_wait_or_abort(&full[st * C::kFulls + f], phase,
+                                                  p.handoff_wait_ns, abort);
                 if (!__all_sync(kFull, ok)) {
                     aborted = true;
                     if (lane == 0) {
