@@ -101,7 +101,10 @@ struct StreamCfg {
     // joining parts: half of them leave half of their registers, a slot a warp
     static constexpr int kJoinFloats = NT * (D / 16 * 2 + 2);
     static constexpr int kJoinBytes = kWph == 1 ? 0 : kWarps / 2 * kJoinFloats * 32 * 4;
-    static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 32;
+    // the abort word and the producer warps' ends, 16 bytes for either
+    static constexpr int kEndBytes = 32;
+    static_assert(kProducers <= 4, "room for their ends");
+    static constexpr int kFixedBytes = kJoinBytes + (kQ8MaxRows + 1) * 4 + 16 + kEndBytes;
     static constexpr int kStagesFit =
         (kSmemLimit - kFixedBytes) / (kStageBytes + kScaleBytes + 8 * (kFulls + 1));
     // A multiple of the turns: a slot then always belongs to the same producers.
@@ -113,7 +116,7 @@ struct StreamCfg {
     static constexpr int kJoinOffset = kScaleOffset + kStages * kScaleBytes;
     static constexpr int kBarOffset = kJoinOffset + kJoinBytes;
     static constexpr int kAbortOffset = kBarOffset + (((kFulls + 1) * kStages * 8 + 15) & ~15);
-    static constexpr int kPrefixOffset = kAbortOffset + 16;
+    static constexpr int kPrefixOffset = kAbortOffset + kEndBytes;
     static constexpr int kSmemBytes = kPrefixOffset + (kQ8MaxRows + 1) * 4;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory budget");
     static_assert(kBulk || kStageBytes % 1024 == 0, "swizzled rows");
@@ -477,24 +480,39 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                 ids[k] = next[k];
             cur = after;
         }
-        // Let this warp's copies land before it exits, with the full time
-        // limit: a consumer that gave up skips its stages, and the block must
-        // not exit while a copy into its shared memory is in flight.
+        // Let this warp's copies land, and their arrivals, before it exits, with the full
+        // time limit: a consumer that gave up skips its stages, and the block must not
+        // exit while a copy into its shared memory is in flight.
         if constexpr (C::kBulk || C::kSplit == 1) {
             const int f = C::kBulk ? pw : 0;
             for (int k = it - C::kTurn, n = 0; k >= 0 && n < NST; k -= C::kTurn, n += C::kTurn)
                 (void)mbar_wait_bounded(&full[k % NST * C::kFulls + f], (uint32_t)((k / NST) & 1));
         } else {
-            // A stage is kSplit warps': one that gave up leaves the others' last stages
-            // open, so what is waited for is this thread's copies, and then the
-            // arrivals that they trigger, unless somebody gave up.
+            // A stage's barrier is kSplit warps', which filled the same stages unless
+            // somebody gave up.
             cp_async_wait_all();
             for (int k = it - C::kTurn, n = 0; k >= 0 && n < NST && !*abort;
                  k -= C::kTurn, n += C::kTurn)
                 (void)mbar_wait_or_abort(&full[k % NST], (uint32_t)((k / NST) & 1),
                                          kWaitLimitNs, abort);
-            if (*abort)
-                __nanosleep(1000);
+            volatile int *ends = abort + 4;
+            if (lane == 0)
+                ends[pw] = it;
+            named_bar_sync(2, C::kProducers * 32);
+            if (*abort) {
+                // Then a warp arrives in the stages that the others filled without it, so
+                // that each completes, and waits for them all.  (Who fills a slot again has
+                // seen its last filling complete: the arrivals go to the stages meant.)
+                int last = it;
+                for (int i = 0; i < C::kSplit; ++i)
+                    last = max(last, ends[pw / C::kSplit * C::kSplit + i]);
+                if (lane == 0)
+                    for (int k = it; k < last; k += C::kTurn)
+                        mbar_arrive(&full[k % NST], 33);
+                for (int k = last - C::kTurn, n = 0; k >= 0 && n < NST;
+                     k -= C::kTurn, n += C::kTurn)
+                    (void)mbar_wait_bounded(&full[k % NST], (uint32_t)((k / NST) & 1));
+            }
         }
         grid_launch_dependents();
         return;
