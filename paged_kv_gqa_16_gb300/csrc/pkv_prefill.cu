@@ -1424,7 +1424,8 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const __grid_constan
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (i0 + j >= np || !(ml[j].y > 0.f))
+            // (a part in which the row sees nothing adds nothing; a NaN sum stays)
+            if (i0 + j >= np || ml[j].y == 0.f)
                 continue;
             if (ml[j].x > mm) {
                 const float r = ex2_fast(mm - ml[j].x);        // 0 while mm is -inf
