@@ -190,50 +190,69 @@ def _pool_ptr(d: Dims, x) -> Optional[int]:
     return _ptr(x)
 
 
-def _bf16_ptr(x) -> Optional[int]:
+def _slot_values(d: Dims) -> int:
+    """Values of K (or V) in a pool of these dims."""
+    return d.num_pages * d.page_size * d.Hkv * d.D
+
+
+def _bf16_ptr(x, least: int) -> Optional[int]:
+    """The pointer of a bf16 tensor of at least `least` values."""
     try:
         if x.dtype is _bf16 and x.is_contiguous():
+            if x.numel() < least:
+                raise ValueError(f"a tensor of {tuple(x.shape)} is too small: these dims take "
+                                 f"{least} values")
             return x.data_ptr()
     except AttributeError:                        # a raw pointer or None
         return x
     if _bf16 is None:
         _load_types()
-        return _bf16_ptr(x)
+        return _bf16_ptr(x, least)
     raise ValueError(f"expected a contiguous bf16 tensor, got {x.dtype}")
 
 
-def _q8_ptr(x, types) -> Optional[int]:
+def _q8_ptr(x, types, least: int) -> Optional[int]:
     if x is None or x.__class__ is int:
         return x
     if x.dtype in types and x.is_contiguous():
+        if x.numel() < least:
+            raise ValueError(f"an 8-bit cache's tensor of {tuple(x.shape)} is too small: these "
+                             f"dims take {least} bytes")
         return x.data_ptr()
     raise ValueError("an 8-bit cache has contiguous e4m3 codes (torch.float8_e4m3fn or uint8) and "
                      f"e8m0 scales (torch.float8_e8m0fnu or uint8), got {x.dtype}")
 
 
-def _q8_ptrs(k, v, ks, vs):
+def _q8_ptrs(d: Dims, k, v, ks, vs):
     """The pointers of an 8-bit cache's codes and scales."""
+    heads = d.num_pages * d.page_size * d.Hkv
+    n = heads * d.D
     try:                                          # (four tensors at once: 0.2 us less)
         if (k.dtype in _codes and v.dtype in _codes and ks.dtype in _scales and
                 vs.dtype in _scales and k.is_contiguous() and v.is_contiguous() and
-                ks.is_contiguous() and vs.is_contiguous()):
+                ks.is_contiguous() and vs.is_contiguous() and k.numel() >= n and
+                v.numel() >= n and ks.numel() >= heads and vs.numel() >= heads):
             return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
     except AttributeError:                        # a raw pointer or None among them
         pass
     if _bf16 is None:
         _load_types()
-    return _q8_ptr(k, _codes), _q8_ptr(v, _codes), _q8_ptr(ks, _scales), _q8_ptr(vs, _scales)
+    return (_q8_ptr(k, _codes, n), _q8_ptr(v, _codes, n), _q8_ptr(ks, _scales, heads),
+            _q8_ptr(vs, _scales, heads))
 
 
-def _q4_ptrs(k, v, ks, vs):
-    """The pointers of a 4-bit cache's codes and scales: bytes, 16 of codes for one of
-    scales (an 8-bit cache's have the same types, and other sizes)."""
+def _q4_ptrs(k, v, ks, vs, least: int = 0):
+    """The pointers of a 4-bit cache's codes and scales, of at least `least` values: bytes,
+    16 of codes for one of scales (an 8-bit cache's have the same types, and other sizes)."""
     try:
         n = k.numel()
         if (n == v.numel() == 16 * ks.numel() == 16 * vs.numel() and k.dtype in _bytes and
                 v.dtype in _bytes and ks.dtype in _scales and vs.dtype in _scales and
                 k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and
                 vs.is_contiguous()):
+            if 2 * n < least:
+                raise ValueError(f"4-bit codes of {tuple(k.shape)} are too few: these dims take "
+                                 f"{least} values")
             return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
     except AttributeError:                        # raw pointers, or a None among tensors
         if all(x is None or x.__class__ is int for x in (k, v, ks, vs)):
@@ -241,7 +260,7 @@ def _q4_ptrs(k, v, ks, vs):
         raise ValueError("a 4-bit cache is four tensors, or four pointers") from None
     if _bf16 is None:
         _load_types()
-        return _q4_ptrs(k, v, ks, vs)
+        return _q4_ptrs(k, v, ks, vs, least)
     raise ValueError("a 4-bit cache has contiguous uint8 codes [num_pages, page_size, Hkv, D / 2] and e8m0 "
                      "scales [num_pages, page_size, Hkv, D / 32] (uint8 or torch.float8_e8m0fnu), got "
                      f"{[(x.dtype, tuple(x.shape)) for x in (k, v, ks, vs)]}")
@@ -542,18 +561,20 @@ def paged_kv_append_norm(d: Dims, t: Tokens, k_pool, v_pool, kv_indices, kv_indp
                          status=None, stream=None) -> None:
     """One new token a row: q and K normalised and rotated, K/V to their slots."""
     _token_count(d, t, per_row=True)
+    n = _slot_values(d)
     _check("paged_kv_append_norm", lib().paged_kv_append_norm(
-        ctypes.byref(d), ctypes.byref(t), _bf16_ptr(k_pool), _bf16_ptr(v_pool), _ptr(kv_indices),
-        _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
+        ctypes.byref(d), ctypes.byref(t), _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
 def paged_kv_extend_norm(d: Dims, t: Tokens, qo_indptr, k_pool, v_pool, kv_indices, kv_indptr,
                          seq_lens, status=None, stream=None) -> None:
     """paged_kv_append_norm for ragged chunks of new tokens."""
+    n = _slot_values(d)
     _check("paged_kv_extend_norm", lib().paged_kv_extend_norm(
-        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t), _bf16_ptr(k_pool),
-        _bf16_ptr(v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status),
-        _stream(stream)))
+        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
+        _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n), _ptr(kv_indices), _ptr(kv_indptr),
+        _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
 # ---- the 8-bit cache ----------------------------------------------------------
@@ -564,7 +585,7 @@ def paged_kv_append_q8(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, k
     (torch.float8_e8m0fnu or uint8)."""
     _token_count(d, t, per_row=True)
     _check("paged_kv_append_q8", lib().paged_kv_append_q8(
-        ctypes.byref(d), ctypes.byref(t), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
+        ctypes.byref(d), ctypes.byref(t), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -573,7 +594,7 @@ def paged_kv_extend_q8(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale,
     """paged_kv_append_q8 for ragged chunks of new tokens."""
     _check("paged_kv_extend_q8", lib().paged_kv_extend_q8(
         ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
-        *_q8_ptrs(k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
+        *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
         _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -581,20 +602,22 @@ def paged_kv_read_q8(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv
                      seq_lens, k_out, v_out, status=None, stream=None) -> None:
     """Every row's tokens as bf16 into pages [num_indices, page_size, Hkv, D]
     in the table's order (pools for paged_prefill_attn with kv_indices 0, 1, ...)."""
+    n = d.num_indices * d.page_size * d.Hkv * d.D
     _check("paged_kv_read_q8", lib().paged_kv_read_q8(
-        ctypes.byref(d), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out), _bf16_ptr(v_out),
-        _ptr(status), _stream(stream)))
+        ctypes.byref(d), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out, n),
+        _bf16_ptr(v_out, n), _ptr(status), _stream(stream)))
 
 
 def paged_decode_attn_q8(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
                          seq_lens, num_splits: int, workspace, out, stream=None) -> None:
     """paged_decode_attn over an 8-bit cache."""
     ws_bytes = workspace.numel() * workspace.element_size()
+    rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_q8", lib().paged_decode_attn_q8(
-        ctypes.byref(d), _bf16_ptr(q), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
+        ctypes.byref(d), _bf16_ptr(q, rows), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
-        ws_bytes, _bf16_ptr(out), _stream(stream)))
+        ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
 
 
 def paged_decode_plan_q8(d: Dims, kv_indices, kv_indptr, seq_lens, num_splits: int, workspace,
@@ -611,10 +634,11 @@ def paged_decode_attn_q8_planned(d: Dims, q, k_codes, v_codes, k_scale, v_scale,
                                  stream=None) -> None:
     """paged_decode_attn_q8 on the workspace's plan (a step's later layers)."""
     ws_bytes = workspace.numel() * workspace.element_size()
+    rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_q8_planned", lib().paged_decode_attn_q8_planned(
-        ctypes.byref(d), _bf16_ptr(q), *_q8_ptrs(k_codes, v_codes, k_scale, v_scale),
+        ctypes.byref(d), _bf16_ptr(q, rows), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
-        ws_bytes, _bf16_ptr(out), _stream(stream)))
+        ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
 
 
 # ---- the 4-bit cache ----------------------------------------------------------
@@ -625,8 +649,9 @@ def paged_kv_append_q4(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, k
     [num_pages, page_size, Hkv, D / 32] (uint8 or torch.float8_e8m0fnu)."""
     _token_count(d, t, per_row=True)
     _check("paged_kv_append_q4", lib().paged_kv_append_q4(
-        ctypes.byref(d), ctypes.byref(t), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
+        ctypes.byref(d), ctypes.byref(t),
+        *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)), _ptr(kv_indices),
+        _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
 def paged_kv_extend_q4(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale, v_scale,
@@ -634,17 +659,18 @@ def paged_kv_extend_q4(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale,
     """paged_kv_append_q4 for ragged chunks of new tokens."""
     _check("paged_kv_extend_q4", lib().paged_kv_extend_q4(
         ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
-        *_q4_ptrs(k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
-        _ptr(seq_lens), _ptr(status), _stream(stream)))
+        *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)), _ptr(kv_indices),
+        _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
 def paged_kv_read_q4(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
                      seq_lens, k_out, v_out, status=None, stream=None) -> None:
     """paged_kv_read_q8 of a 4-bit cache."""
+    n = d.num_indices * d.page_size * d.Hkv * d.D
     _check("paged_kv_read_q4", lib().paged_kv_read_q4(
-        ctypes.byref(d), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out), _bf16_ptr(v_out),
-        _ptr(status), _stream(stream)))
+        ctypes.byref(d), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out, n),
+        _bf16_ptr(v_out, n), _ptr(status), _stream(stream)))
 
 
 def paged_decode_attn_q4(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
@@ -653,10 +679,12 @@ def paged_decode_attn_q4(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indi
     """paged_decode_attn over a 4-bit cache; with a window, over each row's last
     `window` tokens and its first `sinks`."""
     ws_bytes = workspace.numel() * workspace.element_size()
+    rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_q4", lib().paged_decode_attn_q4(
-        ctypes.byref(d), _bf16_ptr(q), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale),
+        ctypes.byref(d), _bf16_ptr(q, rows),
+        *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits,
-        _ptr(workspace), ws_bytes, _bf16_ptr(out), _stream(stream)))
+        _ptr(workspace), ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
 
 
 # ---- sliding windows ----------------------------------------------------------
@@ -666,10 +694,12 @@ def paged_decode_attn_window(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, 
     """paged_decode_attn in which a row's query sees the last `window` of its
     seq_lens[b] tokens and the first `sinks` (window 0: all)."""
     ws_bytes = workspace.numel() * workspace.element_size()
+    n = _slot_values(d)
+    rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_window", lib().paged_decode_attn_window(
-        ctypes.byref(d), _bf16_ptr(q), _bf16_ptr(k_pool), _bf16_ptr(v_pool), _ptr(kv_indices),
-        _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits, _ptr(workspace), ws_bytes,
-        _bf16_ptr(out), _stream(stream)))
+        ctypes.byref(d), _bf16_ptr(q, rows), _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n),
+        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits,
+        _ptr(workspace), ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
 
 
 def paged_prefill_attn_window(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices, kv_indptr,
@@ -679,11 +709,12 @@ def paged_prefill_attn_window(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices,
     and the row's first `sinks` (window 0: all up to its own)."""
     total_q = int(q.shape[0])
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    n, rows = _slot_values(d), total_q * d.Hq * d.D
     _check("paged_prefill_attn_window", lib().paged_prefill_attn_window(
-        ctypes.byref(d), _bf16_ptr(q), _ptr(qo_indptr), total_q,
-        total_q if max_q_len is None else int(max_q_len), _bf16_ptr(k_pool), _bf16_ptr(v_pool),
-        _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, _ptr(workspace), ws_bytes,
-        _bf16_ptr(out), _ptr(status), _stream(stream)))
+        ctypes.byref(d), _bf16_ptr(q, rows), _ptr(qo_indptr), total_q,
+        total_q if max_q_len is None else int(max_q_len), _bf16_ptr(k_pool, n),
+        _bf16_ptr(v_pool, n), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks,
+        _ptr(workspace), ws_bytes, _bf16_ptr(out, rows), _ptr(status), _stream(stream)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
