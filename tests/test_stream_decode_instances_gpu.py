@@ -1,4 +1,6 @@
-"""GPU tests over every kernel of the stream decode: the way out when a wait runs out."""
+"""GPU tests of the stream decode's kernels that have a pipeline of their own: many query heads
+over eight kv heads, bulk copies from pages of any size, and every kernel's way out when a wait
+runs out."""
 
 import pytest
 import torch
@@ -8,6 +10,24 @@ from paged_kv_gqa_16_gb300 import pkv
 from q4_cases import check, decode
 
 pytestmark = pytest.mark.gpu
+
+# Hq, Hkv, D, page size: two tiles of query heads over eight kv heads, at D = 64 (at 4 bits stages
+# of one tile, a warp each) and 128 (bulk copies at 16); bulk copies from pages of 17 and 24
+SHAPES = [(128, 8, 64, 16), (128, 8, 128, 24), (32, 8, 128, 17)]
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_whole_rows(shape, bits):
+    stream.test_whole_rows(shape, bits)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (4097, 4), (2500, 1700)])
+def test_split_rows(shape, window, sinks, bits):
+    stream.test_split_rows(shape, window, sinks, bits)
+
 
 @pytest.mark.parametrize("bits", [4, 16])
 @pytest.mark.parametrize("D", [64, 128])
