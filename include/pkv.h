@@ -646,7 +646,17 @@ pkv_status paged_kv_extend_q4(const pkv_dims *dims, const pkv_tokens *tokens,
                               const int32_t *kv_indices, const int32_t *kv_indptr,
                               const int32_t *seq_lens, uint32_t *status, pkv_stream_t stream);
 
-/* paged_kv_read_q8 of a 4-bit cache: the same outputs, checks and flags. */
+/* paged_kv_read_q8 of a 4-bit cache: the same outputs, checks and flags.
+ * A row whose pages behind a window were given away, their entries then outside the
+ * pool, would be flagged (PKV_FLAG_BAD_PAGE), by either call.  What a windowed chunk
+ * sees of it is read without that, and without the rest, by two calls:
+ *  - the window: kv_indptr[b] advanced by the s pages before the one with the first
+ *    key seen, seq_lens[b] less s * page_size (the row before then seems to have those
+ *    entries, behind its length);
+ *  - the sinks: the whole kv_indptr, seq_lens[b] cut to the tokens of the sinks' pages
+ *    (whole pages, which is what the prefill takes).
+ * An entry's tokens go to its own place all the same, so paged_prefill_attn_window takes
+ * the outputs with the whole kv_indptr and seq_lens. */
 pkv_status paged_kv_read_q4(const pkv_dims *dims, const void *k_codes, const void *v_codes,
                             const void *k_scale, const void *v_scale,
                             const int32_t *kv_indices, const int32_t *kv_indptr,

@@ -665,7 +665,9 @@ def paged_kv_extend_q4(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale,
 
 def paged_kv_read_q4(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
                      seq_lens, k_out, v_out, status=None, stream=None) -> None:
-    """paged_kv_read_q8 of a 4-bit cache."""
+    """paged_kv_read_q8 of a 4-bit cache.  A row whose pages behind a window were given
+    away is read from its window's first page on by a kv_indptr advanced to it and
+    seq_lens without the tokens before it, and its sinks' pages by a second call."""
     n = d.num_indices * d.page_size * d.Hkv * d.D
     _check("paged_kv_read_q4", lib().paged_kv_read_q4(
         ctypes.byref(d), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)),
