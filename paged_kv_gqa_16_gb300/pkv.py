@@ -301,18 +301,17 @@ def version() -> int:
 
 
 def split_chunk(d: Dims, num_splits: int) -> int:
-    return lib().pkv_split_chunk(ctypes.byref(d), num_splits)
+    return lib().pkv_split_chunk(d, num_splits)
 
 
 def workspace_bytes(d: Dims, num_splits: int) -> int:
-    return lib().pkv_workspace_bytes(ctypes.byref(d), num_splits)
+    return lib().pkv_workspace_bytes(d, num_splits)
 
 
 def workspace_layout(d: Dims, num_splits: int):
     ml, o = ctypes.c_size_t(), ctypes.c_size_t()
     _check("pkv_workspace_layout",
-           lib().pkv_workspace_layout(ctypes.byref(d), num_splits, ctypes.byref(ml),
-                                      ctypes.byref(o)))
+           lib().pkv_workspace_layout(d, num_splits, ctypes.byref(ml), ctypes.byref(o)))
     return ml.value, o.value
 
 
@@ -321,12 +320,12 @@ def plan(d: Dims, num_sms: Optional[int] = None):
         import torch
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
     s, ws = ctypes.c_int(), ctypes.c_size_t()
-    _check("pkv_plan", lib().pkv_plan(ctypes.byref(d), num_sms, ctypes.byref(s), ctypes.byref(ws)))
+    _check("pkv_plan", lib().pkv_plan(d, num_sms, ctypes.byref(s), ctypes.byref(ws)))
     return s.value, ws.value
 
 
 def workspace_init(workspace, stream=None) -> None:
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("pkv_workspace_init",
            lib().pkv_workspace_init(_ptr(workspace), ws_bytes, _stream(stream)))
 
@@ -340,16 +339,16 @@ def paged_kv_append(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indices, kv_ind
                     seq_lens, rope_cos_sin=None, rope_max_pos: int = 0, rope_q: bool = False,
                     status=None, stream=None) -> None:
     _check("paged_kv_append", lib().paged_kv_append(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        d, _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
         _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(rope_cos_sin),
         rope_max_pos, int(bool(rope_q)), _ptr(status), _stream(stream)))
 
 
 def paged_decode_attn(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, seq_lens,
                       num_splits: int, workspace, out, stream=None) -> None:
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_decode_attn", lib().paged_decode_attn(
-        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
+        d, _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace), ws_bytes, _ptr(out),
         _stream(stream)))
 
@@ -357,9 +356,9 @@ def paged_decode_attn(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, seq_len
 def paged_decode_step(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indices, kv_indptr,
                       seq_lens, rope_cos_sin, rope_max_pos: int, num_splits: int, workspace,
                       out, stream=None) -> None:
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_decode_step", lib().paged_decode_step(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        d, _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
         _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
         _ptr(rope_cos_sin), rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out),
         _stream(stream)))
@@ -369,17 +368,17 @@ def paged_decode_plan(d: Dims, kv_indices, kv_indptr, seq_lens, num_splits: int,
                       stream=None) -> None:
     """The step's plan (the block partition and first page-table windows)
     written into the workspace for the *_planned calls of the same step."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_decode_plan", lib().paged_decode_plan(
-        ctypes.byref(d), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits,
+        d, _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits,
         _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def paged_decode_attn_planned(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, seq_lens,
                               num_splits: int, workspace, out, stream=None) -> None:
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_decode_attn_planned", lib().paged_decode_attn_planned(
-        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
+        d, _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace), ws_bytes, _ptr(out),
         _stream(stream)))
 
@@ -387,9 +386,9 @@ def paged_decode_attn_planned(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr,
 def paged_decode_step_planned(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indices, kv_indptr,
                               seq_lens, rope_cos_sin, rope_max_pos: int, num_splits: int,
                               workspace, out, stream=None) -> None:
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_decode_step_planned", lib().paged_decode_step_planned(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        d, _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
         _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
         _ptr(rope_cos_sin), rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out),
         _stream(stream)))
@@ -402,7 +401,7 @@ def paged_kv_advance(d: Dims, seq_lens, kv_indptr, kv_indices, free_pages, free_
     a page; seq_lens, kv_indices and free_head are updated on the device."""
     num_free = 0 if free_pages is None else int(free_pages.numel())
     _check("paged_kv_advance", lib().paged_kv_advance(
-        ctypes.byref(d), _ptr(seq_lens), _ptr(kv_indptr), _ptr(kv_indices), _ptr(free_pages),
+        d, _ptr(seq_lens), _ptr(kv_indptr), _ptr(kv_indices), _ptr(free_pages),
         num_free, _ptr(free_head), _ptr(status), _stream(stream)))
 
 
@@ -413,10 +412,10 @@ def paged_decode_step_advance(d: Dims, q, k_new, v_new, k_pool, v_pool, kv_indic
     """paged_decode_step, then paged_kv_advance (its flags in the workspace
     status word): one decode-loop step that leaves the metadata ready for
     the next."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     num_free = 0 if free_pages is None else int(free_pages.numel())
     _check("paged_decode_step_advance", lib().paged_decode_step_advance(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
+        d, _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_pool),
         _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
         _ptr(rope_cos_sin), rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out),
         _ptr(free_pages), num_free, _ptr(free_head), _stream(stream)))
@@ -430,10 +429,10 @@ def decode_attn_contig(d: Dims, q, k_cache, v_cache, seq_lens, num_splits: int, 
     (None: slot b).  With k_new / v_new it is the whole decode step.
     planned: decode_attn_contig_planned (the table and plan the step's first
     call left in the workspace)."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     name = "decode_attn_contig_planned" if planned else "decode_attn_contig"
     _check(name, getattr(lib(), name)(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_cache),
+        d, _ptr(q), _ptr(k_new), _ptr(v_new), _pool_ptr(d, k_cache),
         _pool_ptr(d, v_cache), _ptr(cache_batch_idx), _ptr(seq_lens), _ptr(rope_cos_sin),
         rope_max_pos, num_splits, _ptr(workspace), ws_bytes, _ptr(out), _stream(stream)))
 
@@ -452,13 +451,13 @@ def paged_prefill_attn(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices, kv_ind
     mq = total_q if max_q_len is None else int(max_q_len)
     if workspace is None:
         _check("paged_prefill_attn", lib().paged_prefill_attn(
-            ctypes.byref(d), _ptr(q), _ptr(qo_indptr), total_q, mq, _pool_ptr(d, k_pool),
+            d, _ptr(q), _ptr(qo_indptr), total_q, mq, _pool_ptr(d, k_pool),
             _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(out),
             _ptr(status), _stream(stream)))
         return
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_prefill_attn_ws", lib().paged_prefill_attn_ws(
-        ctypes.byref(d), _ptr(q), _ptr(qo_indptr), total_q, mq, _pool_ptr(d, k_pool),
+        d, _ptr(q), _ptr(qo_indptr), total_q, mq, _pool_ptr(d, k_pool),
         _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens),
         _ptr(workspace), ws_bytes, _ptr(out), _ptr(status), _stream(stream)))
 
@@ -466,8 +465,7 @@ def paged_prefill_attn(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices, kv_ind
 def prefill_plan(d: Dims, max_q_len: int, num_sms: int, ws_bytes: int = 0) -> dict:
     """pkv_prefill_plan: the list paged_prefill_attn(_ws) would launch."""
     out = (ctypes.c_int32 * 7)()
-    _check("pkv_prefill_plan", lib().pkv_prefill_plan(ctypes.byref(d), int(max_q_len),
-                                                       int(num_sms), int(ws_bytes),
+    _check("pkv_prefill_plan", lib().pkv_prefill_plan(d, int(max_q_len), int(num_sms), int(ws_bytes),
                                                        ctypes.cast(out, ctypes.c_void_p)))
     keys = ("pairs", "units", "group_rows", "entries", "split", "split_base", "grid")
     return dict(zip(keys, list(out)))
@@ -485,7 +483,7 @@ def paged_kv_extend(d: Dims, q, k_new, v_new, qo_indptr, k_pool, v_pool, kv_indi
     at their slots: K rotated by position, V copied, q rotated if rope_q."""
     total_q = int(k_new.shape[0])
     _check("paged_kv_extend", lib().paged_kv_extend(
-        ctypes.byref(d), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(qo_indptr), total_q,
+        d, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(qo_indptr), total_q,
         _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices), _ptr(kv_indptr),
         _ptr(seq_lens), _ptr(rope_cos_sin), rope_max_pos, int(bool(rope_q)), _ptr(status),
         _stream(stream)))
@@ -563,7 +561,7 @@ def paged_kv_append_norm(d: Dims, t: Tokens, k_pool, v_pool, kv_indices, kv_indp
     _token_count(d, t, per_row=True)
     n = _slot_values(d)
     _check("paged_kv_append_norm", lib().paged_kv_append_norm(
-        ctypes.byref(d), ctypes.byref(t), _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n),
+        d, t, _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -572,7 +570,7 @@ def paged_kv_extend_norm(d: Dims, t: Tokens, qo_indptr, k_pool, v_pool, kv_indic
     """paged_kv_append_norm for ragged chunks of new tokens."""
     n = _slot_values(d)
     _check("paged_kv_extend_norm", lib().paged_kv_extend_norm(
-        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
+        d, t, _ptr(qo_indptr), _token_count(d, t),
         _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n), _ptr(kv_indices), _ptr(kv_indptr),
         _ptr(seq_lens), _ptr(status), _stream(stream)))
 
@@ -585,7 +583,7 @@ def paged_kv_append_q8(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, k
     (torch.float8_e8m0fnu or uint8)."""
     _token_count(d, t, per_row=True)
     _check("paged_kv_append_q8", lib().paged_kv_append_q8(
-        ctypes.byref(d), ctypes.byref(t), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        d, t, *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
 
@@ -593,7 +591,7 @@ def paged_kv_extend_q8(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale,
                        kv_indices, kv_indptr, seq_lens, status=None, stream=None) -> None:
     """paged_kv_append_q8 for ragged chunks of new tokens."""
     _check("paged_kv_extend_q8", lib().paged_kv_extend_q8(
-        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
+        d, t, _ptr(qo_indptr), _token_count(d, t),
         *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale), _ptr(kv_indices), _ptr(kv_indptr),
         _ptr(seq_lens), _ptr(status), _stream(stream)))
 
@@ -604,7 +602,7 @@ def paged_kv_read_q8(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv
     in the table's order (pools for paged_prefill_attn with kv_indices 0, 1, ...)."""
     n = d.num_indices * d.page_size * d.Hkv * d.D
     _check("paged_kv_read_q8", lib().paged_kv_read_q8(
-        ctypes.byref(d), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        d, *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out, n),
         _bf16_ptr(v_out, n), _ptr(status), _stream(stream)))
 
@@ -612,10 +610,10 @@ def paged_kv_read_q8(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv
 def paged_decode_attn_q8(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indices, kv_indptr,
                          seq_lens, num_splits: int, workspace, out, stream=None) -> None:
     """paged_decode_attn over an 8-bit cache."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_q8", lib().paged_decode_attn_q8(
-        ctypes.byref(d), _bf16_ptr(q, rows), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        d, _bf16_ptr(q, rows), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
         ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
 
@@ -623,9 +621,9 @@ def paged_decode_attn_q8(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indi
 def paged_decode_plan_q8(d: Dims, kv_indices, kv_indptr, seq_lens, num_splits: int, workspace,
                          stream=None) -> None:
     """paged_decode_plan for paged_decode_attn_q8_planned."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_decode_plan_q8", lib().paged_decode_plan_q8(
-        ctypes.byref(d), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits,
+        d, _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits,
         _ptr(workspace), ws_bytes, _stream(stream)))
 
 
@@ -633,10 +631,10 @@ def paged_decode_attn_q8_planned(d: Dims, q, k_codes, v_codes, k_scale, v_scale,
                                  kv_indptr, seq_lens, num_splits: int, workspace, out,
                                  stream=None) -> None:
     """paged_decode_attn_q8 on the workspace's plan (a step's later layers)."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_q8_planned", lib().paged_decode_attn_q8_planned(
-        ctypes.byref(d), _bf16_ptr(q, rows), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
+        d, _bf16_ptr(q, rows), *_q8_ptrs(d, k_codes, v_codes, k_scale, v_scale),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace),
         ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
 
@@ -649,7 +647,7 @@ def paged_kv_append_q4(d: Dims, t: Tokens, k_codes, v_codes, k_scale, v_scale, k
     [num_pages, page_size, Hkv, D / 32] (uint8 or torch.float8_e8m0fnu)."""
     _token_count(d, t, per_row=True)
     _check("paged_kv_append_q4", lib().paged_kv_append_q4(
-        ctypes.byref(d), ctypes.byref(t),
+        d, t,
         *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
@@ -658,7 +656,7 @@ def paged_kv_extend_q4(d: Dims, t: Tokens, qo_indptr, k_codes, v_codes, k_scale,
                        kv_indices, kv_indptr, seq_lens, status=None, stream=None) -> None:
     """paged_kv_append_q4 for ragged chunks of new tokens."""
     _check("paged_kv_extend_q4", lib().paged_kv_extend_q4(
-        ctypes.byref(d), ctypes.byref(t), _ptr(qo_indptr), _token_count(d, t),
+        d, t, _ptr(qo_indptr), _token_count(d, t),
         *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), _ptr(status), _stream(stream)))
 
@@ -670,7 +668,7 @@ def paged_kv_read_q4(d: Dims, k_codes, v_codes, k_scale, v_scale, kv_indices, kv
     seq_lens without the tokens before it, and its sinks' pages by a second call."""
     n = d.num_indices * d.page_size * d.Hkv * d.D
     _check("paged_kv_read_q4", lib().paged_kv_read_q4(
-        ctypes.byref(d), *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)),
+        d, *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), _bf16_ptr(k_out, n),
         _bf16_ptr(v_out, n), _ptr(status), _stream(stream)))
 
@@ -680,10 +678,10 @@ def paged_decode_attn_q4(d: Dims, q, k_codes, v_codes, k_scale, v_scale, kv_indi
                          sinks: int = 0, stream=None) -> None:
     """paged_decode_attn over a 4-bit cache; with a window, over each row's last
     `window` tokens and its first `sinks`."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_q4", lib().paged_decode_attn_q4(
-        ctypes.byref(d), _bf16_ptr(q, rows),
+        d, _bf16_ptr(q, rows),
         *_q4_ptrs(k_codes, v_codes, k_scale, v_scale, _slot_values(d)),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits,
         _ptr(workspace), ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
@@ -695,11 +693,11 @@ def paged_decode_attn_window(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, 
                              stream=None) -> None:
     """paged_decode_attn in which a row's query sees the last `window` of its
     seq_lens[b] tokens and the first `sinks` (window 0: all)."""
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     n = _slot_values(d)
     rows = d.B * d.Hq * d.D
     _check("paged_decode_attn_window", lib().paged_decode_attn_window(
-        ctypes.byref(d), _bf16_ptr(q, rows), _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n),
+        d, _bf16_ptr(q, rows), _bf16_ptr(k_pool, n), _bf16_ptr(v_pool, n),
         _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks, num_splits,
         _ptr(workspace), ws_bytes, _bf16_ptr(out, rows), _stream(stream)))
 
@@ -710,10 +708,10 @@ def paged_prefill_attn_window(d: Dims, q, qo_indptr, k_pool, v_pool, kv_indices,
     """paged_prefill_attn in which a query sees the last `window` keys up to its own
     and the row's first `sinks` (window 0: all up to its own)."""
     total_q = int(q.shape[0])
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = 0 if workspace is None else workspace.nbytes
     n, rows = _slot_values(d), total_q * d.Hq * d.D
     _check("paged_prefill_attn_window", lib().paged_prefill_attn_window(
-        ctypes.byref(d), _bf16_ptr(q, rows), _ptr(qo_indptr), total_q,
+        d, _bf16_ptr(q, rows), _ptr(qo_indptr), total_q,
         total_q if max_q_len is None else int(max_q_len), _bf16_ptr(k_pool, n),
         _bf16_ptr(v_pool, n), _ptr(kv_indices), _ptr(kv_indptr), _ptr(seq_lens), window, sinks,
         _ptr(workspace), ws_bytes, _bf16_ptr(out, rows), _ptr(status), _stream(stream)))
@@ -728,23 +726,23 @@ def paged_decode_attn_noalloc(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr,
     the library's own 16 MiB device array, shared by every call (calls that
     overlap on the GPU race)."""
     _check("paged_decode_attn_noalloc", lib().paged_decode_attn_noalloc(
-        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
+        d, _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(out), _ptr(status),
         _stream(stream)))
 
 
 def paged_decode_partials(d: Dims, q, k_pool, v_pool, kv_indices, kv_indptr, seq_lens,
                           num_splits: int, workspace, stream=None) -> None:
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.nbytes
     _check("paged_decode_partials", lib().paged_decode_partials(
-        ctypes.byref(d), _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
+        d, _ptr(q), _pool_ptr(d, k_pool), _pool_ptr(d, v_pool), _ptr(kv_indices),
         _ptr(kv_indptr), _ptr(seq_lens), num_splits, _ptr(workspace), ws_bytes,
         _stream(stream)))
 
 
 def decode_combine(d: Dims, o_part, ml_part, num_splits: int, out, stream=None) -> None:
     _check("decode_combine", lib().decode_combine(
-        ctypes.byref(d), _ptr(o_part), _ptr(ml_part), num_splits, _ptr(out), _stream(stream)))
+        d, _ptr(o_part), _ptr(ml_part), num_splits, _ptr(out), _stream(stream)))
 
 
 # ---- conveniences over a caller-owned workspace tensor ----------------------
