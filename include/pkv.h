@@ -627,8 +627,9 @@ pkv_status paged_decode_attn_q8_planned(const pkv_dims *dims, const void *q, con
  *   scale = 127 + clamp(ceil(log2(amax / 6)), -40, 40),
  *   code  = x * 2^(127 - scale) rounded to the nearest e2m1 (ties to the even
  *           code, saturating at 6),
- * of the exact value x of the formulas above (its last bits count next to a
- * border; the norm's sum overflows and underflows as in fp32), V: the bf16 value.
+ * of the value x of the formulas above (its last bits count next to a border: the
+ * codes are the exact value's unless a border is within about 2^-44 of its pair's
+ * magnitudes; the norm's sum overflows and underflows as in fp32), V: the bf16 value.
  * Where one of the 32 is infinite or NaN, all have scale 255, which stands for
  * NaN; magnitudes above 6 * 2^40 saturate.  The same pages, tables and lengths as
  * the bf16 calls. */

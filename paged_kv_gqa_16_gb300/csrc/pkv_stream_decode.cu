@@ -34,15 +34,15 @@
 // What bounds it.  The windows over bf16 pools: memory.  The 4-bit cache: instructions.
 // A warp makes 350 for 16 tokens of a head of 128, of which 160 go to the
 // arithmetic-logic pipe at two cycles each (64 conversions, 16 to gather two tokens'
-// codes, 16 for scales, 8 to round weights); issue slots are 60% busy, that pipe 54%,
-// the tensor cores 21%.  On the serving batch the copies alone take 35.6 us, the
+// codes, 16 for scales, 8 to round weights); of the kernel's time issue slots are busy
+// 53%, that pipe 53%, the tensor cores 21%.  On the serving batch the copies alone take 35.6 us, the
 // arithmetic alone 44, neither 18.
 //
 // Measured (CUDA-graph replay, K and V larger than L2 or rotating): 4 bits, 128 rows,
-// lognormal, 154,103 tokens, 64 over 8 heads of 128, 168 MB: 47.1 us, 3,560 GB/s, 53% of
+// lognormal, 154,103 tokens, 64 over 8 heads of 128, 168 MB: 47.7 us, 3,520 GB/s, 53% of
 // the copy bandwidth (the 8-bit cache's 322 MB: 57.7, bf16's 631 MB: 97); one row of
-// 32,768, 32 heads: 17.0 us; 32 rows through a window of 1,024 and 4 sinks: 16.9; 8 rows of
-// 513 to 1,025, heads of 64: 8.5.  bf16, 128 rows of at most 1,028 seen tokens, 312 MB:
+// 32,768, 32 heads: 17.0 us; 32 rows through a window of 1,024 and 4 sinks: 17.0; 8 rows of
+// 513 to 1,025, heads of 64: 8.6.  bf16, 128 rows of at most 1,028 seen tokens, 312 MB:
 // 55.9 us, 5,580 GB/s, 84%; 64 rows of 4,100 seen tokens, 1,076 MB: 158.6 us, 6,785 GB/s.
 #include <cmath>
 #include <type_traits>
@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(StreamCfg<BITS, D, HPC, NT>::kThreads, 1)
                 (void)mbar_wait_bounded(&full[k % NST * C::kFulls + f], (uint32_t)((k / NST) & 1));
         } else {
             // A stage's barrier is kSplit warps', which filled the same stages unless
-            // somebody gave up.
+            // somebody gave up.  (A barrier for each would be complete whatever the others
+            // did, but costs the consumers more waits: 49.4 us in place of 47.7 on the
+            // serving batch, 48.2 with a lane a barrier.)
             cp_async_wait_all();
             for (int k = it - C::kTurn, n = 0; k >= 0 && n < NST && !*abort;
                  k -= C::kTurn, n += C::kTurn)

@@ -14,6 +14,9 @@
 //             a key next to a border is decided as the exact value is: where 32
 //             bits do not tell (their error against the distance, one warp's
 //             round in some hundreds) the warp forms its vectors again in 46.
+//             (The bound of the error holds for any table: a pair's (c, -s; s, c)
+//             is a rotation times sqrt(c^2 + s^2), so |a c| and |b s| are at most
+//             the turned pair's length.)
 //
 // The pass reads and writes every value once and is bound by memory, if the
 // arithmetic is kept small: a head vector belongs to a group of D / 8 lanes with
